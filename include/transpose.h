@@ -85,10 +85,13 @@ typedef enum tr_status {
     TR_ERR_TIMEOUT = 7       /* a bounded in-kernel wait ran out (tr_device_status)    */
 } tr_status;
 
-/* Element width of a transpose. */
+/* Element type.  The transposes take the first two (by their width); the
+ * 8-bit types are those of the quantizer and of the product. */
 typedef enum tr_dtype {
     TR_DTYPE_F32 = 0,        /* 4-byte elements (fp32 bit patterns)  */
-    TR_DTYPE_BF16 = 1        /* 2-byte elements (bf16 bit patterns)  */
+    TR_DTYPE_BF16 = 1,       /* 2-byte elements (bf16 bit patterns)  */
+    TR_DTYPE_E4M3 = 2,       /* 8-bit floating point, 4 bits of exponent, largest value 448, no infinity */
+    TR_DTYPE_E5M2 = 3        /* 8-bit floating point, 5 bits of exponent, largest finite value 57344     */
 } tr_dtype;
 
 /* Kernel variants.  All give bit-identical results; they differ in how the
@@ -254,6 +257,144 @@ tr_status tr_operand_tiles_f32(const float *a, float *out, int64_t m, int64_t k,
  * Time it with events on `stream` to compare layouts. */
 tr_status tr_bank_probe(int32_t layout, int32_t reps, int32_t blocks, uint32_t *result,
                         tr_stream_t stream);
+
+/* ---- A linear layer in 8-bit floating point -----------------------------------
+ *
+ * The three products of a linear layer, y = x w^T, dx = dy w and dw = dy^T x,
+ * contract over three different axes.  An operand in 8 bits carries a scale
+ * for each block of 128 values along the axis that is contracted, so it is
+ * needed row by row for one product and transposed for another: the
+ * quantizer writes both from one read.  Layer norm is what stands before the
+ * product.  All sizes and pitches are in elements; pointers are device
+ * pointers, each on a boundary of its element size (else TR_ERR_UNSUPPORTED);
+ * outputs overlap neither an input nor one another (TR_ERR_OVERLAP); zero
+ * sizes, errors, streams, programmatic launch and graph capture are as at the
+ * top. */
+
+/* Arguments of tr_quantize_fp8.  Zero-initialise. */
+typedef struct tr_quantize_args {
+    const void *x;          /* rows x cols values, row pitch ld_x >= cols                       */
+    void *q;                /* rows x cols bytes, row pitch ld_q >= cols                        */
+    float *scale;           /* ceil(cols/128) x ceil(rows/block_rows), row pitch ld_scale       */
+    void *qt;               /* cols x rows bytes, row pitch ld_qt >= rows; NULL: not wanted     */
+    float *scale_t;         /* ceil(rows/128) x ceil(cols/block_rows), row pitch ld_scale_t     */
+    int32_t x_dtype;        /* TR_DTYPE_F32 or TR_DTYPE_BF16                                    */
+    int32_t q_dtype;        /* TR_DTYPE_E4M3 or TR_DTYPE_E5M2                                   */
+    int32_t block_rows;     /* 1 or 128                                                         */
+    int32_t reserved;       /* must be zero                                                     */
+    int64_t rows, cols;
+    int64_t ld_x, ld_q, ld_scale, ld_qt, ld_scale_t;
+    tr_stream_t stream;
+} tr_quantize_args;
+
+/* Quantizes a matrix to 8-bit floating point with a scale for each block of
+ * block_rows x 128 values (128 along a row), and where qt is given its
+ * transpose as well, with blocks along the columns of x, from one read of x.
+ * For a block with largest magnitude m, with T the type's largest finite
+ * value and all of it in 32-bit arithmetic:
+ *
+ *     a = max(m, 2^-100),  scale = a / T,  q = round(x * (T / a))
+ *
+ * rounded to nearest, ties to even, at most T in magnitude: q * scale stands
+ * for x.  The floor keeps a / T and T / a normal numbers; a block of zeros
+ * gives zeros.  A NaN or an infinity in a block makes its scale the same, so
+ * that no product hides it.  scale[cb * ld_scale + rb] is the scale of row block
+ * rb (rows rb * block_rows ..) and column block cb; scale_t is the same for
+ * the transpose.  Blocks at the edges hold what there is.  q and qt are laid
+ * out as the product reads them: 16-byte aligned, pitches multiples of 16
+ * (else TR_ERR_UNSUPPORTED); bytes between rows are not written. */
+tr_status tr_quantize_fp8(const tr_quantize_args *args);
+
+/* Arguments of tr_matmul_fp8.  Zero-initialise. */
+typedef struct tr_matmul_fp8_args {
+    const void *a;          /* m x k bytes, row pitch lda >= k                                   */
+    const float *scale_a;   /* ceil(k/128) x ceil(m/a_block_rows), row pitch ld_scale_a          */
+    const void *b;          /* n x k bytes, row pitch ldb >= k                                   */
+    const float *scale_b;   /* ceil(k/128) x ceil(n/b_block_rows), row pitch ld_scale_b          */
+    void *out;              /* m x n values, row pitch ld_out >= n                               */
+    int32_t a_dtype, b_dtype;           /* TR_DTYPE_E4M3 or TR_DTYPE_E5M2, each its own          */
+    int32_t out_dtype;                  /* TR_DTYPE_F32 or TR_DTYPE_BF16                         */
+    int32_t a_block_rows, b_block_rows; /* 1 or 128, each its own                                */
+    int32_t accumulate;                 /* 0: out = product, 1: out += product                   */
+    int64_t m, n, k;
+    int64_t lda, ldb, ld_out, ld_scale_a, ld_scale_b;
+    tr_stream_t stream;
+} tr_matmul_fp8_args;
+
+/* Matrix product of two operands as tr_quantize_fp8 leaves them, both with the
+ * contraction along their rows:
+ *
+ *     out[i][j] = sum over blocks c of 128 of
+ *                 scale_a[c][i / a_block_rows] * scale_b[c][j / b_block_rows] *
+ *                 sum over l in block c of a[i][l] * b[j][l]
+ *
+ * Products and sums are held in 32 bits on the tensor cores within a block,
+ * in 32-bit registers across blocks, and rounded once to the output's type;
+ * with `accumulate` the output's old value is added in 32 bits first.  The
+ * order of the sums depends on the sizes alone, so equal calls give equal
+ * bits.  a and b are 16-byte aligned with pitches that are multiples of 16
+ * (else TR_ERR_UNSUPPORTED); m, n and k are below 2^31.  k = 0 gives zeros
+ * (or leaves out as it is, with `accumulate`). */
+tr_status tr_matmul_fp8(const tr_matmul_fp8_args *args);
+
+/* Arguments of tr_layernorm.  Zero-initialise. */
+typedef struct tr_layernorm_args {
+    const void *x;          /* rows x cols, row pitch ld_x >= cols                               */
+    const void *gamma;      /* cols weights                                                      */
+    const void *beta;       /* cols biases; NULL: none                                           */
+    void *y;                /* rows x cols of x's type, row pitch ld_y >= cols                   */
+    float *mean, *rstd;     /* rows values each, for the backward pass; NULL: not wanted         */
+    int32_t x_dtype;        /* TR_DTYPE_F32 or TR_DTYPE_BF16, of x and y                         */
+    int32_t w_dtype;        /* the same choice, of gamma and beta                                */
+    int64_t rows, cols;
+    int64_t ld_x, ld_y;
+    float eps;              /* >= 0                                                              */
+    int32_t reserved;       /* must be zero                                                      */
+    tr_stream_t stream;
+} tr_layernorm_args;
+
+/* Layer norm over the rows of a matrix: with mean = sum(x) / cols and
+ * rstd = 1 / sqrt(sum((x - mean)^2) / cols + eps),
+ *
+ *     y[i][j] = (x[i][j] - mean[i]) * rstd[i] * gamma[j] + beta[j]
+ *
+ * The deviations are summed about the row's own mean (a large offset costs no
+ * accuracy), in 32 bits; y is rounded once.  A negative, infinite or NaN eps
+ * returns TR_ERR_BAD_DIM. */
+tr_status tr_layernorm(const tr_layernorm_args *args);
+
+/* Arguments of tr_layernorm_backward.  Zero-initialise. */
+typedef struct tr_layernorm_backward_args {
+    const void *dy;         /* rows x cols of x's type, row pitch ld_dy >= cols                  */
+    const void *x;          /* rows x cols, row pitch ld_x >= cols                               */
+    const void *gamma;      /* cols weights                                                      */
+    const float *mean, *rstd; /* rows values each, from tr_layernorm                             */
+    void *dx;               /* rows x cols of x's type, row pitch ld_dx >= cols                  */
+    float *dgamma;          /* cols values                                                       */
+    float *dbeta;           /* cols values; NULL: not wanted                                     */
+    void *workspace;        /* tr_layernorm_backward_workspace bytes, 16-byte aligned            */
+    int64_t workspace_bytes;
+    int32_t x_dtype;        /* TR_DTYPE_F32 or TR_DTYPE_BF16, of dy, x and dx                    */
+    int32_t w_dtype;        /* the same choice, of gamma                                         */
+    int64_t rows, cols;
+    int64_t ld_dy, ld_x, ld_dx;
+    tr_stream_t stream;
+} tr_layernorm_backward_args;
+
+/* Gradients of layer norm.  With u = (x - mean) * rstd and g = dy * gamma,
+ *
+ *     dx = rstd * (g - sum(g)/cols - u * sum(g u)/cols)         along each row
+ *     dgamma[j] = sum over rows of dy u,  dbeta[j] = sum over rows of dy
+ *
+ * The sums down the rows are held in 32 bits and joined in an order that the
+ * sizes alone fix (no atomics), so equal calls give equal bits.  Nothing needs
+ * clearing before the call.  TR_ERR_UNSUPPORTED for a workspace that is too
+ * small or misaligned. */
+tr_status tr_layernorm_backward(const tr_layernorm_backward_args *args);
+
+/* Bytes of workspace that tr_layernorm_backward needs for these sizes on any
+ * device (0 for empty sizes, -1 for negative ones).  Host only. */
+int64_t tr_layernorm_backward_workspace(int64_t rows, int64_t cols);
 
 /* Host-only planning: the variant tr_transpose_ex would run for these
  * arguments and options (a tr_variant value, never AUTO), or a negative

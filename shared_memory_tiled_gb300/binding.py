@@ -9,13 +9,15 @@ default stream), e.g. ``torch.cuda.current_stream().cuda_stream``.
 The library is opened on first use.  If it has not been built, or cannot be
 loaded, every call raises ``LibraryMissing``: there is no fallback path.
 
-``transpose`` / ``copy`` are conveniences for torch tensors: they read sizes
-and pitches off the tensors' strides and call the same entry points.
+``transpose`` / ``copy`` and ``quantize_fp8`` / ``matmul_fp8`` / ``layernorm`` /
+``layernorm_backward`` are conveniences for torch tensors: they read sizes and
+pitches off the tensors' strides and call the same entry points.
 """
 from __future__ import annotations
 
 import ctypes
 import enum
+import functools
 import os
 import threading
 
@@ -44,6 +46,8 @@ class Status(enum.IntEnum):
 class DType(enum.IntEnum):
     F32 = 0
     BF16 = 1
+    E4M3 = 2
+    E5M2 = 3
 
 
 class Variant(enum.IntEnum):
@@ -81,6 +85,37 @@ class BoundsReport(ctypes.Structure):
                 ("first_bytes", ctypes.c_int32), ("first_store", ctypes.c_int32)]
 
 
+class QuantizeArgs(ctypes.Structure):
+    _fields_ = [("x", VP), ("q", VP), ("scale", VP), ("qt", VP), ("scale_t", VP),
+                ("x_dtype", ctypes.c_int32), ("q_dtype", ctypes.c_int32),
+                ("block_rows", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("rows", I64), ("cols", I64), ("ld_x", I64), ("ld_q", I64), ("ld_scale", I64),
+                ("ld_qt", I64), ("ld_scale_t", I64), ("stream", VP)]
+
+
+class MatmulFp8Args(ctypes.Structure):
+    _fields_ = [("a", VP), ("scale_a", VP), ("b", VP), ("scale_b", VP), ("out", VP),
+                ("a_dtype", ctypes.c_int32), ("b_dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("a_block_rows", ctypes.c_int32),
+                ("b_block_rows", ctypes.c_int32), ("accumulate", ctypes.c_int32),
+                ("m", I64), ("n", I64), ("k", I64), ("lda", I64), ("ldb", I64), ("ld_out", I64),
+                ("ld_scale_a", I64), ("ld_scale_b", I64), ("stream", VP)]
+
+
+class LayernormArgs(ctypes.Structure):
+    _fields_ = [("x", VP), ("gamma", VP), ("beta", VP), ("y", VP), ("mean", VP), ("rstd", VP),
+                ("x_dtype", ctypes.c_int32), ("w_dtype", ctypes.c_int32), ("rows", I64),
+                ("cols", I64), ("ld_x", I64), ("ld_y", I64), ("eps", ctypes.c_float),
+                ("reserved", ctypes.c_int32), ("stream", VP)]
+
+
+class LayernormBackwardArgs(ctypes.Structure):
+    _fields_ = [("dy", VP), ("x", VP), ("gamma", VP), ("mean", VP), ("rstd", VP), ("dx", VP),
+                ("dgamma", VP), ("dbeta", VP), ("workspace", VP), ("workspace_bytes", I64),
+                ("x_dtype", ctypes.c_int32), ("w_dtype", ctypes.c_int32), ("rows", I64),
+                ("cols", I64), ("ld_dy", I64), ("ld_x", I64), ("ld_dx", I64), ("stream", VP)]
+
+
 class LibraryMissing(RuntimeError):
     pass
 
@@ -107,6 +142,11 @@ SIGNATURES = {
     "tr_bank_probe": ([ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, VP, VP], ctypes.c_int),
     "tr_operand_tiles_f32": ([VP, VP, I64, I64, I64, ctypes.c_int32, ctypes.c_int32,
                               ctypes.c_int32, VP], ctypes.c_int),
+    "tr_quantize_fp8": ([ctypes.POINTER(QuantizeArgs)], ctypes.c_int),
+    "tr_matmul_fp8": ([ctypes.POINTER(MatmulFp8Args)], ctypes.c_int),
+    "tr_layernorm": ([ctypes.POINTER(LayernormArgs)], ctypes.c_int),
+    "tr_layernorm_backward": ([ctypes.POINTER(LayernormBackwardArgs)], ctypes.c_int),
+    "tr_layernorm_backward_workspace": ([I64, I64], I64),
     "tr_device_status": ([], ctypes.c_int),
     "tr_selftest_bounded_wait": ([ctypes.c_int32, I64, VP], ctypes.c_int),
     "tr_debug_bounds": ([ctypes.POINTER(BoundsReport)], ctypes.c_int),
@@ -213,6 +253,26 @@ def tr_operand_tiles_f32(a_ptr, out_ptr, m, k, lda, bm, bk, pad=-1, stream=0) ->
 
 def tr_bank_probe(layout, reps, blocks, result_ptr, stream=0) -> int:
     return _call("tr_bank_probe", layout, reps, blocks, result_ptr, stream)
+
+
+def tr_quantize_fp8(args: QuantizeArgs) -> int:
+    return _call("tr_quantize_fp8", ctypes.byref(args) if args is not None else None)
+
+
+def tr_matmul_fp8(args: MatmulFp8Args) -> int:
+    return _call("tr_matmul_fp8", ctypes.byref(args) if args is not None else None)
+
+
+def tr_layernorm(args: LayernormArgs) -> int:
+    return _call("tr_layernorm", ctypes.byref(args) if args is not None else None)
+
+
+def tr_layernorm_backward(args: LayernormBackwardArgs) -> int:
+    return _call("tr_layernorm_backward", ctypes.byref(args) if args is not None else None)
+
+
+def tr_layernorm_backward_workspace(rows, cols) -> int:
+    return _call("tr_layernorm_backward_workspace", rows, cols)
 
 
 def tr_selftest_bounded_wait(arrive, limit_ns, stream=0) -> int:
@@ -344,3 +404,222 @@ def transpose_(x, stream=None):
     with torch.cuda.device(x.device):
         check(f(x.data_ptr(), b, r, ld, s, stream))
     return x
+
+
+# --- a linear layer in 8-bit floating point: torch conveniences -----------------------
+
+_TORCH_TYPES: dict = {}
+
+
+def _torch_types() -> dict:
+    """{torch dtype: DType} of the linear layer's operators."""
+    if not _TORCH_TYPES:
+        import torch
+        _TORCH_TYPES.update({torch.float32: 0, torch.bfloat16: 1, torch.float8_e4m3fn: 2,
+                             torch.float8_e5m2: 3})
+    return _TORCH_TYPES
+
+
+def _type(t, name, allowed):
+    d = _torch_types().get(t.dtype)
+    if d not in allowed:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
+    return d
+
+
+def _matrix(t, name, device=None):
+    """(rows, cols, pitch) of a CUDA matrix with unit inner stride."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor: the library has no CPU path")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix")
+    r, c = t.shape
+    sr, sc = t.stride()
+    if c > 1 and sc != 1:
+        raise ValueError(f"the innermost dimension of {name} must be contiguous")
+    return r, c, (sr if r > 1 else max(sr, c))
+
+
+def _vector(t, name, n, device):
+    """Checks a contiguous CUDA vector of n values."""
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous vector of {n}")
+
+
+def _run(fn, args, device):
+    """Calls a C entry point with its argument struct on torch's current stream
+    of the device."""
+    import torch
+    args.stream = torch.cuda.current_stream(device).cuda_stream
+    if torch.cuda.current_device() == device.index:
+        check(fn(args))
+    else:
+        with torch.cuda.device(device):  # the library sets kernels up per current device
+            check(fn(args))
+
+
+def _on_stream(f):
+    """``stream=``: the call, and the allocation of what it returns and works in,
+    happens on that cudaStream_t instead of torch's current stream."""
+    @functools.wraps(f)
+    def call(x, *args, stream=None, **kw):
+        if stream is None:
+            return f(x, *args, **kw)
+        import torch
+        if not x.is_cuda:
+            raise ValueError("expected CUDA tensors: the library has no CPU path")
+        s = (torch.cuda.ExternalStream(stream, device=x.device) if stream
+             else torch.cuda.default_stream(x.device))
+        with torch.cuda.stream(s):
+            return f(x, *args, **kw)
+    return call
+
+
+@_on_stream
+def quantize_fp8(x, *, dtype=None, block_rows=1, transposed=False):
+    """Quantize a CUDA matrix (fp32 or bf16) to 8-bit floating point.
+
+    Returns ``(q, scale)``, and with ``transposed`` ``(q, scale, qt, scale_t)``:
+    ``q`` has x's shape and ``dtype`` (torch.float8_e4m3fn, the default, or
+    torch.float8_e5m2), rows padded to 16 bytes; ``scale`` is
+    [ceil(cols/128), ceil(rows/block_rows)] in fp32, one scale for each block of
+    block_rows (1 or 128) x 128 values, and ``q * scale`` stands for x.  ``qt``
+    and ``scale_t`` are the same of x's transpose, from the same read of x.
+    """
+    import torch
+    rows, cols, ld = _matrix(x, "x")
+    if dtype is None:
+        dtype = torch.float8_e4m3fn
+    kind = _torch_types().get(dtype)
+    if kind not in (2, 3):
+        raise TypeError(f"unsupported 8-bit dtype {dtype}")
+    if block_rows not in (1, 128):
+        raise ValueError("block_rows must be 1 or 128")
+    dev = x.device
+
+    def outputs(r, c):
+        pitch = -(-c // 16) * 16
+        return (torch.empty_strided((r, c), (pitch, 1), dtype=dtype, device=dev),
+                torch.empty((-(-c // 128), -(-r // block_rows)), dtype=torch.float32, device=dev))
+
+    q, scale = outputs(rows, cols)
+    args = QuantizeArgs(x=x.data_ptr(), q=q.data_ptr(), scale=scale.data_ptr(),
+                        x_dtype=_type(x, "x", (0, 1)), q_dtype=kind, block_rows=block_rows,
+                        rows=rows, cols=cols, ld_x=ld, ld_q=q.stride(0), ld_scale=scale.shape[1])
+    out = (q, scale)
+    if transposed:
+        qt, scale_t = outputs(cols, rows)
+        args.qt, args.scale_t = qt.data_ptr(), scale_t.data_ptr()
+        args.ld_qt, args.ld_scale_t = qt.stride(0), scale_t.shape[1]
+        out = (q, scale, qt, scale_t)
+    _run(tr_quantize_fp8, args, dev)
+    return out
+
+
+def _block_rows(scale, rows, k, name, device):
+    """Rows to a scale, told by the scales' shape."""
+    kb, rb, ld = _matrix(scale, name, device)
+    if _type(scale, name, (0,)) != 0 or kb != -(-k // 128) or rb not in (rows, -(-rows // 128)):
+        raise ValueError(f"{name} has shape {tuple(scale.shape)}, expected "
+                         f"[{-(-k // 128)}, {rows} or {-(-rows // 128)}]")
+    return (1 if rb == rows else 128), ld
+
+
+@_on_stream
+def matmul_fp8(a, scale_a, b, scale_b, *, out=None, out_dtype=None, accumulate=False):
+    """Product ``a @ b.T`` of two 8-bit operands [m, k] and [n, k] with their scales.
+
+    The operands are as ``quantize_fp8`` returns them (or its transposed pair):
+    scales of shape [ceil(k/128), rows] hold one for each 1 x 128 values, of
+    shape [ceil(k/128), ceil(rows/128)] one for each 128 x 128.  The output is
+    ``out`` (fp32 or bf16, may be a strided view) or a new matrix of
+    ``out_dtype`` (bf16 by default); ``accumulate`` adds to ``out``.
+    """
+    import torch
+    m, k, lda = _matrix(a, "a")
+    dev = a.device
+    n, kb, ldb = _matrix(b, "b", dev)
+    if kb != k:
+        raise ValueError(f"a and b contract over {k} and {kb} values")
+    a_rows, ld_sa = _block_rows(scale_a, m, k, "scale_a", dev)
+    b_rows, ld_sb = _block_rows(scale_b, n, k, "scale_b", dev)
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs an output to add to")
+        out = torch.empty((m, n), dtype=out_dtype or torch.bfloat16, device=dev)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError("out_dtype is not out's dtype")
+    om, on, ld_out = _matrix(out, "out", dev)
+    if (om, on) != (m, n):
+        raise ValueError(f"out has shape {(om, on)}, expected {(m, n)}")
+    args = MatmulFp8Args(a.data_ptr(), scale_a.data_ptr(), b.data_ptr(), scale_b.data_ptr(),
+                         out.data_ptr(), _type(a, "a", (2, 3)), _type(b, "b", (2, 3)),
+                         _type(out, "out", (0, 1)), a_rows, b_rows, int(bool(accumulate)), m, n, k,
+                         lda, ldb, ld_out, ld_sa, ld_sb)
+    _run(tr_matmul_fp8, args, dev)
+    return out
+
+
+@_on_stream
+def layernorm(x, gamma, beta=None, *, eps=1e-5, out=None):
+    """Layer norm over the rows of a CUDA matrix (fp32 or bf16).
+
+    Returns ``(y, mean, rstd)``: y of x's type (``out`` if given), the rows'
+    means and reciprocal deviations in fp32 for ``layernorm_backward``.
+    ``gamma`` and ``beta`` are fp32 or bf16, both the same.
+    """
+    import torch
+    rows, cols, ld = _matrix(x, "x")
+    dev = x.device
+    _vector(gamma, "gamma", cols, dev)
+    if beta is not None:
+        _vector(beta, "beta", cols, dev)
+        if beta.dtype != gamma.dtype:
+            raise TypeError("gamma and beta must have the same dtype")
+    if out is None:
+        out = torch.empty((rows, cols), dtype=x.dtype, device=dev)
+    if _matrix(out, "out", dev)[:2] != (rows, cols) or out.dtype != x.dtype:
+        raise ValueError("out must match x in shape and dtype")
+    stats = torch.empty((2, rows), dtype=torch.float32, device=dev)
+    mean, rstd = stats[0], stats[1]
+    args = LayernormArgs(x.data_ptr(), gamma.data_ptr(), None if beta is None else beta.data_ptr(),
+                         out.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _type(x, "x", (0, 1)),
+                         _type(gamma, "gamma", (0, 1)), rows, cols, ld, _matrix(out, "out")[2], eps)
+    _run(tr_layernorm, args, dev)
+    return out, mean, rstd
+
+
+@_on_stream
+def layernorm_backward(dy, x, gamma, mean, rstd, *, bias=True, out=None):
+    """Gradients of ``layernorm``: ``(dx, dgamma, dbeta)``, dx of x's type (``out``
+    if given), the others in fp32; without ``bias`` dbeta is None."""
+    import torch
+    rows, cols, ld = _matrix(x, "x")
+    dev = x.device
+    r, c, ld_dy = _matrix(dy, "dy", dev)
+    if (r, c) != (rows, cols) or dy.dtype != x.dtype:
+        raise ValueError("dy must match x in shape and dtype")
+    _vector(gamma, "gamma", cols, dev)
+    for t, name in ((mean, "mean"), (rstd, "rstd")):
+        _vector(t, name, rows, dev)
+        _type(t, name, (0,))
+    if out is None:
+        out = torch.empty((rows, cols), dtype=x.dtype, device=dev)
+    r, c, ld_dx = _matrix(out, "out", dev)
+    if (r, c) != (rows, cols) or out.dtype != x.dtype:
+        raise ValueError("out must match x in shape and dtype")
+    dgamma = torch.empty(cols, dtype=torch.float32, device=dev)
+    dbeta = torch.empty(cols, dtype=torch.float32, device=dev) if bias else None
+    size = tr_layernorm_backward_workspace(rows, cols)
+    workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+    args = LayernormBackwardArgs(dy.data_ptr(), x.data_ptr(), gamma.data_ptr(), mean.data_ptr(),
+                                 rstd.data_ptr(), out.data_ptr(), dgamma.data_ptr(),
+                                 dbeta.data_ptr() if bias else None, workspace.data_ptr(), size,
+                                 _type(x, "x", (0, 1)), _type(gamma, "gamma", (0, 1)), rows, cols,
+                                 ld_dy, ld, ld_dx)
+    _run(tr_layernorm_backward, args, dev)
+    return out, dgamma, dbeta

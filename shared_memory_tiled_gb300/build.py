@@ -35,7 +35,9 @@ FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", 
          "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]
 SOURCES = ["api.cu", "copy.cu", "tile_lsu.cu", "tile_vec.cu", "tile_vec_u32.cu",
            "tile_vec_u32_prefetch.cu", "tile_vec_u16.cu", "tile_vec_u16_prefetch.cu",
-           "tile_tma.cu", "inplace.cu", "bank_probe.cu", "operand_tiles.cu", "bounds.cu"]
+           "tile_tma.cu", "inplace.cu", "bank_probe.cu", "operand_tiles.cu", "bounds.cu",
+           "linear_api.cu", "quantize_fp8.cu", "matmul_fp8.cu", "layernorm.cu",
+           "layernorm_backward.cu"]
 
 
 def nvcc() -> str:

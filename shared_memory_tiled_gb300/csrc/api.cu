@@ -11,9 +11,12 @@
 #include <string>
 
 namespace tr {
+
 namespace {
 
 thread_local std::string t_last_error;
+
+}  // namespace
 
 void set_error(const char *what, cudaError_t e) {
     char buf[512];
@@ -25,13 +28,14 @@ void set_error(const char *what, cudaError_t e) {
     t_last_error = buf;
 }
 
-// a*b + c with overflow detection; all inputs non-negative.
 bool mul_add(int64_t a, int64_t b, int64_t c, int64_t *r) {
     __int128 v = (__int128)a * b + c;
     if (v > INT64_MAX) return false;
     *r = int64_t(v);
     return true;
 }
+
+namespace {
 
 // Elements from the first to one past the last logical element of a side.
 bool side_extent(int64_t batch, int64_t lines, int64_t elems, int64_t ld, int64_t stride,
@@ -440,13 +444,14 @@ tr_status tr_selftest_bounded_wait(int32_t arrive, int64_t limit_ns, tr_stream_t
 }
 
 tr_status tr_device_status(void) {
-    unsigned v = 0;
-    const cudaError_t e = tr::read_and_clear_fault(&v);
+    unsigned v = 0, w = 0;
+    cudaError_t e = tr::read_and_clear_fault(&v);
+    if (e == cudaSuccess) e = tr::read_and_clear_fault_matmul(&w);
     if (e != cudaSuccess) {
         tr::set_error("reading the device fault flag failed", e);
         return TR_ERR_CUDA;
     }
-    return v ? TR_ERR_TIMEOUT : TR_OK;
+    return v | w ? TR_ERR_TIMEOUT : TR_OK;
 }
 
 tr_status tr_debug_bounds(tr_bounds_report *report) {

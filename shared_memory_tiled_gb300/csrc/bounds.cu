@@ -18,6 +18,10 @@ cudaError_t read_bounds_inplace(dbg::Record *r);
 cudaError_t read_bounds_copy(dbg::Record *r);
 cudaError_t read_bounds_operand_tiles(dbg::Record *r);
 cudaError_t read_bounds_bank_probe(dbg::Record *r);
+cudaError_t read_bounds_quantize(dbg::Record *r);
+cudaError_t read_bounds_matmul_fp8(dbg::Record *r);
+cudaError_t read_bounds_layernorm(dbg::Record *r);
+cudaError_t read_bounds_layernorm_backward(dbg::Record *r);
 
 namespace {
 
@@ -75,6 +79,8 @@ cudaError_t read_and_clear_bounds(BoundsSummary *sum) {
         read_bounds_vec_u32, read_bounds_vec_u32_prefetch, read_bounds_vec_u16,
         read_bounds_vec_u16_prefetch, read_bounds_lsu, read_bounds_tma, read_bounds_inplace,
         read_bounds_copy, read_bounds_operand_tiles, read_bounds_bank_probe,
+        read_bounds_quantize, read_bounds_matmul_fp8, read_bounds_layernorm,
+        read_bounds_layernorm_backward,
         read_bounds_selftest};
     for (auto read : readers) {
         dbg::Record r{};

@@ -1,0 +1,375 @@
+// Matrix product of 8-bit operands with a scale for each block of 128 along
+// the contraction.
+//
+// One operand, P, supplies the 128 rows of a tensor-core tile and the other,
+// Q, its BN columns: P = a and Q = b, or, for a few rows of a, the other way
+// round (TURN), so that they are the short side.  Per block of the contraction the tensor
+// cores sum P Q^T in tensor memory; since the scales change with every block,
+// four warps then take the sums out, multiply them by the block's scales and
+// add them up in registers, while the next block's product runs into the other
+// half of the tensor memory.
+//
+//   warp 0     TMA: keeps the ring of operand stages full
+//   warp 1     matrix instructions, 4 per stage
+//   warps 2-5  lane = row of P: sums += scale_p * scale_q * block sums
+//
+// Few tiles: the blocks of the contraction are split over a cluster of CTAs and
+// their sums joined through distributed shared memory, in rank order.
+#include <atomic>
+#include <cstring>
+#include <mutex>
+
+#include "bounds.cuh"
+#include "launch.cuh"
+#include "row_chunk.cuh"
+#include "tcgen05.cuh"
+#include "tensor_map.cuh"
+#include "tr_internal.h"
+
+namespace tr {
+
+// Set when a bounded in-kernel wait ran out; read and cleared by the host.
+__device__ unsigned g_fault_flag_matmul = 0;
+
+namespace {
+
+constexpr int kThreads = 192;
+constexpr int kBlockK = 128;             // bytes, values and the scales' block
+constexpr int kTileP = 128;
+constexpr int kBytesP = kTileP * kBlockK;
+
+template <int BN>
+struct Shape {
+    static constexpr int kStageBytes = kBytesP + BN * kBlockK;
+    static constexpr int kStages = BN == 128 ? 3 : BN == 64 ? 4 : 5;
+    static constexpr int kColumns = BN < 16 ? 32 : 2 * BN;  // two buffers of sums
+    static constexpr size_t kSmem = 1024 + size_t(kStages) * kStageBytes;
+};
+
+struct Product {
+    const float *scale_p, *scale_q;
+    void *out;
+    int64_t ld_p, ld_q, ld_out;          // pitches of the scales and of the output
+    int64_t p, q;                        // rows of the two operands
+    int64_t tiles_p, tiles_q;
+    int32_t blocks;                      // blocks of the contraction
+    int32_t split;                       // CTAs that share one tile's contraction
+    int32_t p_block, q_block;            // rows to a scale: 1 or 128
+    int32_t p_e5m2, q_e5m2;
+    int32_t out_bf16, accumulate;
+};
+
+// Rows of P and of Q at which a tile begins; 16 tiles of P go with each tile of Q
+// before the next, so that the operands in use at one time stay in L2.
+__device__ __forceinline__ void tile_at(const Product &g, int64_t tile, int bn, int64_t *p0,
+                                        int64_t *q0) {
+    const int64_t group = tile / (16 * g.tiles_q), at = tile - group * 16 * g.tiles_q;
+    const int64_t left = g.tiles_p - group * 16, tall = left < 16 ? left : 16;
+    *p0 = (group * 16 + at % tall) * kTileP;
+    *q0 = at / tall * bn;
+}
+
+// out[i][j] = v, or += v; `s` is the output's logical extent.
+__device__ __forceinline__ void put(const Product &g, int64_t i, int64_t j, float v,
+                                    const dbg::Side &s) {
+    if (g.out_bf16) {
+        __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(g.out) + i * g.ld_out + j;
+        if (!TR_STORE_OK(s, o, 2)) return;
+        if (g.accumulate) v += __bfloat162float(*o);
+        *o = __float2bfloat16_rn(v);
+    } else {
+        float *o = static_cast<float *>(g.out) + i * g.ld_out + j;
+        if (!TR_STORE_OK(s, o, 4)) return;
+        if (g.accumulate) v += *o;
+        *o = v;
+    }
+}
+
+template <int BN, bool TURN>
+__global__ void __launch_bounds__(kThreads, 2)
+k_matmul_fp8(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
+             const __grid_constant__ Product g) {
+    using S = Shape<BN>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t full[S::kStages], empty[S::kStages], sums_full[2], sums_empty[2], drained;
+    __shared__ uint32_t tmem_base;
+    __shared__ alignas(16) float scales[2][BN];
+    uint8_t *stages = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+
+    if (t == 0) {
+        ptx::prefetch_tensormap(&map_p);
+        ptx::prefetch_tensormap(&map_q);
+        for (int i = 0; i < S::kStages; ++i) {
+            ptx::mbar_init(full + i, 1);
+            ptx::mbar_init(empty + i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(sums_full + i, 1);
+            ptx::mbar_init(sums_empty + i, 4);
+        }
+        ptx::mbar_init(&drained, 1);
+        ptx::fence_barrier_init();
+    }
+    if (warp == 1) ptx::tmem_alloc(&tmem_base, S::kColumns);
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = tmem_base;
+    // The dependents may start once every block has its tensor memory: one that
+    // waited for columns held by a dependent would wait for ever.
+    pdl_prologue();
+
+    const int64_t tile = blockIdx.x / unsigned(g.split);
+    const int rank = int(blockIdx.x % unsigned(g.split));
+    int64_t p0, q0;
+    tile_at(g, tile, BN, &p0, &q0);
+    const int first = int(int64_t(g.blocks) * rank / g.split);
+    const int count = int(int64_t(g.blocks) * (rank + 1) / g.split) - first;
+    bool ok = true;
+
+    float acc[BN];
+#pragma unroll
+    for (int c = 0; c < BN; ++c) acc[c] = 0.0f;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int i = 0;
+            for (; i < count; ++i) {
+                const int s = i % S::kStages;
+                if (i >= S::kStages && !ptx::mbar_wait_bounded(empty + s, ((i / S::kStages) - 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                uint8_t *dst = stages + s * S::kStageBytes;
+                ptx::mbar_arrive_expect_tx(full + s, S::kStageBytes);
+                ptx::tma_load_2d(dst, &map_p, full + s, (first + i) * kBlockK, int32_t(p0));
+                ptx::tma_load_2d(dst + kBytesP, &map_q, full + s, (first + i) * kBlockK, int32_t(q0));
+            }
+            if (!ok)  // no load may land after the block has gone
+                for (int k = i > S::kStages ? i - S::kStages : 0; k < i; ++k)
+                    ptx::mbar_wait_bounded(full + k % S::kStages, (k / S::kStages) & 1);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t idesc = ptx::f8_idesc(g.p_e5m2, g.q_e5m2, BN);
+            for (int i = 0; i < count; ++i) {
+                const int s = i % S::kStages, b = i & 1;
+                ok = ptx::mbar_wait_bounded(full + s, (i / S::kStages) & 1) &&
+                     (i < 2 || ptx::mbar_wait_bounded(sums_empty + b, ((i >> 1) - 1) & 1));
+                if (!ok) break;
+                ptx::tc_fence_after();
+                const uint32_t at = ptx::smem_addr(stages + s * S::kStageBytes);
+                const uint64_t dp = ptx::operand_desc(at), dq = ptx::operand_desc(at + kBytesP);
+#pragma unroll
+                for (int k = 0; k < kBlockK / 32; ++k)
+                    ptx::mma_f8(tmem + b * BN, dp + 2 * k, dq + 2 * k, idesc, k > 0);
+                ptx::mma_commit(empty + s);
+                ptx::mma_commit(sums_full + b);
+            }
+            if (!ok) {
+                ptx::mma_commit(&drained);
+                ptx::mbar_wait_bounded(&drained, 0);
+            }
+        }
+    } else {
+        const int w = warp & 3;                       // the quarter of the lanes this warp may read
+        const int row = w * 32 + lane, th = t - 64;   // row of P; index among the 128 threads
+        const bool has_p = p0 + row < g.p, has_q = th < BN && q0 + th < g.q;
+        const float *sp = g.scale_p + (g.p_block == 1 ? p0 + row : (p0 + row) >> 7);
+        const float *sq = g.scale_q + (g.q_block == 1 ? q0 + th : (q0 + th) >> 7);
+        [[maybe_unused]] const dbg::Side side_p = dbg::side(g.scale_p, 1, g.blocks, g.p_block == 1 ? g.p : (g.p + 127) / 128, g.ld_p, 0, 4);
+        [[maybe_unused]] const dbg::Side side_q = dbg::side(g.scale_q, 1, g.blocks, g.q_block == 1 ? g.q : (g.q + 127) / 128, g.ld_q, 0, 4);
+        auto scale = [](const float *p, bool has, [[maybe_unused]] const dbg::Side &s) {
+            return has && TR_LOAD_OK(s, p, 4) ? *p : 0.0f;
+        };
+        float next_p = scale(sp + first * g.ld_p, has_p && count > 0, side_p);
+        float next_q = scale(sq + first * g.ld_q, has_q && count > 0, side_q);
+        for (int i = 0; i < count; ++i) {
+            const int b = i & 1;
+            const float mine = next_p;
+            if (th < BN) scales[b][th] = next_q;
+            if (i + 1 < count) {
+                next_p = scale(sp + (first + i + 1) * g.ld_p, has_p, side_p);
+                next_q = scale(sq + (first + i + 1) * g.ld_q, has_q, side_q);
+            }
+            ptx::named_sync(1, 128);
+            // A wait that ran out is not repeated, but the meetings go on.
+            if (ok) ok = ptx::mbar_wait_bounded(sums_full + b, (i >> 1) & 1);
+            ptx::tc_fence_after();
+            __syncwarp();
+#pragma unroll
+            for (int c = 0; c < BN; c += 16) {
+                float v[16];
+                ptx::tmem_load16(v, tmem + (uint32_t(w * 32) << 16) + b * BN + c);
+                ptx::tmem_wait_load();
+#pragma unroll
+                for (int k = 0; k < 16; k += 4) {
+                    const float4 f = *reinterpret_cast<const float4 *>(&scales[b][c + k]);
+                    acc[c + k] = fmaf(v[k], mine * f.x, acc[c + k]);
+                    acc[c + k + 1] = fmaf(v[k + 1], mine * f.y, acc[c + k + 1]);
+                    acc[c + k + 2] = fmaf(v[k + 2], mine * f.z, acc[c + k + 2]);
+                    acc[c + k + 3] = fmaf(v[k + 3], mine * f.w, acc[c + k + 3]);
+                }
+            }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(sums_empty + b);
+        }
+        // The sums go through shared memory (the stages are free: every product is
+        // complete) so that lanes write neighbouring words of the output.
+        float *red = reinterpret_cast<float *>(stages);
+#pragma unroll
+        for (int c = 0; c < BN; ++c)
+            red[TURN ? c * 128 + row : row * (BN + 1) + c] = acc[c];
+    }
+    if (!ok) atomicExch(&g_fault_flag_matmul, 1u);
+    __syncwarp();
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (g.split > 1) ptx::cluster_sync();
+    if (warp >= 2) {
+        float *red = reinterpret_cast<float *>(stages);
+        const int th = t - 64;
+        [[maybe_unused]] const dbg::Side so = dbg::side(g.out, 1, TURN ? g.q : g.p, TURN ? g.p : g.q, g.ld_out, 0, g.out_bf16 ? 2 : 4);
+        auto total = [&](const float *p) {
+            if (g.split == 1) return *p;
+            float v = 0.0f;
+            for (int r = 0; r < g.split; ++r) v += ptx::load_peer(p, uint32_t(r));
+            return v;
+        };
+        if constexpr (TURN) {
+            if (p0 + th < g.p)
+                for (int c = rank; c < BN && q0 + c < g.q; c += g.split)
+                    put(g, q0 + c, p0 + th, total(red + c * 128 + th), so);
+        } else {
+            for (int r = rank * 4 + (th >> 5); r < 128 && p0 + r < g.p; r += g.split * 4)
+                for (int c = lane; c < BN && q0 + c < g.q; c += 32)
+                    put(g, p0 + r, q0 + c, total(red + r * (BN + 1) + c), so);
+        }
+    }
+    if (g.split > 1) ptx::cluster_sync();  // no block leaves while another reads its sums
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_free(tmem, S::kColumns);
+    }
+}
+
+bool encode_operand(CUtensorMap *map, const void *base, int64_t k, int64_t rows, int64_t ld,
+                    int box_rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {cuuint64_t(k), cuuint64_t(rows)};
+    const cuuint64_t strides[1] = {cuuint64_t(ld)};
+    const cuuint32_t box[2] = {kBlockK, cuuint32_t(box_rows)};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box,
+              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int BN, bool TURN>
+cudaError_t launch_shape(const CUtensorMap &map_p, const CUtensorMap &map_q, const Product &g,
+                         cudaStream_t stream) {
+    auto kern = k_matmul_fp8<BN, TURN>;
+    constexpr size_t smem = Shape<BN>::kSmem;
+    static std::atomic<bool> opted[64];  // per device, zero-initialised (static)
+    static std::mutex mu;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!opted[dev].load(std::memory_order_acquire)) {
+        std::lock_guard<std::mutex> lock(mu);
+        if (!opted[dev].load(std::memory_order_relaxed)) {
+            e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+            if (e != cudaSuccess) return e;
+            opted[dev].store(true, std::memory_order_release);
+        }
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(g.tiles_p * g.tiles_q * g.split));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = unsigned(g.split);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, kern, map_p, map_q, g);
+    if (e != cudaSuccess) (void)cudaGetLastError();
+    return e;
+}
+
+}  // namespace
+
+// Debug builds: this unit's record of refused accesses.
+TR_BOUNDS_READER(read_bounds_matmul_fp8)
+
+cudaError_t read_and_clear_fault_matmul(unsigned *value) {
+    cudaError_t e = cudaDeviceSynchronize();
+    if (e != cudaSuccess) return e;
+    e = cudaMemcpyFromSymbol(value, g_fault_flag_matmul, sizeof(unsigned));
+    if (e != cudaSuccess) return e;
+    const unsigned zero = 0;
+    return cudaMemcpyToSymbol(g_fault_flag_matmul, &zero, sizeof(unsigned));
+}
+
+cudaError_t launch_matmul_fp8(const tr_matmul_fp8_args &a, const char **why) {
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(a.stream);
+    const bool out_bf16 = a.out_dtype == TR_DTYPE_BF16;
+    if (a.k == 0) {
+        if (a.accumulate) return cudaSuccess;
+        const size_t es = out_bf16 ? 2 : 4;
+        return cudaMemset2DAsync(a.out, size_t(a.ld_out) * es, 0, size_t(a.n) * es, size_t(a.m), stream);
+    }
+    // Up to 64 rows of a: they are the columns of the tile, and b its 128 rows.
+    const bool turn = a.m <= 64;
+    const int bn = !turn ? 128 : a.m <= 16 ? 16 : a.m <= 32 ? 32 : 64;
+    Product g{};
+    g.scale_p = turn ? a.scale_b : a.scale_a;
+    g.scale_q = turn ? a.scale_a : a.scale_b;
+    g.out = a.out;
+    g.ld_p = turn ? a.ld_scale_b : a.ld_scale_a;
+    g.ld_q = turn ? a.ld_scale_a : a.ld_scale_b;
+    g.ld_out = a.ld_out;
+    g.p = turn ? a.n : a.m;
+    g.q = turn ? a.m : a.n;
+    g.tiles_p = (g.p + kTileP - 1) / kTileP;
+    g.tiles_q = (g.q + bn - 1) / bn;
+    g.blocks = int32_t((a.k + kBlockK - 1) / kBlockK);
+    g.p_block = turn ? a.b_block_rows : a.a_block_rows;
+    g.q_block = turn ? a.a_block_rows : a.b_block_rows;
+    g.p_e5m2 = (turn ? a.b_dtype : a.a_dtype) == TR_DTYPE_E5M2;
+    g.q_e5m2 = (turn ? a.a_dtype : a.b_dtype) == TR_DTYPE_E5M2;
+    g.out_bf16 = out_bf16;
+    g.accumulate = a.accumulate;
+    // Split the contraction until the tiles fill two CTAs to each SM, each CTA
+    // keeping four blocks or more.
+    const int64_t tiles = g.tiles_p * g.tiles_q;
+    g.split = 1;
+    while (g.split < 8 && tiles * g.split * 2 <= int64_t(sm_count()) * 2 && g.blocks >= g.split * 8)
+        g.split *= 2;
+    if (tiles * g.split > 0x7fffffffll) {
+        *why = "matmul: too many tiles for one launch";
+        return cudaErrorInvalidValue;
+    }
+    CUtensorMap map_a, map_b;
+    if (!encode_operand(&map_a, a.a, a.k, a.m, a.lda, turn ? bn : kTileP) ||
+        !encode_operand(&map_b, a.b, a.k, a.n, a.ldb, turn ? kTileP : bn)) {
+        *why = "matmul: cuTensorMapEncodeTiled rejected the operands (a pitch of 2^40 bytes or more)";
+        return cudaErrorInvalidValue;
+    }
+    if (!turn) return launch_shape<128, false>(map_a, map_b, g, stream);
+    if (bn == 16) return launch_shape<16, true>(map_b, map_a, g, stream);
+    if (bn == 32) return launch_shape<32, true>(map_b, map_a, g, stream);
+    return launch_shape<64, true>(map_b, map_a, g, stream);
+}
+
+}  // namespace tr

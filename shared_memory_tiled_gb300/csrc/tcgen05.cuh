@@ -1,0 +1,119 @@
+// Thin inline-PTX wrappers for the fifth-generation tensor cores: tensor
+// memory, the 8-bit matrix instruction and its completion, and the 2-D TMA load
+// that feeds it.  Written from the public PTX ISA description of each
+// instruction.
+#pragma once
+
+#include <cstdint>
+
+#include "ptx.cuh"
+
+namespace tr {
+namespace ptx {
+
+// Tensor memory is 128 lanes x 512 columns of 32-bit cells; an address is
+// lane << 16 | column.  One whole warp allocates (a power of two of columns, at
+// least 32; waits while they are taken) and one frees.
+__device__ __forceinline__ void tmem_alloc(uint32_t *smem_dst, uint32_t columns) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_addr(smem_dst)),
+                 "r"(columns)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+}
+
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t columns) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns));
+}
+
+// Order between tensor-core work and what other threads do around a barrier.
+__device__ __forceinline__ void tc_fence_before() {
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_fence_after() {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+
+// D[128][N] (+)= A[128][32] B[N][32]^T on 8-bit operands in shared memory,
+// 32-bit sums in tensor memory.
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(add))
+        : "memory");
+}
+
+// One arrival on `bar` once all matrix instructions this thread has issued are
+// complete (their operands read, their sums written).
+__device__ __forceinline__ void mma_commit(uint64_t *bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+            smem_addr(bar))
+        : "memory");
+}
+
+// 16 columns of this warp's 32 lanes: lane l gets row l.
+__device__ __forceinline__ void tmem_load16(float (&v)[16], uint32_t addr) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(addr));
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ void tmem_wait_load() {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// Descriptor of an operand tile in shared memory: rows of 128 bytes along the
+// contraction in the 128-byte swizzle, groups of 8 rows 1024 bytes apart, as a
+// TMA load with that swizzle leaves it in a 1024-byte aligned buffer.  A step
+// of 32 bytes along the contraction adds 2.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
+    return uint64_t((addr >> 4) & 0x3fffu) | uint64_t(1) << 16 | uint64_t(1024 >> 4) << 32 |
+           uint64_t(1) << 46 | uint64_t(2) << 61;
+}
+
+// Instruction descriptor: fp32 sums, operand types (0 e4m3, 1 e5m2), 128 x N.
+__device__ __forceinline__ uint32_t f8_idesc(uint32_t a_e5m2, uint32_t b_e5m2, uint32_t n) {
+    return 1u << 4 | a_e5m2 << 7 | b_e5m2 << 10 | (n >> 3) << 17 | (128u >> 4) << 24;
+}
+
+__device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, uint64_t *bar,
+                                            int32_t c0, int32_t c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(c0), "r"(c1)
+        : "memory");
+}
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Word at the same shared address in CTA `rank` of the cluster.
+__device__ __forceinline__ float load_peer(const float *p, uint32_t rank) {
+    uint32_t a;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+
+// Meeting point of `threads` threads (whole warps) of the block.
+__device__ __forceinline__ void named_sync(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+}  // namespace ptx
+}  // namespace tr

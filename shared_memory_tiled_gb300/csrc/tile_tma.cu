@@ -50,6 +50,7 @@
 #include "bounds.cuh"
 #include "launch.cuh"
 #include "ptx.cuh"
+#include "tensor_map.cuh"
 #include "tr_internal.h"
 #include "vec_common.cuh"
 
@@ -655,25 +656,6 @@ k_tma_ws(const __grid_constant__ CUtensorMap tm_in, TmaGeom g) {
             }
         }
     }
-}
-
-using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                   const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                   const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-    static EncodeTiledFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q{};
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
-                                             cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-    });
-    return fn;
 }
 
 // 3-D map over [planes][lines][elems] with a 128-byte-wide box of box_lines lines.

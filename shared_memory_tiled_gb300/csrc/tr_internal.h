@@ -68,8 +68,22 @@ cudaError_t launch_inplace(void *data, int esize, int64_t batch, int64_t n, int6
 // otherwise the bounded wait runs out after limit_ns and raises the fault flag.
 cudaError_t launch_wait_selftest(bool arrive, int64_t limit_ns, cudaStream_t stream);
 
-// Device-side fault flag (bounded waits that ran out).  Reads and clears it.
+// Device-side fault flag (bounded waits that ran out).  Reads and clears it;
+// the product keeps one of its own.
 cudaError_t read_and_clear_fault(unsigned *value);
+cudaError_t read_and_clear_fault_matmul(unsigned *value);
+
+// The linear layer's operators; their arguments are checked (linear_api.cu).
+cudaError_t launch_quantize(const tr_quantize_args &a);
+cudaError_t launch_matmul_fp8(const tr_matmul_fp8_args &a, const char **why);
+cudaError_t launch_layernorm(const tr_layernorm_args &a);
+cudaError_t launch_layernorm_backward(const tr_layernorm_backward_args &a);
+
+// Message behind tr_last_error() for this host thread (e: cudaSuccess = none).
+void set_error(const char *what, cudaError_t e);
+
+// a*b + c with overflow detection; all inputs non-negative.
+bool mul_add(int64_t a, int64_t b, int64_t c, int64_t *r);
 
 // Number of SMs of the current device (cached per device).
 int sm_count();
