@@ -407,75 +407,82 @@ def transpose_(x, stream=None):
 
 
 # --- a linear layer in 8-bit floating point: torch conveniences -----------------------
+#
+# Kept short on the host: a call on one token costs the GPU 3-5 us, about what the
+# C entry point costs the host, and each torch lookup here 0.1-2 us on top.
 
-_TORCH_TYPES: dict = {}
+_KINDS: dict = {}  # {torch dtype: DType value}, filled on first use
+_WIDE, _NARROW = (0, 1), (2, 3)
 
 
-def _torch_types() -> dict:
-    """{torch dtype: DType} of the linear layer's operators."""
-    if not _TORCH_TYPES:
+def _kind(dtype, allowed, name):
+    if not _KINDS:
         import torch
-        _TORCH_TYPES.update({torch.float32: 0, torch.bfloat16: 1, torch.float8_e4m3fn: 2,
-                             torch.float8_e5m2: 3})
-    return _TORCH_TYPES
+        _KINDS.update({torch.float32: 0, torch.bfloat16: 1, torch.float8_e4m3fn: 2,
+                       torch.float8_e5m2: 3})
+    k = _KINDS.get(dtype)
+    if k not in allowed:
+        raise TypeError(f"{name}: unsupported dtype {dtype}")
+    return k
 
 
-def _type(t, name, allowed):
-    d = _torch_types().get(t.dtype)
-    if d not in allowed:
-        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
-    return d
-
-
-def _matrix(t, name, device=None):
-    """(rows, cols, pitch) of a CUDA matrix with unit inner stride."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor: the library has no CPU path")
-    if device is not None and t.device != device:
+def _matrix(t, name, device):
+    """(rows, cols, pitch) of a matrix with unit inner stride on a CUDA device."""
+    if t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
     if t.dim() != 2:
         raise ValueError(f"{name} must be a matrix")
     r, c = t.shape
     sr, sc = t.stride()
-    if c > 1 and sc != 1:
+    if sc != 1 and c > 1:
         raise ValueError(f"the innermost dimension of {name} must be contiguous")
-    return r, c, (sr if r > 1 else max(sr, c))
+    return r, c, (sr if r > 1 and c else max(sr, c))
 
 
 def _vector(t, name, n, device):
-    """Checks a contiguous CUDA vector of n values."""
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} must be a CUDA tensor on {device}")
-    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+    """Checks a contiguous vector of n values on a CUDA device."""
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if t.shape != (n,) or (t.stride(0) != 1 and n > 1):
         raise ValueError(f"{name} must be a contiguous vector of {n}")
 
 
-def _run(fn, args, device):
+def _cuda(x):
+    if not x.is_cuda:
+        raise ValueError("expected CUDA tensors: the library has no CPU path")
+    return x.device
+
+
+def _run(name, args, device):
     """Calls a C entry point with its argument struct on torch's current stream
     of the device."""
     import torch
-    args.stream = torch.cuda.current_stream(device).cuda_stream
-    if torch.cuda.current_device() == device.index:
-        check(fn(args))
+    index = device.index
+    # torch.cuda.current_stream(device).cuda_stream, without its 2 us of wrapping
+    args.stream = torch._C._cuda_getCurrentRawStream(index)
+    f = getattr(_lib or load(), name)
+    if torch.cuda.current_device() == index:
+        status = f(ctypes.byref(args))
     else:
         with torch.cuda.device(device):  # the library sets kernels up per current device
-            check(fn(args))
+            status = f(ctypes.byref(args))
+    if status:
+        check(status)
 
 
 def _on_stream(f):
     """``stream=``: the call, and the allocation of what it returns and works in,
     happens on that cudaStream_t instead of torch's current stream."""
     @functools.wraps(f)
-    def call(x, *args, stream=None, **kw):
+    def call(*args, stream=None, **kw):
         if stream is None:
-            return f(x, *args, **kw)
+            return f(*args, **kw)
         import torch
-        if not x.is_cuda:
-            raise ValueError("expected CUDA tensors: the library has no CPU path")
-        s = (torch.cuda.ExternalStream(stream, device=x.device) if stream
-             else torch.cuda.default_stream(x.device))
+        device = _cuda(args[0])
+        s = (torch.cuda.ExternalStream(stream, device=device) if stream
+             else torch.cuda.default_stream(device))
         with torch.cuda.stream(s):
-            return f(x, *args, **kw)
+            return f(*args, **kw)
     return call
 
 
@@ -489,43 +496,40 @@ def quantize_fp8(x, *, dtype=None, block_rows=1, transposed=False):
     [ceil(cols/128), ceil(rows/block_rows)] in fp32, one scale for each block of
     block_rows (1 or 128) x 128 values, and ``q * scale`` stands for x.  ``qt``
     and ``scale_t`` are the same of x's transpose, from the same read of x.
+    ``stream`` (a cudaStream_t): default torch's current stream.
     """
     import torch
-    rows, cols, ld = _matrix(x, "x")
+    dev = _cuda(x)
+    rows, cols, ld = _matrix(x, "x", dev)
     if dtype is None:
         dtype = torch.float8_e4m3fn
-    kind = _torch_types().get(dtype)
-    if kind not in (2, 3):
-        raise TypeError(f"unsupported 8-bit dtype {dtype}")
-    if block_rows not in (1, 128):
+    xk, qk = _kind(x.dtype, _WIDE, "x"), _kind(dtype, _NARROW, "dtype")
+    if block_rows != 1 and block_rows != 128:
         raise ValueError("block_rows must be 1 or 128")
-    dev = x.device
-
-    def outputs(r, c):
-        pitch = -(-c // 16) * 16
-        return (torch.empty_strided((r, c), (pitch, 1), dtype=dtype, device=dev),
-                torch.empty((-(-c // 128), -(-r // block_rows)), dtype=torch.float32, device=dev))
-
-    q, scale = outputs(rows, cols)
-    args = QuantizeArgs(x=x.data_ptr(), q=q.data_ptr(), scale=scale.data_ptr(),
-                        x_dtype=_type(x, "x", (0, 1)), q_dtype=kind, block_rows=block_rows,
-                        rows=rows, cols=cols, ld_x=ld, ld_q=q.stride(0), ld_scale=scale.shape[1])
-    out = (q, scale)
-    if transposed:
-        qt, scale_t = outputs(cols, rows)
-        args.qt, args.scale_t = qt.data_ptr(), scale_t.data_ptr()
-        args.ld_qt, args.ld_scale_t = qt.stride(0), scale_t.shape[1]
-        out = (q, scale, qt, scale_t)
-    _run(tr_quantize_fp8, args, dev)
-    return out
+    cb, rb, ld_q = (cols + 127) // 128, (rows + block_rows - 1) // block_rows, (cols + 15) // 16 * 16
+    q = torch.empty_strided((rows, cols), (ld_q, 1), dtype=dtype, device=dev)
+    scale = torch.empty((cb, rb), dtype=torch.float32, device=dev)
+    if not transposed:
+        _run("tr_quantize_fp8", QuantizeArgs(
+            x.data_ptr(), q.data_ptr(), scale.data_ptr(), None, None, xk, qk, block_rows, 0, rows,
+            cols, ld, ld_q, rb, 0, 0), dev)
+        return q, scale
+    cbt, rbt, ld_t = (rows + 127) // 128, (cols + block_rows - 1) // block_rows, (rows + 15) // 16 * 16
+    qt = torch.empty_strided((cols, rows), (ld_t, 1), dtype=dtype, device=dev)
+    scale_t = torch.empty((cbt, rbt), dtype=torch.float32, device=dev)
+    _run("tr_quantize_fp8", QuantizeArgs(
+        x.data_ptr(), q.data_ptr(), scale.data_ptr(), qt.data_ptr(), scale_t.data_ptr(), xk, qk,
+        block_rows, 0, rows, cols, ld, ld_q, rb, ld_t, rbt), dev)
+    return q, scale, qt, scale_t
 
 
-def _block_rows(scale, rows, k, name, device):
-    """Rows to a scale, told by the scales' shape."""
+def _scales(scale, rows, blocks, name, device):
+    """(rows to a scale, pitch): the former is told by the scales' shape."""
     kb, rb, ld = _matrix(scale, name, device)
-    if _type(scale, name, (0,)) != 0 or kb != -(-k // 128) or rb not in (rows, -(-rows // 128)):
+    if kb != blocks or (rb != rows and rb != (rows + 127) // 128):
         raise ValueError(f"{name} has shape {tuple(scale.shape)}, expected "
-                         f"[{-(-k // 128)}, {rows} or {-(-rows // 128)}]")
+                         f"[{blocks}, {rows} or {(rows + 127) // 128}]")
+    _kind(scale.dtype, (0,), name)
     return (1 if rb == rows else 128), ld
 
 
@@ -538,30 +542,44 @@ def matmul_fp8(a, scale_a, b, scale_b, *, out=None, out_dtype=None, accumulate=F
     shape [ceil(k/128), ceil(rows/128)] one for each 128 x 128.  The output is
     ``out`` (fp32 or bf16, may be a strided view) or a new matrix of
     ``out_dtype`` (bf16 by default); ``accumulate`` adds to ``out``.
+    ``stream`` (a cudaStream_t): default torch's current stream.
     """
     import torch
-    m, k, lda = _matrix(a, "a")
-    dev = a.device
+    dev = _cuda(a)
+    m, k, lda = _matrix(a, "a", dev)
     n, kb, ldb = _matrix(b, "b", dev)
     if kb != k:
         raise ValueError(f"a and b contract over {k} and {kb} values")
-    a_rows, ld_sa = _block_rows(scale_a, m, k, "scale_a", dev)
-    b_rows, ld_sb = _block_rows(scale_b, n, k, "scale_b", dev)
+    blocks = (k + 127) // 128
+    a_rows, ld_sa = _scales(scale_a, m, blocks, "scale_a", dev)
+    b_rows, ld_sb = _scales(scale_b, n, blocks, "scale_b", dev)
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs an output to add to")
         out = torch.empty((m, n), dtype=out_dtype or torch.bfloat16, device=dev)
-    elif out_dtype is not None and out.dtype != out_dtype:
-        raise ValueError("out_dtype is not out's dtype")
-    om, on, ld_out = _matrix(out, "out", dev)
-    if (om, on) != (m, n):
-        raise ValueError(f"out has shape {(om, on)}, expected {(m, n)}")
-    args = MatmulFp8Args(a.data_ptr(), scale_a.data_ptr(), b.data_ptr(), scale_b.data_ptr(),
-                         out.data_ptr(), _type(a, "a", (2, 3)), _type(b, "b", (2, 3)),
-                         _type(out, "out", (0, 1)), a_rows, b_rows, int(bool(accumulate)), m, n, k,
-                         lda, ldb, ld_out, ld_sa, ld_sb)
-    _run(tr_matmul_fp8, args, dev)
+        ld_out = n
+    else:
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError("out_dtype is not out's dtype")
+        om, on, ld_out = _matrix(out, "out", dev)
+        if om != m or on != n:
+            raise ValueError(f"out has shape {(om, on)}, expected {(m, n)}")
+    _run("tr_matmul_fp8", MatmulFp8Args(
+        a.data_ptr(), scale_a.data_ptr(), b.data_ptr(), scale_b.data_ptr(), out.data_ptr(),
+        _kind(a.dtype, _NARROW, "a"), _kind(b.dtype, _NARROW, "b"), _kind(out.dtype, _WIDE, "out"),
+        a_rows, b_rows, 1 if accumulate else 0, m, n, k, lda, ldb, ld_out, ld_sa, ld_sb), dev)
     return out
+
+
+def _like(out, x, rows, cols, dev):
+    """An output of x's shape and type: (tensor, pitch)."""
+    if out is None:
+        import torch
+        return torch.empty((rows, cols), dtype=x.dtype, device=dev), cols
+    r, c, ld = _matrix(out, "out", dev)
+    if r != rows or c != cols or out.dtype != x.dtype:
+        raise ValueError("out must match x in shape and dtype")
+    return out, ld
 
 
 @_on_stream
@@ -570,56 +588,51 @@ def layernorm(x, gamma, beta=None, *, eps=1e-5, out=None):
 
     Returns ``(y, mean, rstd)``: y of x's type (``out`` if given), the rows'
     means and reciprocal deviations in fp32 for ``layernorm_backward``.
-    ``gamma`` and ``beta`` are fp32 or bf16, both the same.
+    ``gamma`` and ``beta`` are fp32 or bf16, both the same.  ``stream`` (a
+    cudaStream_t): default torch's current stream.
     """
     import torch
-    rows, cols, ld = _matrix(x, "x")
-    dev = x.device
+    dev = _cuda(x)
+    rows, cols, ld = _matrix(x, "x", dev)
     _vector(gamma, "gamma", cols, dev)
     if beta is not None:
         _vector(beta, "beta", cols, dev)
         if beta.dtype != gamma.dtype:
             raise TypeError("gamma and beta must have the same dtype")
-    if out is None:
-        out = torch.empty((rows, cols), dtype=x.dtype, device=dev)
-    if _matrix(out, "out", dev)[:2] != (rows, cols) or out.dtype != x.dtype:
-        raise ValueError("out must match x in shape and dtype")
-    stats = torch.empty((2, rows), dtype=torch.float32, device=dev)
-    mean, rstd = stats[0], stats[1]
-    args = LayernormArgs(x.data_ptr(), gamma.data_ptr(), None if beta is None else beta.data_ptr(),
-                         out.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _type(x, "x", (0, 1)),
-                         _type(gamma, "gamma", (0, 1)), rows, cols, ld, _matrix(out, "out")[2], eps)
-    _run(tr_layernorm, args, dev)
+    xk, wk = _kind(x.dtype, _WIDE, "x"), _kind(gamma.dtype, _WIDE, "gamma")
+    out, ld_y = _like(out, x, rows, cols, dev)
+    mean = torch.empty(rows, dtype=torch.float32, device=dev)
+    rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+    _run("tr_layernorm", LayernormArgs(
+        x.data_ptr(), gamma.data_ptr(), None if beta is None else beta.data_ptr(), out.data_ptr(),
+        mean.data_ptr(), rstd.data_ptr(), xk, wk, rows, cols, ld, ld_y, eps, 0), dev)
     return out, mean, rstd
 
 
 @_on_stream
 def layernorm_backward(dy, x, gamma, mean, rstd, *, bias=True, out=None):
     """Gradients of ``layernorm``: ``(dx, dgamma, dbeta)``, dx of x's type (``out``
-    if given), the others in fp32; without ``bias`` dbeta is None."""
+    if given), the others in fp32; without ``bias`` dbeta is None.  ``stream``
+    (a cudaStream_t): default torch's current stream."""
     import torch
-    rows, cols, ld = _matrix(x, "x")
-    dev = x.device
+    dev = _cuda(x)
+    rows, cols, ld = _matrix(x, "x", dev)
     r, c, ld_dy = _matrix(dy, "dy", dev)
-    if (r, c) != (rows, cols) or dy.dtype != x.dtype:
+    if r != rows or c != cols or dy.dtype != x.dtype:
         raise ValueError("dy must match x in shape and dtype")
     _vector(gamma, "gamma", cols, dev)
-    for t, name in ((mean, "mean"), (rstd, "rstd")):
-        _vector(t, name, rows, dev)
-        _type(t, name, (0,))
-    if out is None:
-        out = torch.empty((rows, cols), dtype=x.dtype, device=dev)
-    r, c, ld_dx = _matrix(out, "out", dev)
-    if (r, c) != (rows, cols) or out.dtype != x.dtype:
-        raise ValueError("out must match x in shape and dtype")
+    _vector(mean, "mean", rows, dev)
+    _vector(rstd, "rstd", rows, dev)
+    _kind(mean.dtype, (0,), "mean")
+    _kind(rstd.dtype, (0,), "rstd")
+    xk, wk = _kind(x.dtype, _WIDE, "x"), _kind(gamma.dtype, _WIDE, "gamma")
+    out, ld_dx = _like(out, x, rows, cols, dev)
     dgamma = torch.empty(cols, dtype=torch.float32, device=dev)
     dbeta = torch.empty(cols, dtype=torch.float32, device=dev) if bias else None
     size = tr_layernorm_backward_workspace(rows, cols)
     workspace = torch.empty(size, dtype=torch.uint8, device=dev)
-    args = LayernormBackwardArgs(dy.data_ptr(), x.data_ptr(), gamma.data_ptr(), mean.data_ptr(),
-                                 rstd.data_ptr(), out.data_ptr(), dgamma.data_ptr(),
-                                 dbeta.data_ptr() if bias else None, workspace.data_ptr(), size,
-                                 _type(x, "x", (0, 1)), _type(gamma, "gamma", (0, 1)), rows, cols,
-                                 ld_dy, ld, ld_dx)
-    _run(tr_layernorm_backward, args, dev)
+    _run("tr_layernorm_backward", LayernormBackwardArgs(
+        dy.data_ptr(), x.data_ptr(), gamma.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
+        out.data_ptr(), dgamma.data_ptr(), dbeta.data_ptr() if bias else None,
+        workspace.data_ptr(), size, xk, wk, rows, cols, ld_dy, ld, ld_dx), dev)
     return out, dgamma, dbeta

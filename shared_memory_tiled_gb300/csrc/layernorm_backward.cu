@@ -21,7 +21,8 @@ struct Bwd {
 template <typename T, int V>
 __global__ void __launch_bounds__(512) k_ln_dx(Bwd a) {
     pdl_prologue();
-    __shared__ float slots[2][32];
+    __shared__ float slots[2][64];
+    int turn = 0;
     [[maybe_unused]] const dbg::Side sd = dbg::side(a.dy, 1, a.rows, a.cols, a.ld_dy, 0, sizeof(T));
     [[maybe_unused]] const dbg::Side sx = dbg::side(a.x, 1, a.rows, a.cols, a.ld_x, 0, sizeof(T));
     [[maybe_unused]] const dbg::Side so = dbg::side(a.dx, 1, a.rows, a.cols, a.ld_dx, 0, sizeof(T));
@@ -44,23 +45,29 @@ __global__ void __launch_bounds__(512) k_ln_dx(Bwd a) {
 #pragma unroll
             for (int q = 0; q < V; ++q) {
                 if (lo + q < 0 || lo + q >= a.cols) continue;
-                const float g = to_f32(pd.e[q]) * weight(a.gamma, a.w_bf16, lo + q, sw);
+                const float g = pd.get(q) * weight(a.gamma, a.w_bf16, lo + q, sw);
                 s1 += g;
-                s2 = fmaf(g, (to_f32(px.e[q]) - mean) * rstd, s2);
+                s2 = fmaf(g, (px.get(q) - mean) * rstd, s2);
             }
         }
-        s1 = group_sum<512>(s1, slots[0]) * inv_cols;
-        s2 = group_sum<512>(s2, slots[1]) * inv_cols;
+        float s[2] = {s1, s2};
+        group_sum<512, 2>(s, slots[turn]);
+        turn ^= 1;
+        s1 = s[0] * inv_cols;
+        s2 = s[1] * inv_cols;
         for (int64_t lo = first; lo < a.cols; lo += step) {
             const Pack<T, V> px = load_chunk<T, V>(xr, lo, a.cols, sx);
             Pack<T, V> pd = load_chunk<T, V>(dyr, lo, a.cols, sd);
+            float v[V];
 #pragma unroll
             for (int q = 0; q < V; ++q) {
+                v[q] = 0.0f;
                 if (lo + q < 0 || lo + q >= a.cols) continue;
-                const float g = to_f32(pd.e[q]) * weight(a.gamma, a.w_bf16, lo + q, sw);
-                const float u = (to_f32(px.e[q]) - mean) * rstd;
-                pd.e[q] = from_f32<T>(rstd * (g - s1 - u * s2));
+                const float g = pd.get(q) * weight(a.gamma, a.w_bf16, lo + q, sw);
+                const float u = (px.get(q) - mean) * rstd;
+                v[q] = rstd * (g - s1 - u * s2);
             }
+            pd.round(v);
             store_chunk<T, V>(dxr, lo, a.cols, pd, so);
         }
     }

@@ -84,6 +84,13 @@ __device__ __forceinline__ void cp_async_16(void *smem_dst, const void *gmem_src
                  : "memory");
 }
 
+// The same of 4 bytes.
+__device__ __forceinline__ void cp_async_4(void *smem_dst, const void *gmem_src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(smem_dst)),
+                 "l"(gmem_src)
+                 : "memory");
+}
+
 __device__ __forceinline__ void cp_async_wait_all() {
     asm volatile("cp.async.wait_all;" ::: "memory");
 }

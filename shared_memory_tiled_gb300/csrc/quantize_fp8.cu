@@ -3,8 +3,12 @@
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
+#include <atomic>
+#include <mutex>
+
 #include "bounds.cuh"
 #include "launch.cuh"
+#include "ptx.cuh"
 #include "tr_internal.h"
 
 namespace tr {
@@ -21,8 +25,6 @@ struct Quant {
     int64_t tiles_r, tiles_c;
     float top;  // the 8-bit type's largest finite value
 };
-
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
 // Eight values times r as eight bytes, the first lowest.
 template <bool E5M2>
@@ -46,111 +48,296 @@ __device__ __forceinline__ void store8(uint8_t *row, int64_t c, int64_t cols, ui
         if (TR_STORE_OK(s, row + c + i, 1)) row[c + i] = uint8_t((i < 4 ? v.x >> (8 * i) : v.y >> (8 * (i - 4))));
 }
 
+// How a tile's values reach the registers.
+enum Load {
+    kVector,   // 16-byte loads: base and pitch on 16-byte boundaries
+    kWords,    // fp32 rows off those boundaries: 4-byte copies into a shared tile, coalesced
+    kElements  // bf16 rows off them: one element at a time
+};
+
+constexpr int kWordPitch = 132;  // words to a row of the shared tile: rows stay 16-byte aligned
+constexpr size_t kWordTileBytes = size_t(128) * kWordPitch * 4;
+
+// The 8 x 8 values of one thread.  bf16 stays packed in pairs along the row.
+template <typename T>
+struct Values;
+template <>
+struct Values<__nv_bfloat16> {
+    uint32_t w[8][4];
+    __device__ __forceinline__ float at(int i, int j) const {
+        return __uint_as_float(j & 1 ? w[i][j >> 1] & 0xffff0000u : w[i][j >> 1] << 16);
+    }
+    __device__ __forceinline__ void row(int i, const uint4 *v) {
+        w[i][0] = v[0].x;
+        w[i][1] = v[0].y;
+        w[i][2] = v[0].z;
+        w[i][3] = v[0].w;
+    }
+    __device__ __forceinline__ void set(int i, int j, __nv_bfloat16 v) {
+        const uint32_t b = __bfloat16_as_ushort(v);
+        w[i][j >> 1] = j & 1 ? (w[i][j >> 1] & 0xffffu) | b << 16 : (w[i][j >> 1] & 0xffff0000u) | b;
+    }
+};
+template <>
+struct Values<float> {
+    float v[8][8];
+    __device__ __forceinline__ float at(int i, int j) const { return v[i][j]; }
+    __device__ __forceinline__ void row(int i, const uint4 *r) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            v[i][4 * k] = __uint_as_float(r[k].x);
+            v[i][4 * k + 1] = __uint_as_float(r[k].y);
+            v[i][4 * k + 2] = __uint_as_float(r[k].z);
+            v[i][4 * k + 3] = __uint_as_float(r[k].w);
+        }
+    }
+    __device__ __forceinline__ void set(int i, int j, float x) { v[i][j] = x; }
+};
+
+// Larger of two pairs of magnitudes; a NaN wins.
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 m = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162 *>(&a),
+                                         *reinterpret_cast<const __nv_bfloat162 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&m);
+}
+
+__device__ __forceinline__ uint32_t shfl(uint32_t v, int mask) {
+    return __shfl_xor_sync(0xffffffffu, v, mask);
+}
+
+// Magnitudes of one thread's rows and columns, and the joins over the 16 lanes
+// of a row and the two row groups of a warp.  A magnitude is the bits of its
+// fp32 value (a NaN is larger than every number there too).
+template <typename T>
+struct Magnitudes;
+
+template <>
+struct Magnitudes<__nv_bfloat16> {
+    uint32_t r[4], c[4];  // pairs: rows 2k, 2k+1 and columns 2k, 2k+1
+    __device__ __forceinline__ void of(const Values<__nv_bfloat16> &x) {
+        uint32_t rows[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t a = x.w[i][k] & 0x7fff7fffu;
+                rows[i] = k ? max2(rows[i], a) : a;
+                c[k] = i ? max2(c[k], a) : a;
+            }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            r[k] = max2(__byte_perm(rows[2 * k], rows[2 * k + 1], 0x5410),
+                        __byte_perm(rows[2 * k], rows[2 * k + 1], 0x7632));
+    }
+    __device__ __forceinline__ uint32_t all() const {
+        const uint32_t m = max2(max2(r[0], r[1]), max2(r[2], r[3]));
+        return max(m << 16, m & 0xffff0000u);
+    }
+    // Over the 16 lanes of a row group: lane l ends up with row
+    // 4*(l>>3 & 1) + 2*(l>>2 & 1) + (l & 1).
+    __device__ __forceinline__ uint32_t row(int lane) const {
+        uint32_t a = lane & 8 ? r[2] : r[0], b = lane & 8 ? r[3] : r[1];
+        a = max2(a, shfl(lane & 8 ? r[0] : r[2], 8));
+        b = max2(b, shfl(lane & 8 ? r[1] : r[3], 8));
+        uint32_t m = max2(lane & 4 ? b : a, shfl(lane & 4 ? a : b, 4));
+        m = max2(m, shfl(m, 2));
+        m = max2(m, shfl(m, 1));
+        return lane & 1 ? m & 0xffff0000u : m << 16;
+    }
+    // Over the warp's two row groups, into eight columns' worth of shared words.
+    static constexpr int kBytes = 2;
+    __device__ __forceinline__ void columns(int lane, uint8_t *warp_row) const {
+        uint4 m;
+        m.x = max2(c[0], shfl(c[0], 16));
+        m.y = max2(c[1], shfl(c[1], 16));
+        m.z = max2(c[2], shfl(c[2], 16));
+        m.w = max2(c[3], shfl(c[3], 16));
+        if (lane < 16) *reinterpret_cast<uint4 *>(warp_row + lane * 16) = m;
+    }
+    static __device__ __forceinline__ uint32_t word(const uint8_t *p) {
+        return uint32_t(*reinterpret_cast<const uint16_t *>(p)) << 16;
+    }
+};
+
+template <>
+struct Magnitudes<float> {
+    uint32_t r[8], c[8];
+    __device__ __forceinline__ void of(const Values<float> &x) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const uint32_t a = __float_as_uint(x.v[i][k]) & 0x7fffffffu;
+                r[i] = k ? max(r[i], a) : a;
+                c[k] = i ? max(c[k], a) : a;
+            }
+    }
+    __device__ __forceinline__ uint32_t all() const {
+        uint32_t m = r[0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) m = max(m, r[i]);
+        return m;
+    }
+    __device__ __forceinline__ uint32_t row(int lane) const {
+        uint32_t a[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[i] = max(lane & 8 ? r[i + 4] : r[i], shfl(lane & 8 ? r[i] : r[i + 4], 8));
+        const uint32_t b0 = max(lane & 4 ? a[2] : a[0], shfl(lane & 4 ? a[0] : a[2], 4));
+        const uint32_t b1 = max(lane & 4 ? a[3] : a[1], shfl(lane & 4 ? a[1] : a[3], 4));
+        uint32_t m = max(lane & 1 ? b1 : b0, shfl(lane & 1 ? b0 : b1, 1));
+        return max(m, shfl(m, 2));
+    }
+    static constexpr int kBytes = 4;
+    __device__ __forceinline__ void columns(int lane, uint8_t *warp_row) const {
+        uint32_t m[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) m[k] = max(c[k], shfl(c[k], 16));
+        if (lane < 16) {
+            uint4 *p = reinterpret_cast<uint4 *>(warp_row + lane * 32);
+            p[0] = make_uint4(m[0], m[1], m[2], m[3]);
+            p[1] = make_uint4(m[4], m[5], m[6], m[7]);
+        }
+    }
+    static __device__ __forceinline__ uint32_t word(const uint8_t *p) {
+        return *reinterpret_cast<const uint32_t *>(p);
+    }
+};
+
 // One 128 x 128 tile per turn.  A thread holds the 8 x 8 values of row group rg
-// and column group cg; 16 lanes share a row group, so a row's maximum is a
-// shuffle and a column's goes through shared memory.  Row bytes are stored
-// straight from the registers (16 lanes write 128 contiguous bytes); the
-// transposed ones go through a shared tile of 8-byte slots, slot XOR column
-// group, so that neither its writes nor its reads share a bank.
-template <typename T, bool VEC, bool E5M2, bool BLOCK, bool BOTH>
-__global__ void __launch_bounds__(kThreads) k_quantize(Quant a) {
+// and column group cg; 16 lanes share a row group, so a row's magnitude is a
+// butterfly of shuffles that leaves one row to each lane, and a column's goes
+// through shared memory to one thread per column: each T / a and a / T is
+// divided once.  Row bytes are stored straight from the registers (16 lanes
+// write 128 contiguous bytes); the transposed ones go through a shared tile of
+// 8-byte slots, slot XOR column group, so that neither its writes nor its
+// reads share a bank.
+template <typename T, Load LOAD, bool E5M2, bool BLOCK, bool BOTH>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) k_quantize(const Quant a) {
     pdl_prologue();
-    __shared__ uint32_t col_max[8][128];
+    using M = Magnitudes<T>;
+    extern __shared__ uint4 word_tile[];
+    __shared__ alignas(16) uint8_t col_max[8][128 * M::kBytes];
+    __shared__ alignas(16) float col_inv[128];
     __shared__ uint2 turned[BOTH ? 128 * 16 : 1];
     [[maybe_unused]] const dbg::Side sx = dbg::side(a.x, 1, a.rows, a.cols, a.ld_x, 0, sizeof(T));
     [[maybe_unused]] const dbg::Side sq = dbg::side(a.q, 1, a.rows, a.cols, a.ld_q, 0, 1);
     [[maybe_unused]] const dbg::Side st = dbg::side(a.qt, 1, a.cols, a.rows, a.ld_qt, 0, 1);
     [[maybe_unused]] const dbg::Side ss = dbg::side(a.scale, 1, a.tiles_c, BLOCK ? a.tiles_r : a.rows, a.ld_scale, 0, 4);
     [[maybe_unused]] const dbg::Side su = dbg::side(a.scale_t, 1, a.tiles_r, BLOCK ? a.tiles_c : a.cols, a.ld_scale_t, 0, 4);
-    const int t = threadIdx.x, cg = t & 15, rg = t >> 4, warp = t >> 5;
+    const int t = threadIdx.x, lane = t & 31, cg = t & 15, rg = t >> 4, warp = t >> 5;
     const T *x = static_cast<const T *>(a.x);
     for (int64_t tile = blockIdx.x; tile < a.tiles_r * a.tiles_c; tile += gridDim.x) {
         const int64_t tr = tile / a.tiles_c, tc = tile - tr * a.tiles_c;
         const int64_t r0 = tr * 128 + rg * 8, c0 = tc * 128 + cg * 8;
-        float v[8][8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const T *p = x + (r0 + i) * a.ld_x + c0;
-            if (VEC && r0 + i < a.rows && c0 + 8 <= a.cols && TR_LOAD_OK(sx, p, int(8 * sizeof(T)))) {
-                constexpr int N = int(sizeof(T)) / 2;
-                uint4 raw[N];
-#pragma unroll
-                for (int k = 0; k < N; ++k) raw[k] = __ldcs(reinterpret_cast<const uint4 *>(p) + k);
-                const T *e = reinterpret_cast<const T *>(raw);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[i][j] = float(e[j]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    v[i][j] = r0 + i < a.rows && c0 + j < a.cols && TR_LOAD_OK(sx, p + j, int(sizeof(T)))
-                                  ? float(p[j]) : 0.0f;
+        Values<T> v;
+        if constexpr (LOAD == kWords) {
+            float *words = reinterpret_cast<float *>(word_tile);
+#pragma unroll 8
+            for (int k = 0; k < 64; ++k) {  // a warp copies 16 rows, 32 columns at a time
+                const int r = warp * 16 + (k >> 2), c = (k & 3) * 32 + lane;
+                const int64_t row = tr * 128 + r, col = tc * 128 + c;
+                float *dst = words + r * kWordPitch + c;
+                const T *p = x + row * a.ld_x + col;
+                if (row < a.rows && col < a.cols && TR_LOAD_OK(sx, p, 4)) ptx::cp_async_4(dst, p);
+                else *dst = 0.0f;
             }
-        }
-        uint32_t rm[8], cm[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            rm[i] = kFloorBits;
-            cm[i] = kFloorBits;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const uint32_t b = abs_bits(v[i][j]);
-                rm[i] = max(rm[i], b);
-                cm[j] = max(cm[j], b);
-            }
-        if constexpr (BLOCK) {
-            uint32_t m = kFloorBits;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) m = max(m, rm[i]);
-            m = __reduce_max_sync(0xffffffffu, m);
-            if ((t & 31) == 0) col_max[0][warp] = m;
-            __syncthreads();
-#pragma unroll
-            for (int w = 0; w < 8; ++w) m = max(m, col_max[0][w]);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) rm[i] = cm[i] = m;
-        } else {
+            ptx::cp_async_wait_all();
+            __syncwarp();  // a warp reads back only what it copied: rows 16*warp ..
 #pragma unroll
             for (int i = 0; i < 8; ++i)
+                v.row(i, reinterpret_cast<const uint4 *>(words + (rg * 8 + i) * kWordPitch + cg * 8));
+        } else {
 #pragma unroll
-                for (int o = 8; o; o >>= 1) rm[i] = max(rm[i], __shfl_xor_sync(0xffffffffu, rm[i], o));
-            if constexpr (BOTH) {
+            for (int i = 0; i < 8; ++i) {
+                const T *p = x + (r0 + i) * a.ld_x + c0;
+                uint4 raw[sizeof(T) / 2] = {};
+                if (LOAD == kVector && r0 + i < a.rows && c0 + 8 <= a.cols && TR_LOAD_OK(sx, p, int(8 * sizeof(T)))) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    cm[j] = max(cm[j], __shfl_xor_sync(0xffffffffu, cm[j], 16));
-                    if ((t & 16) == 0) col_max[warp][cg * 8 + j] = cm[j];
+                    for (int k = 0; k < int(sizeof(T)) / 2; ++k) raw[k] = __ldcs(reinterpret_cast<const uint4 *>(p) + k);
+                    v.row(i, raw);
+                } else {
+                    v.row(i, raw);
+                    if (r0 + i < a.rows)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if (c0 + j < a.cols && TR_LOAD_OK(sx, p + j, int(sizeof(T)))) v.set(i, j, p[j]);
                 }
+            }
+        }
+        M m;
+        m.of(v);
+        float inv[8];  // T / a of the rows, then of the columns
+        if constexpr (BLOCK) {
+            uint32_t w = __reduce_max_sync(0xffffffffu, m.all());
+            uint32_t *shared = reinterpret_cast<uint32_t *>(col_inv);
+            if (lane == 0) shared[warp] = w;
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < 8; ++k) w = max(w, shared[k]);
+            const float amax = __uint_as_float(max(w, kFloorBits));
+            const float one = a.top / amax;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) inv[i] = one;
+            if (t == 0) {
+                float *s = a.scale + tc * a.ld_scale + tr;
+                if (TR_STORE_OK(ss, s, 4)) *s = amax / a.top;
+                if (BOTH) {
+                    float *u = a.scale_t + tr * a.ld_scale_t + tc;
+                    if (TR_STORE_OK(su, u, 4)) *u = amax / a.top;
+                }
+            }
+        } else {
+            if constexpr (BOTH) m.columns(lane, col_max[warp]);
+            const float amax = __uint_as_float(max(m.row(lane), kFloorBits));
+            const float mine = a.top / amax;
+            const int64_t row = r0 + (lane >> 3 & 1) * 4 + (lane >> 2 & 1) * 2 + (lane & 1);
+            if ((lane & 2) == 0 && row < a.rows) {
+                float *s = a.scale + tc * a.ld_scale + row;
+                if (TR_STORE_OK(ss, s, 4)) *s = amax / a.top;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                inv[i] = __shfl_sync(0xffffffffu, mine, (lane & 16) | (i >> 2) << 3 | (i >> 1 & 1) << 2 | (i & 1));
+            if constexpr (BOTH) {
                 __syncthreads();
+                if (t < 128) {
+                    uint32_t w = kFloorBits;
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-#pragma unroll
-                    for (int w = 0; w < 8; ++w) cm[j] = max(cm[j], col_max[w][cg * 8 + j]);
+                    for (int k = 0; k < 8; ++k) w = max(w, M::word(col_max[k] + t * M::kBytes));
+                    const float cmax = __uint_as_float(w);
+                    col_inv[t] = a.top / cmax;
+                    if (tc * 128 + t < a.cols) {
+                        float *u = a.scale_t + tr * a.ld_scale_t + tc * 128 + t;
+                        if (TR_STORE_OK(su, u, 4)) *u = cmax / a.top;
+                    }
+                }
             }
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            if (r0 + i >= a.rows) continue;
-            const float m = __uint_as_float(rm[i]);
-            store8(a.q + (r0 + i) * a.ld_q, c0, a.cols, to_bytes<E5M2>(v[i], a.top / m), sq);
-            if (BLOCK ? t == 0 && i == 0 : cg == 0) {
-                float *s = a.scale + tc * a.ld_scale + (BLOCK ? tr : r0 + i);
-                if (TR_STORE_OK(ss, s, 4)) *s = m / a.top;
-            }
+            float row[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) row[j] = v.at(i, j);
+            if (r0 + i < a.rows) store8(a.q + (r0 + i) * a.ld_q, c0, a.cols, to_bytes<E5M2>(row, inv[i]), sq);
         }
         if constexpr (BOTH) {
+            if constexpr (!BLOCK) {
+                __syncthreads();
+#pragma unroll
+                for (int j = 0; j < 8; j += 4) {
+                    const float4 f = *reinterpret_cast<const float4 *>(col_inv + cg * 8 + j);
+                    inv[j] = f.x;
+                    inv[j + 1] = f.y;
+                    inv[j + 2] = f.z;
+                    inv[j + 3] = f.w;
+                }
+            }
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float m = __uint_as_float(cm[j]);
                 float col[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) col[i] = v[i][j];
-                turned[(cg * 8 + j) * 16 + (rg ^ cg)] = to_bytes<E5M2>(col, a.top / m);
-                if ((BLOCK ? t == 0 && j == 0 : rg == 0) && c0 + j < a.cols) {
-                    float *s = a.scale_t + tr * a.ld_scale_t + (BLOCK ? tc : c0 + j);
-                    if (TR_STORE_OK(su, s, 4)) *s = m / a.top;
-                }
+                for (int i = 0; i < 8; ++i) col[i] = v.at(i, j);
+                turned[(cg * 8 + j) * 16 + (rg ^ cg)] = to_bytes<E5M2>(col, inv[j]);
             }
             __syncthreads();
 #pragma unroll
@@ -161,26 +348,48 @@ __global__ void __launch_bounds__(kThreads) k_quantize(Quant a) {
                     store8(a.qt + col * a.ld_qt, tr * 128 + cg * 8, a.rows, turned[c * 16 + (cg ^ (c >> 3))], st);
             }
         }
-        if (BOTH || BLOCK) __syncthreads();  // the shared words are written anew in the next turn
+        // The shared words are written anew in the next turn.
+        if (tile + gridDim.x < a.tiles_r * a.tiles_c && (BOTH || BLOCK || LOAD == kWords)) __syncthreads();
     }
 }
 
-template <typename T, bool VEC, bool E5M2>
-cudaError_t launch_typed(const Quant &a, bool block, cudaStream_t stream) {
+template <typename T, Load LOAD, bool E5M2, bool BLOCK, bool BOTH>
+cudaError_t launch_one(const Quant &a, cudaStream_t stream) {
+    auto kern = k_quantize<T, LOAD, E5M2, BLOCK, BOTH>;
+    constexpr size_t smem = LOAD == kWords ? kWordTileBytes : 0;
+    if (smem) {
+        static std::atomic<bool> opted[64];  // per device, zero-initialised (static)
+        static std::mutex mu;
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+        if (!opted[dev].load(std::memory_order_acquire)) {
+            std::lock_guard<std::mutex> lock(mu);
+            if (!opted[dev].load(std::memory_order_relaxed)) {
+                e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+                if (e != cudaSuccess) return e;
+                opted[dev].store(true, std::memory_order_release);
+            }
+        }
+    }
     const int64_t tiles = a.tiles_r * a.tiles_c, most = int64_t(1) << 30;
-    const dim3 grid(unsigned(tiles < most ? tiles : most)), threads(kThreads);
+    return launch_pdl(kern, dim3(unsigned(tiles < most ? tiles : most)), dim3(kThreads), smem, stream, a);
+}
+
+template <typename T, Load LOAD, bool E5M2>
+cudaError_t launch_typed(const Quant &a, bool block, cudaStream_t stream) {
     if (block)
-        return a.qt ? launch_pdl(k_quantize<T, VEC, E5M2, true, true>, grid, threads, 0, stream, a)
-                    : launch_pdl(k_quantize<T, VEC, E5M2, true, false>, grid, threads, 0, stream, a);
-    return a.qt ? launch_pdl(k_quantize<T, VEC, E5M2, false, true>, grid, threads, 0, stream, a)
-                : launch_pdl(k_quantize<T, VEC, E5M2, false, false>, grid, threads, 0, stream, a);
+        return a.qt ? launch_one<T, LOAD, E5M2, true, true>(a, stream) : launch_one<T, LOAD, E5M2, true, false>(a, stream);
+    return a.qt ? launch_one<T, LOAD, E5M2, false, true>(a, stream) : launch_one<T, LOAD, E5M2, false, false>(a, stream);
 }
 
 template <typename T>
 cudaError_t launch_in(const Quant &a, bool block, bool e5m2, cudaStream_t stream) {
-    const bool vec = side_aligned16(a.x, a.ld_x, 0, 1, sizeof(T));
-    if (vec) return e5m2 ? launch_typed<T, true, true>(a, block, stream) : launch_typed<T, true, false>(a, block, stream);
-    return e5m2 ? launch_typed<T, false, true>(a, block, stream) : launch_typed<T, false, false>(a, block, stream);
+    constexpr Load kOther = sizeof(T) == 4 ? kWords : kElements;
+    if (side_aligned16(a.x, a.ld_x, 0, 1, sizeof(T)))
+        return e5m2 ? launch_typed<T, kVector, true>(a, block, stream) : launch_typed<T, kVector, false>(a, block, stream);
+    return e5m2 ? launch_typed<T, kOther, true>(a, block, stream) : launch_typed<T, kOther, false>(a, block, stream);
 }
 
 }  // namespace
