@@ -444,14 +444,15 @@ tr_status tr_selftest_bounded_wait(int32_t arrive, int64_t limit_ns, tr_stream_t
 }
 
 tr_status tr_device_status(void) {
-    unsigned v = 0, w = 0;
+    unsigned v = 0, w = 0, u = 0;
     cudaError_t e = tr::read_and_clear_fault(&v);
     if (e == cudaSuccess) e = tr::read_and_clear_fault_matmul(&w);
+    if (e == cudaSuccess) e = tr::read_and_clear_fault_layernorm(&u);
     if (e != cudaSuccess) {
         tr::set_error("reading the device fault flag failed", e);
         return TR_ERR_CUDA;
     }
-    return v | w ? TR_ERR_TIMEOUT : TR_OK;
+    return v | w | u ? TR_ERR_TIMEOUT : TR_OK;
 }
 
 tr_status tr_debug_bounds(tr_bounds_report *report) {

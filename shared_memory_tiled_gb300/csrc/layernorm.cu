@@ -2,7 +2,6 @@
 #include "launch.cuh"
 #include "row_chunk.cuh"
 #include "tr_internal.h"
-
 namespace tr {
 namespace {
 
@@ -15,16 +14,15 @@ struct Fwd {
     bool w_bf16;
 };
 
-// TPR threads hold R rows at a time, NCH chunks of each to a thread, in
-// registers: x is read once, the deviations are summed about the mean from the
-// registers, and a weight read serves R rows.  EDGE: rows or weights that do not
-// start on 16-byte boundaries, or do not end on them.
-template <typename T, int V, int TPR, int NCH, int R, bool EDGE>
-__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, EDGE || TPR > 512 ? 1 : 768 / (TPR < 128 ? 128 : TPR))
-k_layernorm(const Fwd a) {
+// Few rows: TPR threads hold one row, NCH chunks to a thread, in registers, so that
+// x is read once; the deviations are summed about the mean from the registers.
+// EDGE: rows or weights that do not start on 16-byte boundaries, or do not end on
+// them.
+template <typename T, int V, int TPR, int NCH, bool EDGE>
+__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) k_layernorm(const Fwd a) {
     pdl_prologue();
     constexpr int GROUPS = (TPR < 128 ? 128 : TPR) / TPR;
-    __shared__ float slots[2][R * 32];
+    __shared__ float slots[2][32];
     const T *x = static_cast<const T *>(a.x);
     T *y = static_cast<T *>(a.y);
     [[maybe_unused]] const dbg::Side sx = dbg::side(x, 1, a.rows, a.cols, a.ld_x, 0, sizeof(T));
@@ -35,52 +33,38 @@ k_layernorm(const Fwd a) {
     [[maybe_unused]] const dbg::Side sr = dbg::side(a.rstd, 1, 1, a.rows, a.rows, 0, 4);
     const int t = threadIdx.x % TPR;
     const int cols = int(a.cols);  // a row that fits the registers
-    for (int64_t row0 = (int64_t(blockIdx.x) * GROUPS + threadIdx.x / TPR) * R; row0 < a.rows;
-         row0 += int64_t(gridDim.x) * GROUPS * R) {
-        Pack<T, V> p[R][NCH];
-        const int d = EDGE ? row_shift<T, V>(x + row0 * a.ld_x) : 0;
-        static_assert(!EDGE || R == 1, "rows of their own shift go one at a time");
+    const uint32_t z1 = opaque_zero_1(), z2 = opaque_zero_2();
+    for (int64_t row = int64_t(blockIdx.x) * GROUPS + threadIdx.x / TPR; row < a.rows;
+         row += int64_t(gridDim.x) * GROUPS) {
+        const T *xr = x + row * a.ld_x;
+        const int d = EDGE ? row_shift<T, V>(xr) : 0;
+        Pack<T, V> p[NCH];
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const T *xr = x + (row0 + r) * a.ld_x;
+        for (int i = 0; i < NCH; ++i) p[i] = load_chunk<T, V, EDGE>(xr, (t + i * TPR) * V - d, cols, sx);
+        float mean[1] = {0.0f}, rstd[1] = {0.0f};
 #pragma unroll
-            for (int i = 0; i < NCH; ++i)
-                p[r][i] = load_chunk<T, V, EDGE>(xr, (t + i * TPR) * V - d, row0 + r < a.rows ? cols : 0, sx);
-        }
-        float mean[R], rstd[R];
+        for (int i = 0; i < NCH; ++i)
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            mean[r] = 0.0f;
+            for (int q = 0; q < V; ++q) mean[0] += p[i].get(q);
+        group_sum<TPR, 1>(mean, slots[0]);
+        mean[0] *= a.inv_cols;
 #pragma unroll
-            for (int i = 0; i < NCH; ++i)
+        for (int i = 0; i < NCH; ++i) {
+            const int lo = (t + i * TPR) * V - d;
+            if (!EDGE && lo >= cols) continue;
 #pragma unroll
-                for (int q = 0; q < V; ++q) mean[r] += p[r][i].get(q);
-        }
-        group_sum<TPR, R>(mean, slots[0]);
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            mean[r] *= a.inv_cols;
-            rstd[r] = 0.0f;
-#pragma unroll
-            for (int i = 0; i < NCH; ++i) {
-                const int lo = (t + i * TPR) * V - d;
-                if (!EDGE && lo >= cols) continue;
-                p[r][i].forget();
-#pragma unroll
-                for (int q = 0; q < V; ++q) {
-                    const float o = p[r][i].get(q) - mean[r];
-                    if (!EDGE || (lo + q >= 0 && lo + q < cols)) rstd[r] = fmaf(o, o, rstd[r]);
-                }
+            for (int q = 0; q < V; ++q) {
+                const float o = p[i].get(q, z1) - mean[0];
+                if (!EDGE || (lo + q >= 0 && lo + q < cols)) rstd[0] = fmaf(o, o, rstd[0]);
             }
         }
-        group_sum<TPR, R>(rstd, slots[1]);
-#pragma unroll
-        for (int r = 0; r < R; ++r) rstd[r] = 1.0f / sqrtf(fmaf(rstd[r], a.inv_cols, a.eps));
+        group_sum<TPR, 1>(rstd, slots[1]);
+        rstd[0] = 1.0f / sqrtf(fmaf(rstd[0], a.inv_cols, a.eps));
 #pragma unroll
         for (int i = 0; i < NCH; ++i) {
             const int lo = (t + i * TPR) * V - d;
             if (lo >= cols) continue;
-            float w[V], b[V];
+            float w[V], b[V], v[V];
             if constexpr (EDGE) {
 #pragma unroll
                 for (int q = 0; q < V; ++q) {
@@ -92,28 +76,131 @@ k_layernorm(const Fwd a) {
                 load_weights<V>(a.gamma, a.w_bf16, lo, w, sw);
                 if (a.beta) load_weights<V>(a.beta, a.w_bf16, lo, b, sb);
             }
+            Pack<T, V> o;
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                if (row0 + r >= a.rows) continue;
-                Pack<T, V> o;
-                float v[V];
-                p[r][i].forget();
+            for (int q = 0; q < V; ++q) {
+                const float u = (p[i].get(q, z2) - mean[0]) * rstd[0];
+                v[q] = a.beta ? fmaf(u, w[q], b[q]) : u * w[q];
+            }
+            o.round(v);
+            store_chunk<T, V, EDGE>(y + row * a.ld_y, lo, cols, o, sy);
+        }
+        if (t == 0) {
+            if (a.mean && TR_STORE_OK(ss, a.mean + row, 4)) a.mean[row] = mean[0];
+            if (a.rstd && TR_STORE_OK(sr, a.rstd + row, 4)) a.rstd[row] = rstd[0];
+        }
+    }
+}
+
+// Many rows: a resident block walks the rows, G threads (one warp, or a few with
+// a named barrier of their own) to a row, so that a row's loads, sums and stores
+// run beside those of the block's other rows and no barrier stops them all.  The
+// weights are read from memory once per block and kept in shared memory in
+// fp32, laid out so that a warp's reads share no bank: without EDGE the V weights
+// of a chunk in groups of 4, group h of chunk c at 4 * (h * chunks + c); with EDGE
+// weight j at (j % V) * chunks + j / V, which any shift of the row leaves in
+// neighbouring words.
+template <typename T, int V, int G, int NCH, bool EDGE>
+__global__ void __launch_bounds__(G == 32 && NCH <= 8 ? 1024 : NCH <= 8 ? 768 : 640, 1) k_layernorm_rows(const Fwd a) {
+    extern __shared__ float4 weights4[];
+    __shared__ float slots[2][32];
+    float *gamma = reinterpret_cast<float *>(weights4);
+    const int cols = int(a.cols);
+    const int chunks = (cols + V - 1) / V + (EDGE ? 1 : 0);
+    float *beta = gamma + chunks * V;
+    const T *x = static_cast<const T *>(a.x);
+    T *y = static_cast<T *>(a.y);
+    [[maybe_unused]] const dbg::Side sx = dbg::side(x, 1, a.rows, a.cols, a.ld_x, 0, sizeof(T));
+    [[maybe_unused]] const dbg::Side sy = dbg::side(y, 1, a.rows, a.cols, a.ld_y, 0, sizeof(T));
+    [[maybe_unused]] const dbg::Side sw = dbg::side(a.gamma, 1, 1, a.cols, a.cols, 0, a.w_bf16 ? 2 : 4);
+    [[maybe_unused]] const dbg::Side sb = dbg::side(a.beta, 1, 1, a.cols, a.cols, 0, a.w_bf16 ? 2 : 4);
+    [[maybe_unused]] const dbg::Side ss = dbg::side(a.mean, 1, 1, a.rows, a.rows, 0, 4);
+    [[maybe_unused]] const dbg::Side sr = dbg::side(a.rstd, 1, 1, a.rows, a.rows, 0, 4);
+    pdl_prologue();
+    auto place = [&](int j) {
+        return EDGE ? j % V * chunks + j / V : 4 * (j % V / 4 * chunks + j / V) + j % 4;
+    };
+    for (int j = threadIdx.x; j < cols; j += blockDim.x) {
+        gamma[place(j)] = weight(a.gamma, a.w_bf16, j, sw);
+        if (a.beta) beta[place(j)] = weight(a.beta, a.w_bf16, j, sb);
+    }
+    __syncthreads();
+    const int group = threadIdx.x / G, groups = blockDim.x / G, t = threadIdx.x % G;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t z1 = opaque_zero_1(), z2 = opaque_zero_2();
+    auto sum = [&](float v, int slot) {
+        v = warp_sum(v);
+        if constexpr (G > 32) {
+            if (lane == 0) slots[slot][warp] = v;
+            asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(G) : "memory");
+            v = slots[slot][group * (G / 32)];
+#pragma unroll
+            for (int k = 1; k < G / 32; ++k) v += slots[slot][group * (G / 32) + k];
+        }
+        return v;
+    };
+    for (int64_t row = int64_t(blockIdx.x) * groups + group; row < a.rows; row += int64_t(gridDim.x) * groups) {
+        const T *xr = x + row * a.ld_x;
+        const int d = EDGE ? row_shift<T, V>(xr) : 0;
+        Pack<T, V> p[NCH];
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) p[i] = load_chunk<T, V, EDGE>(xr, (t + i * G) * V - d, cols, sx);
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+            float part = 0.0f;
+#pragma unroll
+            for (int q = 0; q < V; ++q) part += p[i].get(q);
+            s += part;
+        }
+        const float mean = sum(s, 0) * a.inv_cols;
+        s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+            const int lo = (t + i * G) * V - d;
+            if (!EDGE && lo >= cols) continue;
+            float part = 0.0f;
+#pragma unroll
+            for (int q = 0; q < V; ++q) {
+                const float o = p[i].get(q, z1) - mean;
+                if (!EDGE || (lo + q >= 0 && lo + q < cols)) part = fmaf(o, o, part);
+            }
+            s += part;
+        }
+        const float rstd = 1.0f / sqrtf(fmaf(sum(s, 1), a.inv_cols, a.eps));
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+            const int c = t + i * G, lo = c * V - d;
+            if (lo >= cols) continue;
+            float v[V];
+#pragma unroll
+            for (int q = 0; q < V; ++q) v[q] = (p[i].get(q, z2) - mean) * rstd;
+            if constexpr (EDGE) {
 #pragma unroll
                 for (int q = 0; q < V; ++q) {
-                    const float u = (p[r][i].get(q) - mean[r]) * rstd[r];
-                    v[q] = a.beta ? fmaf(u, w[q], b[q]) : u * w[q];
+                    if (lo + q < 0 || lo + q >= cols) continue;
+                    const int at = place(lo + q);
+                    v[q] = a.beta ? fmaf(v[q], gamma[at], beta[at]) : v[q] * gamma[at];
                 }
-                o.round(v);
-                store_chunk<T, V, EDGE>(y + (row0 + r) * a.ld_y, lo, cols, o, sy);
-            }
-        }
-        if (t == 0)
+            } else {
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                if (row0 + r >= a.rows) continue;
-                if (a.mean && TR_STORE_OK(ss, a.mean + row0 + r, 4)) a.mean[row0 + r] = mean[r];
-                if (a.rstd && TR_STORE_OK(sr, a.rstd + row0 + r, 4)) a.rstd[row0 + r] = rstd[r];
+                for (int h = 0; h < V / 4; ++h) {
+                    const float4 w = weights4[h * chunks + c];
+                    const float4 b = a.beta ? weights4[chunks * (V / 4) + h * chunks + c] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    v[4 * h] = fmaf(v[4 * h], w.x, b.x);
+                    v[4 * h + 1] = fmaf(v[4 * h + 1], w.y, b.y);
+                    v[4 * h + 2] = fmaf(v[4 * h + 2], w.z, b.z);
+                    v[4 * h + 3] = fmaf(v[4 * h + 3], w.w, b.w);
+                }
             }
+            Pack<T, V> o;
+            o.round(v);
+            store_chunk<T, V, EDGE>(y + row * a.ld_y, lo, cols, o, sy);
+        }
+        if (t == 0) {
+            if (a.mean && TR_STORE_OK(ss, a.mean + row, 4)) a.mean[row] = mean;
+            if (a.rstd && TR_STORE_OK(sr, a.rstd + row, 4)) a.rstd[row] = rstd;
+        }
     }
 }
 
@@ -176,6 +263,16 @@ __global__ void __launch_bounds__(1024) k_layernorm_long(const Fwd a) {
     }
 }
 
+// One block to an SM, with its copy of the weights.
+template <typename K>
+cudaError_t launch_rows(K kern, int threads, int v, const Fwd &a, bool edge, cudaStream_t stream) {
+    const int64_t chunks = (a.cols + v - 1) / v + (edge ? 1 : 0);
+    const size_t smem = size_t(chunks) * v * 4 * (a.beta ? 2 : 1);
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, dim3(unsigned(sm_count())), dim3(threads), smem, stream, a);
+}
+
 template <typename T>
 cudaError_t launch_typed(const tr_layernorm_args &p) {
     constexpr int V = 16 / int(sizeof(T));
@@ -196,22 +293,30 @@ cudaError_t launch_typed(const tr_layernorm_args &p) {
     };
     if (!alike) return run(k_layernorm_long<T, 1>, 1024, 1);
     const int64_t chunks = (a.cols + (shifted ? V - 1 : 0) + V - 1) / V;
-    const bool many = a.rows >= int64_t(sm_count()) * 16;  // two rows to a block still fill the machine
+    // Rows for every group of every resident block: the weights' copy pays.
+    if (a.rows >= int64_t(sm_count()) * 32 && chunks <= 2048) {
+#define TR_ROWS(G, NCH, BLOCK)                                                            \
+    if (chunks <= G * NCH)                                                                \
+        return edge ? launch_rows(k_layernorm_rows<T, V, G, NCH, true>, BLOCK, V, a, true, stream) \
+                    : launch_rows(k_layernorm_rows<T, V, G, NCH, false>, BLOCK, V, a, false, stream);
+        TR_ROWS(32, 4, 1024)
+        TR_ROWS(32, 8, 1024)
+        TR_ROWS(32, 16, 640)
+        TR_ROWS(128, 8, 768)
+        TR_ROWS(128, 16, 640)
+#undef TR_ROWS
+    }
 #define TR_ROWS(TPR, NCH, BLOCK)                                                              \
     if (chunks <= TPR * NCH)                                                                  \
-        return edge   ? run(k_layernorm<T, V, TPR, NCH, 1, true>, BLOCK, BLOCK / TPR)         \
-               : many ? run(k_layernorm<T, V, TPR, NCH, 2, false>, BLOCK, 2 * BLOCK / TPR)    \
-                      : run(k_layernorm<T, V, TPR, NCH, 1, false>, BLOCK, BLOCK / TPR);
+        return edge ? run(k_layernorm<T, V, TPR, NCH, true>, BLOCK, BLOCK / TPR)              \
+                    : run(k_layernorm<T, V, TPR, NCH, false>, BLOCK, BLOCK / TPR);
     TR_ROWS(32, 1, 128)
-    TR_ROWS(32, 2, 128)
     TR_ROWS(32, 4, 128)
-    TR_ROWS(128, 2, 128)
     TR_ROWS(128, 4, 128)
     TR_ROWS(256, 4, 256)
     TR_ROWS(512, 4, 512)
+    TR_ROWS(1024, 4, 1024)
 #undef TR_ROWS
-    if (chunks <= 4096)
-        return edge ? run(k_layernorm<T, V, 1024, 4, 1, true>, 1024, 1) : run(k_layernorm<T, V, 1024, 4, 1, false>, 1024, 1);
     return run(k_layernorm_long<T, V>, 1024, 1);
 }
 

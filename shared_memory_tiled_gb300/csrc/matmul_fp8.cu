@@ -313,9 +313,7 @@ cudaError_t launch_shape(const CUtensorMap &map_p, const CUtensorMap &map_q, con
 TR_BOUNDS_READER(read_bounds_matmul_fp8)
 
 cudaError_t read_and_clear_fault_matmul(unsigned *value) {
-    cudaError_t e = cudaDeviceSynchronize();
-    if (e != cudaSuccess) return e;
-    e = cudaMemcpyFromSymbol(value, g_fault_flag_matmul, sizeof(unsigned));
+    cudaError_t e = cudaMemcpyFromSymbol(value, g_fault_flag_matmul, sizeof(unsigned));
     if (e != cudaSuccess) return e;
     const unsigned zero = 0;
     return cudaMemcpyToSymbol(g_fault_flag_matmul, &zero, sizeof(unsigned));

@@ -20,8 +20,11 @@ namespace tr {
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 
-// V values of type T: 16 bytes, or one value.  bf16 stays packed in words and is
-// unpacked where it is used.
+// V values of type T: 16 bytes, or one value.  bf16 stays packed in words.  A row in
+// registers is unpacked once in every walk over it: the compiler would rather
+// keep the first walk's unpacked values, twice the registers, and spill, so
+// each walk after the first passes a zero that it cannot see through (`z`, one
+// register per walk), which the byte permutation takes its zero bytes from.
 template <typename T, int V>
 struct Pack;
 
@@ -38,8 +41,8 @@ struct alignas(4 * V) Pack<float, V> {
 #pragma unroll
         for (int q = 0; q < V; ++q) e[q] = v[q];
     }
-    // Unpack anew from here on (nothing is unpacked).
-    __device__ __forceinline__ void forget() {}
+    __device__ __forceinline__ float get(int q, uint32_t) const { return e[q]; }
+    __device__ __forceinline__ float2 pair(int k) const { return make_float2(e[2 * k], e[2 * k + 1]); }
 };
 
 template <>
@@ -63,9 +66,9 @@ struct alignas(16) Pack<__nv_bfloat16, 8> {
             w[k] = *reinterpret_cast<const uint32_t *>(&h);
         }
     }
-    // Unpack anew from here on, instead of keeping twice the registers.
-    __device__ __forceinline__ void forget() {
-        asm volatile("" : "+r"(w[0]), "+r"(w[1]), "+r"(w[2]), "+r"(w[3]));
+    __device__ __forceinline__ float2 pair(int k) const { return make_float2(get(2 * k), get(2 * k + 1)); }
+    __device__ __forceinline__ float get(int q, uint32_t z) const {
+        return __uint_as_float(__byte_perm(w[q >> 1], z, q & 1 ? 0x3244 : 0x1044));
     }
 };
 
@@ -77,7 +80,7 @@ struct Pack<__nv_bfloat16, 1> {
     __device__ __forceinline__ void set(int, __nv_bfloat16 v) { e = v; }
     __device__ __forceinline__ __nv_bfloat16 elem(int) const { return e; }
     __device__ __forceinline__ void round(const float (&v)[1]) { e = __float2bfloat16_rn(v[0]); }
-    __device__ __forceinline__ void forget() {}
+    __device__ __forceinline__ float get(int q, uint32_t) const { return get(q); }
 };
 
 template <int V>
@@ -139,6 +142,10 @@ __device__ __forceinline__ void store_chunk(T *row, int64_t lo, int64_t cols, co
                 row[lo + q] = pack_elem(p, q);
     }
 }
+
+// Zeros for Pack::get: the launches here are one-dimensional.
+__device__ __forceinline__ uint32_t opaque_zero_1() { return gridDim.y - 1; }
+__device__ __forceinline__ uint32_t opaque_zero_2() { return gridDim.z - 1; }
 
 // Sum over the 32 lanes, in every lane.
 __device__ __forceinline__ float warp_sum(float v) {
