@@ -16,8 +16,6 @@
 // Few tiles: the blocks of the contraction are split over a cluster of CTAs and
 // their sums joined through distributed shared memory, in rank order.
 #include <atomic>
-#include <cstring>
-#include <mutex>
 
 #include "bounds.cuh"
 #include "launch.cuh"
@@ -59,14 +57,15 @@ struct Product {
     int32_t out_bf16, accumulate;
 };
 
-// Rows of P and of Q at which a tile begins; 16 tiles of P go with each tile of Q
-// before the next, so that the operands in use at one time stay in L2.
-__device__ __forceinline__ void tile_at(const Product &g, int64_t tile, int bn, int64_t *p0,
-                                        int64_t *q0) {
-    const int64_t group = tile / (16 * g.tiles_q), at = tile - group * 16 * g.tiles_q;
-    const int64_t left = g.tiles_p - group * 16, tall = left < 16 ? left : 16;
-    *p0 = (group * 16 + at % tall) * kTileP;
-    *q0 = at / tall * bn;
+// Rows of P and of Q at which a tile of bp x bq begins; `most` tiles of P go with
+// each tile of Q before the next, so that the operands in use at one time stay
+// in L2.
+__device__ __forceinline__ void tile_at(const Product &g, int64_t tile, int bp, int bq, int most,
+                                        int64_t *p0, int64_t *q0) {
+    const int64_t group = tile / (most * g.tiles_q), at = tile - group * most * g.tiles_q;
+    const int64_t left = g.tiles_p - group * most, tall = left < most ? left : most;
+    *p0 = (group * most + at % tall) * bp;
+    *q0 = at / tall * bq;
 }
 
 // out[i][j] = v, or += v; `s` is the output's logical extent.
@@ -124,7 +123,7 @@ k_matmul_fp8(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ 
     const int64_t tile = blockIdx.x / unsigned(g.split);
     const int rank = int(blockIdx.x % unsigned(g.split));
     int64_t p0, q0;
-    tile_at(g, tile, BN, &p0, &q0);
+    tile_at(g, tile, kTileP, BN, 16, &p0, &q0);
     const int first = int(int64_t(g.blocks) * rank / g.split);
     const int count = int(int64_t(g.blocks) * (rank + 1) / g.split) - first;
     bool ok = true;
@@ -153,7 +152,7 @@ k_matmul_fp8(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ 
         }
     } else if (warp == 1) {
         if (lane == 0) {
-            const uint32_t idesc = ptx::f8_idesc(g.p_e5m2, g.q_e5m2, BN);
+            const uint32_t idesc = ptx::f8_idesc(g.p_e5m2, g.q_e5m2, 128, BN);
             for (int i = 0; i < count; ++i) {
                 const int s = i % S::kStages, b = i & 1;
                 ok = ptx::mbar_wait_bounded(full + s, (i / S::kStages) & 1) &&
@@ -203,7 +202,7 @@ k_matmul_fp8(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ 
             for (int c = 0; c < BN; c += 16) {
                 float v[16];
                 ptx::tmem_load16(v, tmem + (uint32_t(w * 32) << 16) + b * BN + c);
-                ptx::tmem_wait_load();
+                ptx::tmem_wait_load16(v);
 #pragma unroll
                 for (int k = 0; k < 16; k += 4) {
                     const float4 f = *reinterpret_cast<const float4 *>(&scales[b][c + k]);
@@ -256,6 +255,279 @@ k_matmul_fp8(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ 
     }
 }
 
+// --- large products: two CTAs to a 256 x 256 tile --------------------------------------
+//
+// A CTA pair loads 64 KB per block of the contraction for a 256 x 256 tile, 64 bytes
+// a clock and SM at the tensor cores' full rate, half of what two 128 x 128 tiles
+// would take from L2 and shared memory.  Resident pairs walk the tiles.  Per CTA:
+//
+//   warp 0     TMA of its 128 rows of P and of its half of Q
+//   warp 1     (rank 0) matrix instructions of both CTAs, 4 per stage
+//   warps 4-11 two groups of 128 threads, 128 columns each: a thread takes its row's
+//              block sums out of tensor memory, 16 columns at a time with the next
+//              16 on the way, and adds them, scaled, to 128 sums in registers
+//
+// QROW: Q has a scale to each row (a column of the tile): its 128 scales go through
+// shared memory; else one scale for the group's columns, and one multiplication
+// fewer to each value.
+
+constexpr int kPairThreads = 384;
+// Registers at launch (168 x 384 = 64512), and how the warpgroups share them:
+// 56 x 128 + 224 x 256 = 64512.
+constexpr int kFewRegisters = 56, kManyRegisters = 224;
+constexpr int kPairTile = 256;
+constexpr int kPairStages = 5;
+constexpr int kPairStageBytes = 2 * kBytesP;       // 128 rows of P and 128 of Q
+constexpr int kStagingBytes = 8 * 32 * 128;        // 32 rows of 128 bytes to each of 8 warps
+constexpr size_t kPairSmem = 1024 + size_t(kPairStages) * kPairStageBytes + kStagingBytes;
+
+// Writes 32 rows x 128 columns from registers: a thread holds a row's sums, lanes
+// write 128-byte pieces of rows.  The staging tile's 16-byte chunks stand at chunk
+// XOR row % 8, so that neither side shares a bank.
+template <typename F>
+__device__ __forceinline__ void store_rows(const Product &g, int64_t row0, int64_t col0, uint4 *staging,
+                                           const F &value, const dbg::Side &s) {
+    const int lane = threadIdx.x & 31;
+    const int es = g.out_bf16 ? 2 : 4;
+    const bool whole = !g.accumulate && col0 + 128 <= g.q && (g.ld_out * es) % 16 == 0 &&
+                       (reinterpret_cast<uintptr_t>(g.out) & 15u) == 0;
+    if (whole && g.out_bf16) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            __syncwarp();
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                uint32_t w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int j = half * 64 + c * 8 + 2 * k;
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(value(j), value(j + 1));
+                    w[k] = *reinterpret_cast<const uint32_t *>(&h);
+                }
+                staging[lane * 8 + (c ^ (lane & 7))] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int r = k * 4 + (lane >> 3), c = lane & 7;
+                __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(g.out) + (row0 + r) * g.ld_out + col0 + half * 64 + c * 8;
+                if (row0 + r < g.p && TR_STORE_OK(s, o, 16))
+                    *reinterpret_cast<uint4 *>(o) = staging[r * 8 + (c ^ (r & 7))];
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int quarter = 0; quarter < 4; ++quarter) {
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            const int j = quarter * 32 + c * 4;
+            staging[lane * 8 + (c ^ (lane & 7))] =
+                make_uint4(__float_as_uint(value(j)), __float_as_uint(value(j + 1)),
+                           __float_as_uint(value(j + 2)), __float_as_uint(value(j + 3)));
+        }
+        __syncwarp();
+        if (whole) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int r = k * 4 + (lane >> 3), c = lane & 7;
+                float *o = static_cast<float *>(g.out) + (row0 + r) * g.ld_out + col0 + quarter * 32 + c * 4;
+                if (row0 + r < g.p && TR_STORE_OK(s, o, 16))
+                    *reinterpret_cast<uint4 *>(o) = staging[r * 8 + (c ^ (r & 7))];
+            }
+        } else {
+            const float *f = reinterpret_cast<const float *>(staging);
+            const int64_t col = col0 + quarter * 32 + lane;
+            for (int r = 0; r < 32 && row0 + r < g.p; ++r)
+                if (col < g.q) put(g, row0 + r, col, f[(r * 8 + ((lane >> 2) ^ (r & 7))) * 4 + (lane & 3)], s);
+        }
+    }
+}
+
+template <bool QROW>
+__global__ void __launch_bounds__(kPairThreads, 1)
+k_matmul_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
+              const __grid_constant__ Product g) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t full[kPairStages], empty[kPairStages], sums_full[2], sums_empty[2];
+    __shared__ uint32_t tmem_base;
+    __shared__ alignas(16) float scales[2][QROW ? 256 : 4];
+    uint8_t *stages = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint4 *staging = reinterpret_cast<uint4 *>(stages + kPairStages * kPairStageBytes);
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const uint32_t rank = ptx::cluster_rank();
+
+    if (t == 0) {
+        ptx::prefetch_tensormap(&map_p);
+        ptx::prefetch_tensormap(&map_q);
+        for (int i = 0; i < kPairStages; ++i) {
+            ptx::mbar_init(full + i, 1);
+            ptx::mbar_init(empty + i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(sums_full + i, 1);
+            ptx::mbar_init(sums_empty + i, 16);  // the warps of both CTAs
+        }
+        ptx::fence_barrier_init();
+    }
+    if (warp == 1) ptx::tmem_alloc_pair(&tmem_base, 512);
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::cluster_sync();  // the other CTA's barriers are ready
+    ptx::tc_fence_after();
+    const uint32_t tmem = tmem_base;
+    pdl_prologue();  // after the tensor memory is taken, as above
+
+    const int64_t tiles = g.tiles_p * g.tiles_q;
+    const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    bool ok = true;
+
+    if (warp < 4) {
+      ptx::registers_down<kFewRegisters>();
+      if (warp == 0) {
+        if (lane == 0) {
+            int s = 0;
+            uint32_t phase = 1;  // the first round finds every stage empty
+            for (int64_t tile = pair; tile < tiles && ok; tile += pairs) {
+                int64_t p0, q0;
+                tile_at(g, tile, kPairTile, kPairTile, 8, &p0, &q0);
+                for (int i = 0; i < g.blocks; ++i) {
+                    if (!ptx::mbar_wait_bounded(empty + s, phase)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t *dst = stages + s * kPairStageBytes;
+                    if (rank == 0) ptx::mbar_arrive_expect_tx(full + s, 2 * kPairStageBytes);
+                    const uint32_t bar = ptx::peer_addr(full + s, 0);
+                    ptx::tma_load_2d_pair(dst, &map_p, bar, i * kBlockK, int32_t(p0) + int32_t(rank) * 128);
+                    ptx::tma_load_2d_pair(dst + kBytesP, &map_q, bar, i * kBlockK, int32_t(q0) + int32_t(rank) * 128);
+                    if (++s == kPairStages) {
+                        s = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            if (!ok) {  // no load may land after the block has gone: they take microseconds
+                const uint64_t t0 = ptx::global_timer_ns();
+                for (uint32_t n = 0; n < 1u << 24 && ptx::global_timer_ns() - t0 < 2000000; ++n) {
+                }
+            }
+        }
+      } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            const uint32_t idesc = ptx::f8_idesc(g.p_e5m2, g.q_e5m2, 256, 256);
+            int s = 0, b = 0;
+            uint32_t phase = 0, sums_phase = 1;
+            for (int64_t tile = pair; tile < tiles && ok; tile += pairs)
+                for (int i = 0; i < g.blocks; ++i) {
+                    ok = ptx::mbar_wait_bounded(full + s, phase) && ptx::mbar_wait_bounded(sums_empty + b, sums_phase);
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    const uint32_t at = ptx::smem_addr(stages + s * kPairStageBytes);
+                    const uint64_t dp = ptx::operand_desc(at), dq = ptx::operand_desc(at + kBytesP);
+#pragma unroll
+                    for (int k = 0; k < kBlockK / 32; ++k)
+                        ptx::mma_f8_pair(tmem + b * 256, dp + 2 * k, dq + 2 * k, idesc, k > 0);
+                    ptx::mma_commit_pair(empty + s);
+                    ptx::mma_commit_pair(sums_full + b);
+                    if (++s == kPairStages) {
+                        s = 0;
+                        phase ^= 1;
+                    }
+                    b ^= 1;
+                    if (b == 0) sums_phase ^= 1;
+                }
+        }
+      }
+    } else {
+        ptx::registers_up<kManyRegisters>();
+        const int w = warp & 3, group = (warp - 4) >> 2, th = t & 127;
+        const uint32_t tsum = tmem + (uint32_t(w * 32) << 16) + group * 128;
+        const uint32_t release[2] = {ptx::peer_addr(sums_empty, 0), ptx::peer_addr(sums_empty + 1, 0)};
+        [[maybe_unused]] const dbg::Side side_p = dbg::side(g.scale_p, 1, g.blocks, g.p_block == 1 ? g.p : (g.p + 127) / 128, g.ld_p, 0, 4);
+        [[maybe_unused]] const dbg::Side side_q = dbg::side(g.scale_q, 1, g.blocks, g.q_block == 1 ? g.q : (g.q + 127) / 128, g.ld_q, 0, 4);
+        [[maybe_unused]] const dbg::Side so = dbg::side(g.out, 1, g.p, g.q, g.ld_out, 0, g.out_bf16 ? 2 : 4);
+        int b = 0;
+        uint32_t phase = 0;
+        for (int64_t tile = pair; tile < tiles; tile += pairs) {
+            int64_t p0, q0;
+            tile_at(g, tile, kPairTile, kPairTile, 8, &p0, &q0);
+            p0 += rank * 128;
+            q0 += group * 128;
+            const int64_t row = p0 + w * 32 + lane, col = q0 + (QROW ? th : 0);
+            const float *sp = g.scale_p + (g.p_block == 1 ? row : row >> 7);
+            const float *sq = g.scale_q + (g.q_block == 1 ? col : col >> 7);
+            // Scales two blocks ahead: a block takes about as long as a read from L2.
+            auto scale_p = [&](int i) {
+                const float *p = sp + i * g.ld_p;
+                return i < g.blocks && row < g.p && TR_LOAD_OK(side_p, p, 4) ? *p : 0.0f;
+            };
+            auto scale_q = [&](int i) {
+                const float *p = sq + i * g.ld_q;
+                return i < g.blocks && col < g.q && TR_LOAD_OK(side_q, p, 4) ? *p : 0.0f;
+            };
+            float p_now = scale_p(0), p_next = scale_p(1), q_now = scale_q(0), q_next = scale_q(1);
+            float2 acc[64];
+#pragma unroll
+            for (int c = 0; c < 64; ++c) acc[c] = make_float2(0.0f, 0.0f);
+            for (int i = 0; i < g.blocks; ++i) {
+                const float f = QROW ? p_now : p_now * q_now;
+                const float2 f2 = make_float2(f, f);
+                if constexpr (QROW) {
+                    scales[b][group * 128 + th] = q_now;
+                    ptx::named_sync(1 + group, 128);
+                }
+                p_now = p_next;
+                q_now = q_next;
+                p_next = scale_p(i + 2);
+                q_next = scale_q(i + 2);
+                // A wait that ran out is not repeated, but the meetings go on.
+                if (ok) ok = ptx::mbar_wait_bounded(sums_full + b, phase);
+                __syncwarp();
+                ptx::tc_fence_after();
+                float v[2][16];
+                ptx::tmem_load16(v[0], tsum + b * 256);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    ptx::tmem_wait_load16(v[c & 1]);
+                    if (c < 7) {
+                        ptx::tmem_load16(v[(c + 1) & 1], tsum + b * 256 + (c + 1) * 16);
+                    } else {  // every sum is in registers: the tensor cores may go on
+                        ptx::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive_at(release[b]);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 16; k += 4) {
+                        float2 f01 = f2, f23 = f2;
+                        if constexpr (QROW) {
+                            const float4 q = *reinterpret_cast<const float4 *>(&scales[b][group * 128 + c * 16 + k]);
+                            f01 = __fmul2_rn(f2, make_float2(q.x, q.y));
+                            f23 = __fmul2_rn(f2, make_float2(q.z, q.w));
+                        }
+                        float2 &a0 = acc[c * 8 + k / 2], &a1 = acc[c * 8 + k / 2 + 1];
+                        a0 = __ffma2_rn(make_float2(v[c & 1][k], v[c & 1][k + 1]), f01, a0);
+                        a1 = __ffma2_rn(make_float2(v[c & 1][k + 2], v[c & 1][k + 3]), f23, a1);
+                    }
+                }
+                b ^= 1;
+                if (b == 0) phase ^= 1;
+            }
+            store_rows(g, p0 + w * 32, q0, staging + (warp - 4) * 256,
+                       [&](int j) { return j & 1 ? acc[j >> 1].y : acc[j >> 1].x; }, so);
+        }
+    }
+    if (!ok) atomicExch(&g_fault_flag_matmul, 1u);
+    __syncwarp();
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::cluster_sync();  // neither CTA leaves while the other's instructions read its operands
+    ptx::tc_fence_after();
+    if (warp == 1) ptx::tmem_free_pair(tmem, 512);
+}
+
 bool encode_operand(CUtensorMap *map, const void *base, int64_t k, int64_t rows, int64_t ld,
                     int box_rows) {
     EncodeTiledFn fn = encode_fn();
@@ -269,35 +541,31 @@ bool encode_operand(CUtensorMap *map, const void *base, int64_t k, int64_t rows,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BN, bool TURN>
-cudaError_t launch_shape(const CUtensorMap &map_p, const CUtensorMap &map_q, const Product &g,
-                         cudaStream_t stream) {
-    auto kern = k_matmul_fp8<BN, TURN>;
-    constexpr size_t smem = Shape<BN>::kSmem;
-    static std::atomic<bool> opted[64];  // per device, zero-initialised (static)
-    static std::mutex mu;
+// Launches a kernel of this unit in clusters of `cluster` blocks, with its shared
+// memory allowed once per device.
+template <typename K>
+cudaError_t launch_kernel(K kern, std::atomic<bool> *opted, int64_t grid, int threads, size_t smem, int cluster,
+                          const CUtensorMap &map_p, const CUtensorMap &map_q, const Product &g,
+                          cudaStream_t stream) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (!opted[dev].load(std::memory_order_acquire)) {
-        std::lock_guard<std::mutex> lock(mu);
-        if (!opted[dev].load(std::memory_order_relaxed)) {
-            e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-            if (e != cudaSuccess) return e;
-            opted[dev].store(true, std::memory_order_release);
-        }
+    if (!opted[dev].load(std::memory_order_acquire)) {  // setting it twice is harmless
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+        if (e != cudaSuccess) return e;
+        opted[dev].store(true, std::memory_order_release);
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(g.tiles_p * g.tiles_q * g.split));
-    cfg.blockDim = dim3(kThreads);
+    cfg.gridDim = dim3(unsigned(grid));
+    cfg.blockDim = dim3(unsigned(threads));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = unsigned(g.split);
+    attr[1].val.clusterDim.x = unsigned(cluster);
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
@@ -305,6 +573,23 @@ cudaError_t launch_shape(const CUtensorMap &map_p, const CUtensorMap &map_q, con
     e = cudaLaunchKernelEx(&cfg, kern, map_p, map_q, g);
     if (e != cudaSuccess) (void)cudaGetLastError();
     return e;
+}
+
+template <int BN, bool TURN>
+cudaError_t launch_shape(const CUtensorMap &map_p, const CUtensorMap &map_q, const Product &g,
+                         cudaStream_t stream) {
+    static std::atomic<bool> opted[64];  // per device, zero-initialised (static)
+    return launch_kernel(k_matmul_fp8<BN, TURN>, opted, g.tiles_p * g.tiles_q * g.split, kThreads,
+                         Shape<BN>::kSmem, g.split, map_p, map_q, g, stream);
+}
+
+template <bool QROW>
+cudaError_t launch_pair(const CUtensorMap &map_p, const CUtensorMap &map_q, const Product &g,
+                        cudaStream_t stream) {
+    static std::atomic<bool> opted[64];
+    const int64_t pairs = sm_count() / 2, tiles = g.tiles_p * g.tiles_q;
+    return launch_kernel(k_matmul_pair<QROW>, opted, 2 * (tiles < pairs ? tiles : pairs), kPairThreads, kPairSmem, 2,
+                         map_p, map_q, g, stream);
 }
 
 }  // namespace
@@ -329,7 +614,8 @@ cudaError_t launch_matmul_fp8(const tr_matmul_fp8_args &a, const char **why) {
     }
     // Up to 64 rows of a: they are the columns of the tile, and b its 128 rows.
     const bool turn = a.m <= 64;
-    const int bn = !turn ? 128 : a.m <= 16 ? 16 : a.m <= 32 ? 32 : 64;
+    const bool pair = !turn && ((a.m + 255) / 256) * ((a.n + 255) / 256) >= sm_count() / 2;
+    const int bn = pair ? 256 : !turn ? 128 : a.m <= 16 ? 16 : a.m <= 32 ? 32 : 64;
     Product g{};
     g.scale_p = turn ? a.scale_b : a.scale_a;
     g.scale_q = turn ? a.scale_a : a.scale_b;
@@ -339,7 +625,7 @@ cudaError_t launch_matmul_fp8(const tr_matmul_fp8_args &a, const char **why) {
     g.ld_out = a.ld_out;
     g.p = turn ? a.n : a.m;
     g.q = turn ? a.m : a.n;
-    g.tiles_p = (g.p + kTileP - 1) / kTileP;
+    g.tiles_p = pair ? (g.p + 255) / 256 : (g.p + kTileP - 1) / kTileP;
     g.tiles_q = (g.q + bn - 1) / bn;
     g.blocks = int32_t((a.k + kBlockK - 1) / kBlockK);
     g.p_block = turn ? a.b_block_rows : a.a_block_rows;
@@ -352,7 +638,7 @@ cudaError_t launch_matmul_fp8(const tr_matmul_fp8_args &a, const char **why) {
     // keeping four blocks or more.
     const int64_t tiles = g.tiles_p * g.tiles_q;
     g.split = 1;
-    while (g.split < 8 && tiles * g.split * 2 <= int64_t(sm_count()) * 2 && g.blocks >= g.split * 8)
+    while (!pair && g.split < 8 && tiles * g.split * 2 <= int64_t(sm_count()) * 2 && g.blocks >= g.split * 8)
         g.split *= 2;
     if (tiles * g.split > 0x7fffffffll) {
         *why = "matmul: too many tiles for one launch";
@@ -360,10 +646,12 @@ cudaError_t launch_matmul_fp8(const tr_matmul_fp8_args &a, const char **why) {
     }
     CUtensorMap map_a, map_b;
     if (!encode_operand(&map_a, a.a, a.k, a.m, a.lda, turn ? bn : kTileP) ||
-        !encode_operand(&map_b, a.b, a.k, a.n, a.ldb, turn ? kTileP : bn)) {
+        !encode_operand(&map_b, a.b, a.k, a.n, a.ldb, turn || pair ? kTileP : bn)) {
         *why = "matmul: cuTensorMapEncodeTiled rejected the operands (a pitch of 2^40 bytes or more)";
         return cudaErrorInvalidValue;
     }
+    if (pair)
+        return g.q_block == 1 ? launch_pair<true>(map_a, map_b, g, stream) : launch_pair<false>(map_a, map_b, g, stream);
     if (!turn) return launch_shape<128, false>(map_a, map_b, g, stream);
     if (bn == 16) return launch_shape<16, true>(map_b, map_a, g, stream);
     if (bn == 32) return launch_shape<32, true>(map_b, map_a, g, stream);

@@ -69,8 +69,12 @@ __device__ __forceinline__ void tmem_load16(float (&v)[16], uint32_t addr) {
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-__device__ __forceinline__ void tmem_wait_load() {
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+// The loads are complete; `v`, the last one's values, may be used from here on.
+__device__ __forceinline__ void tmem_wait_load16(float (&v)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]),
+                   "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]),
+                   "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])::"memory");
 }
 
 // Descriptor of an operand tile in shared memory: rows of 128 bytes along the
@@ -82,9 +86,9 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
            uint64_t(1) << 46 | uint64_t(2) << 61;
 }
 
-// Instruction descriptor: fp32 sums, operand types (0 e4m3, 1 e5m2), 128 x N.
-__device__ __forceinline__ uint32_t f8_idesc(uint32_t a_e5m2, uint32_t b_e5m2, uint32_t n) {
-    return 1u << 4 | a_e5m2 << 7 | b_e5m2 << 10 | (n >> 3) << 17 | (128u >> 4) << 24;
+// Instruction descriptor: fp32 sums, operand types (0 e4m3, 1 e5m2), M x N.
+__device__ __forceinline__ uint32_t f8_idesc(uint32_t a_e5m2, uint32_t b_e5m2, uint32_t m, uint32_t n) {
+    return 1u << 4 | a_e5m2 << 7 | b_e5m2 << 10 | (n >> 3) << 17 | (m >> 4) << 24;
 }
 
 __device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, uint64_t *bar,
@@ -101,12 +105,84 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+// Address, in the cluster's window, of the same shared word in CTA `rank`.
+__device__ __forceinline__ uint32_t peer_addr(const void *p, uint32_t rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+    return a;
+}
+
+__device__ __forceinline__ void mbar_arrive_at(uint32_t addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+
+// Registers of each thread of this warpgroup: a block's warpgroups share what it was
+// launched with, so their sum stays at or below that.
+template <int N>
+__device__ __forceinline__ void registers_down() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void registers_up() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// --- two CTAs on one tile (cta_group::2) ---------------------------------------------
+// The pair's tensor cores compute D[256][N] = A[256][32] B[N][32]^T: each CTA holds
+// 128 rows of A, N/2 rows of B and 128 rows of D, at the same shared offsets and
+// columns.  The CTA of rank 0 issues; tensor memory is taken and freed by both.
+
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t *smem_dst, uint32_t columns) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_addr(smem_dst)),
+                 "r"(columns)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+}
+
+__device__ __forceinline__ void tmem_free_pair(uint32_t addr, uint32_t columns) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns));
+}
+
+__device__ __forceinline__ void mma_f8_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                            bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(add))
+        : "memory");
+}
+
+// One arrival on the barrier at this offset in both CTAs.
+__device__ __forceinline__ void mma_commit_pair(uint64_t *bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+        " [%0], %1;" ::"r"(smem_addr(bar)),
+        "h"(uint16_t(3))
+        : "memory");
+}
+
+// Load into this CTA's shared memory that completes on a barrier of the pair.
+__device__ __forceinline__ void tma_load_2d_pair(void *dst, const CUtensorMap *map, uint32_t bar,
+                                                 int32_t c0, int32_t c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
+        : "memory");
+}
+
 // Word at the same shared address in CTA `rank` of the cluster.
 __device__ __forceinline__ float load_peer(const float *p, uint32_t rank) {
-    uint32_t a;
     float v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(peer_addr(p, rank)) : "memory");
     return v;
 }
 

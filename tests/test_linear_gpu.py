@@ -188,6 +188,30 @@ def test_product_types_and_blocks(m, ab, bb, ka, kb):
     check_product(m, 333, 1500, ka, kb, ab, bb, "f32", seed=m)
 
 
+@pytest.mark.parametrize("ab,bb", [(1, 1), (1, 128), (128, 1), (128, 128)])
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_large_product(ab, bb, kind):
+    """Tiles of 256 x 256, whole and at the edges, contractions of one block and of
+    more than the ring holds, more tiles than pairs of CTAs."""
+    check_product(2304, 2304, 128, "e4m3", "e4m3", ab, bb, kind, seed=1)
+    check_product(2304, 2304, 1536, "e5m2", "e4m3", ab, bb, kind, seed=2)
+    check_product(2435, 2311, 777, "e4m3", "e4m3", ab, bb, kind, seed=3)
+    check_product(130, 20000, 300, "e4m3", "e4m3", ab, bb, kind, seed=4)
+
+
+def test_large_product_into_a_view_and_accumulated():
+    import torch
+    m, n, k = 2310, 2300, 520
+    for kind in ("bf16", "f32"):
+        for pitch, off in [(n, 0), (n + 3, 1), (n + 4, 8)]:
+            buf = torch.full((off + m * pitch + 8,), -3.0, dtype=torch_types(kind), device="cuda")
+            view = buf[off: off + m * pitch].view(m, pitch)[:, :n]
+            check_product(m, n, k, kind=kind, seed=m, out=view)
+            check_product(m, n, k, kind=kind, seed=m + 2, out=view, accumulate=True)
+            view.fill_(-3.0)
+            assert bool((buf == -3.0).all())
+
+
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
 @pytest.mark.parametrize("m", [3, 150])
 def test_product_into_a_view_and_accumulated(m, kind):
