@@ -214,7 +214,7 @@ k_matmul_fp8(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ 
             }
             ptx::tc_fence_before();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(sums_empty + b);
+            if (lane == 0) ptx::mbar_arrive_relaxed(sums_empty + b);
         }
         // The sums go through shared memory (the stages are free: every product is
         // complete) so that lanes write neighbouring words of the output.
@@ -264,8 +264,8 @@ k_matmul_fp8(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ 
 //   warp 0     TMA of its 128 rows of P and of its half of Q
 //   warp 1     (rank 0) matrix instructions of both CTAs, 4 per stage
 //   warps 4-11 two groups of 128 threads, 128 columns each: a thread takes its row's
-//              block sums out of tensor memory, 16 columns at a time with the next
-//              16 on the way, and adds them, scaled, to 128 sums in registers
+//              block sums out of tensor memory, 32 columns at a time with the next
+//              32 on the way, and adds them, scaled, to 128 sums in registers
 //
 // QROW: Q has a scale to each row (a column of the tile): its 128 scales go through
 // shared memory; else one scale for the group's columns, and one multiplication
@@ -472,6 +472,17 @@ k_matmul_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__
             float2 acc[64];
 #pragma unroll
             for (int c = 0; c < 64; ++c) acc[c] = make_float2(0.0f, 0.0f);
+            // The sums of block i + 1 are waited for, and their first columns on
+            // the way, before the last columns of block i are added up.
+            float v[2][32];
+            auto fetch_first = [&](int buffer, uint32_t parity) {
+                // A wait that ran out is not repeated, but the meetings go on.
+                if (ok) ok = ptx::mbar_wait_bounded(sums_full + buffer, parity);
+                __syncwarp();
+                ptx::tc_fence_after();
+                ptx::tmem_load32(v[0], tsum + buffer * 256);
+            };
+            if (g.blocks > 0) fetch_first(b, phase);
             for (int i = 0; i < g.blocks; ++i) {
                 const float f = QROW ? p_now : p_now * q_now;
                 const float2 f2 = make_float2(f, f);
@@ -483,37 +494,33 @@ k_matmul_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__
                 q_now = q_next;
                 p_next = scale_p(i + 2);
                 q_next = scale_q(i + 2);
-                // A wait that ran out is not repeated, but the meetings go on.
-                if (ok) ok = ptx::mbar_wait_bounded(sums_full + b, phase);
-                __syncwarp();
-                ptx::tc_fence_after();
-                float v[2][16];
-                ptx::tmem_load16(v[0], tsum + b * 256);
+                const int at = b;
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    ptx::tmem_wait_load16(v[c & 1]);
-                    if (c < 7) {
-                        ptx::tmem_load16(v[(c + 1) & 1], tsum + b * 256 + (c + 1) * 16);
+                for (int c = 0; c < 4; ++c) {
+                    ptx::tmem_wait_load32(v[c & 1]);
+                    if (c < 3) {
+                        ptx::tmem_load32(v[(c + 1) & 1], tsum + at * 256 + (c + 1) * 32);
                     } else {  // every sum is in registers: the tensor cores may go on
                         ptx::tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive_at(release[b]);
+                        if (lane == 0) ptx::mbar_arrive_at(release[at]);
+                        b ^= 1;
+                        if (b == 0) phase ^= 1;
+                        if (i + 1 < g.blocks) fetch_first(b, phase);
                     }
 #pragma unroll
-                    for (int k = 0; k < 16; k += 4) {
+                    for (int k = 0; k < 32; k += 4) {
                         float2 f01 = f2, f23 = f2;
                         if constexpr (QROW) {
-                            const float4 q = *reinterpret_cast<const float4 *>(&scales[b][group * 128 + c * 16 + k]);
+                            const float4 q = *reinterpret_cast<const float4 *>(&scales[at][group * 128 + c * 32 + k]);
                             f01 = __fmul2_rn(f2, make_float2(q.x, q.y));
                             f23 = __fmul2_rn(f2, make_float2(q.z, q.w));
                         }
-                        float2 &a0 = acc[c * 8 + k / 2], &a1 = acc[c * 8 + k / 2 + 1];
+                        float2 &a0 = acc[c * 16 + k / 2], &a1 = acc[c * 16 + k / 2 + 1];
                         a0 = __ffma2_rn(make_float2(v[c & 1][k], v[c & 1][k + 1]), f01, a0);
                         a1 = __ffma2_rn(make_float2(v[c & 1][k + 2], v[c & 1][k + 3]), f23, a1);
                     }
                 }
-                b ^= 1;
-                if (b == 0) phase ^= 1;
             }
             store_rows(g, p0 + w * 32, q0, staging + (warp - 4) * 256,
                        [&](int j) { return j & 1 ? acc[j >> 1].y : acc[j >> 1].x; }, so);
