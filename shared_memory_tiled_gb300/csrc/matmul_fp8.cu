@@ -36,6 +36,8 @@ constexpr int kBlockK = 128;             // bytes, values and the scales' block
 constexpr int kTileP = 128;
 constexpr int kBytesP = kTileP * kBlockK;
 
+constexpr int kSumPitch = 132;           // words to a row of a tile's sums in shared memory
+
 template <int BN>
 struct Shape {
     static constexpr int kStageBytes = kBytesP + BN * kBlockK;
@@ -84,7 +86,30 @@ __device__ __forceinline__ void put(const Product &g, int64_t i, int64_t j, floa
     }
 }
 
-template <int BN, bool TURN>
+// The same for four neighbouring values on a boundary of their size together.
+__device__ __forceinline__ void put4(const Product &g, int64_t i, int64_t j, float (&v)[4], const dbg::Side &s) {
+    if (g.out_bf16) {
+        uint2 *o = reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(g.out) + i * g.ld_out + j);
+        if (!TR_STORE_OK(s, o, 8)) return;
+        if (g.accumulate) {
+            const uint2 old = *o;
+            v[0] += __uint_as_float(old.x << 16);
+            v[1] += __uint_as_float(old.x & 0xffff0000u);
+            v[2] += __uint_as_float(old.y << 16);
+            v[3] += __uint_as_float(old.y & 0xffff0000u);
+        }
+        const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+        *o = make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+    } else {
+        float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(g.out) + i * g.ld_out + j);
+        if (!TR_STORE_OK(s, o, 16)) return;
+        float4 old = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (g.accumulate) old = *o;
+        *o = make_float4(v[0] + old.x, v[1] + old.y, v[2] + old.z, v[3] + old.w);
+    }
+}
+
+template <int BN, bool TURN, bool QROW>
 __global__ void __launch_bounds__(kThreads, 2)
 k_matmul_fp8(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
              const __grid_constant__ Product g) {
@@ -128,9 +153,9 @@ k_matmul_fp8(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ 
     const int count = int(int64_t(g.blocks) * (rank + 1) / g.split) - first;
     bool ok = true;
 
-    float acc[BN];
+    float2 acc[BN / 2];
 #pragma unroll
-    for (int c = 0; c < BN; ++c) acc[c] = 0.0f;
+    for (int c = 0; c < BN / 2; ++c) acc[c] = make_float2(0.0f, 0.0f);
 
     if (warp == 0) {
         if (lane == 0) {
@@ -175,9 +200,10 @@ k_matmul_fp8(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ 
     } else {
         const int w = warp & 3;                       // the quarter of the lanes this warp may read
         const int row = w * 32 + lane, th = t - 64;   // row of P; index among the 128 threads
-        const bool has_p = p0 + row < g.p, has_q = th < BN && q0 + th < g.q;
+        const int64_t col = q0 + (QROW ? th : 0);     // whose scale this thread takes
+        const bool has_p = p0 + row < g.p, has_q = (!QROW || th < BN) && col < g.q;
         const float *sp = g.scale_p + (g.p_block == 1 ? p0 + row : (p0 + row) >> 7);
-        const float *sq = g.scale_q + (g.q_block == 1 ? q0 + th : (q0 + th) >> 7);
+        const float *sq = g.scale_q + (g.q_block == 1 ? col : col >> 7);
         [[maybe_unused]] const dbg::Side side_p = dbg::side(g.scale_p, 1, g.blocks, g.p_block == 1 ? g.p : (g.p + 127) / 128, g.ld_p, 0, 4);
         [[maybe_unused]] const dbg::Side side_q = dbg::side(g.scale_q, 1, g.blocks, g.q_block == 1 ? g.q : (g.q + 127) / 128, g.ld_q, 0, 4);
         auto scale = [](const float *p, bool has, [[maybe_unused]] const dbg::Side &s) {
@@ -187,41 +213,60 @@ k_matmul_fp8(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ 
         float next_q = scale(sq + first * g.ld_q, has_q && count > 0, side_q);
         for (int i = 0; i < count; ++i) {
             const int b = i & 1;
-            const float mine = next_p;
-            if (th < BN) scales[b][th] = next_q;
+            const float f = QROW ? next_p : next_p * next_q;
+            const float2 f2 = make_float2(f, f);
+            if (QROW && th < BN) scales[b][th] = next_q;
             if (i + 1 < count) {
                 next_p = scale(sp + (first + i + 1) * g.ld_p, has_p, side_p);
                 next_q = scale(sq + (first + i + 1) * g.ld_q, has_q, side_q);
             }
-            ptx::named_sync(1, 128);
+            if (QROW) ptx::named_sync(1, 128);
             // A wait that ran out is not repeated, but the meetings go on.
             if (ok) ok = ptx::mbar_wait_bounded(sums_full + b, (i >> 1) & 1);
-            ptx::tc_fence_after();
             __syncwarp();
+            ptx::tc_fence_after();
+            const uint32_t from = tmem + (uint32_t(w * 32) << 16) + b * BN;
+            float v[2][16];
+            ptx::tmem_load16(v[0], from);
 #pragma unroll
-            for (int c = 0; c < BN; c += 16) {
-                float v[16];
-                ptx::tmem_load16(v, tmem + (uint32_t(w * 32) << 16) + b * BN + c);
-                ptx::tmem_wait_load16(v);
+            for (int c = 0; c < BN / 16; ++c) {
+                ptx::tmem_wait_load16(v[c & 1]);
+                if (c + 1 < BN / 16) {
+                    ptx::tmem_load16(v[(c + 1) & 1], from + (c + 1) * 16);
+                } else {  // every sum is in registers: the tensor cores may go on
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive_relaxed(sums_empty + b);
+                }
 #pragma unroll
                 for (int k = 0; k < 16; k += 4) {
-                    const float4 f = *reinterpret_cast<const float4 *>(&scales[b][c + k]);
-                    acc[c + k] = fmaf(v[k], mine * f.x, acc[c + k]);
-                    acc[c + k + 1] = fmaf(v[k + 1], mine * f.y, acc[c + k + 1]);
-                    acc[c + k + 2] = fmaf(v[k + 2], mine * f.z, acc[c + k + 2]);
-                    acc[c + k + 3] = fmaf(v[k + 3], mine * f.w, acc[c + k + 3]);
+                    float2 f01 = f2, f23 = f2;
+                    if constexpr (QROW) {
+                        const float4 q = *reinterpret_cast<const float4 *>(&scales[b][c * 16 + k]);
+                        f01 = __fmul2_rn(f2, make_float2(q.x, q.y));
+                        f23 = __fmul2_rn(f2, make_float2(q.z, q.w));
+                    }
+                    float2 &a0 = acc[c * 8 + k / 2], &a1 = acc[c * 8 + k / 2 + 1];
+                    a0 = __ffma2_rn(make_float2(v[c & 1][k], v[c & 1][k + 1]), f01, a0);
+                    a1 = __ffma2_rn(make_float2(v[c & 1][k + 2], v[c & 1][k + 3]), f23, a1);
                 }
             }
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive_relaxed(sums_empty + b);
         }
         // The sums go through shared memory (the stages are free: every product is
         // complete) so that lanes write neighbouring words of the output.
         float *red = reinterpret_cast<float *>(stages);
+        if constexpr (TURN) {
 #pragma unroll
-        for (int c = 0; c < BN; ++c)
-            red[TURN ? c * 128 + row : row * (BN + 1) + c] = acc[c];
+            for (int c = 0; c < BN / 2; ++c) {
+                red[2 * c * 128 + row] = acc[c].x;
+                red[(2 * c + 1) * 128 + row] = acc[c].y;
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < BN / 4; ++c)
+                *reinterpret_cast<float4 *>(red + row * kSumPitch + 4 * c) =
+                    make_float4(acc[2 * c].x, acc[2 * c].y, acc[2 * c + 1].x, acc[2 * c + 1].y);
+        }
     }
     if (!ok) atomicExch(&g_fault_flag_matmul, 1u);
     __syncwarp();
@@ -232,20 +277,36 @@ k_matmul_fp8(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ 
         float *red = reinterpret_cast<float *>(stages);
         const int th = t - 64;
         [[maybe_unused]] const dbg::Side so = dbg::side(g.out, 1, TURN ? g.q : g.p, TURN ? g.p : g.q, g.ld_out, 0, g.out_bf16 ? 2 : 4);
-        auto total = [&](const float *p) {
-            if (g.split == 1) return *p;
-            float v = 0.0f;
-            for (int r = 0; r < g.split; ++r) v += ptx::load_peer(p, uint32_t(r));
-            return v;
-        };
         if constexpr (TURN) {
             if (p0 + th < g.p)
-                for (int c = rank; c < BN && q0 + c < g.q; c += g.split)
-                    put(g, q0 + c, p0 + th, total(red + c * 128 + th), so);
+                for (int c = rank; c < BN && q0 + c < g.q; c += g.split) {
+                    float v = 0.0f;
+                    for (int r = 0; r < g.split; ++r) v += ptx::load_peer(red + c * 128 + th, uint32_t(r));
+                    put(g, q0 + c, p0 + th, v, so);
+                }
         } else {
-            for (int r = rank * 4 + (th >> 5); r < 128 && p0 + r < g.p; r += g.split * 4)
-                for (int c = lane; c < BN && q0 + c < g.q; c += 32)
-                    put(g, p0 + r, q0 + c, total(red + r * (BN + 1) + c), so);
+            // A warp takes a row at a time: 4 neighbouring columns to a lane where they
+            // can be stored at once, else every 32nd.
+            const int es = g.out_bf16 ? 2 : 4;
+            const bool whole = q0 + BN <= g.q && g.ld_out % 4 == 0 && reinterpret_cast<uintptr_t>(g.out) % (4 * es) == 0;
+            const int rows = 32 / g.split;
+#pragma unroll 4
+            for (int i = 0; i < rows; ++i) {
+                const int r = (i * g.split + rank) * 4 + (th >> 5);
+                float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                for (int peer = 0; peer < g.split; ++peer)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        v[k] += ptx::load_peer(red + r * kSumPitch + (whole ? lane * 4 + k : lane + k * 32), uint32_t(peer));
+                if (p0 + r >= g.p) continue;
+                if (whole) {
+                    put4(g, p0 + r, q0 + lane * 4, v, so);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (q0 + lane + k * 32 < g.q) put(g, p0 + r, q0 + lane + k * 32, v[k], so);
+                }
+            }
         }
     }
     if (g.split > 1) ptx::cluster_sync();  // no block leaves while another reads its sums
@@ -275,6 +336,7 @@ constexpr int kPairThreads = 384;
 // Registers at launch (168 x 384 = 64512), and how the warpgroups share them:
 // 56 x 128 + 224 x 256 = 64512.
 constexpr int kFewRegisters = 56, kManyRegisters = 224;
+constexpr int kScaleSlots = 4;
 constexpr int kPairTile = 256;
 constexpr int kPairStages = 5;
 constexpr int kPairStageBytes = 2 * kBytesP;       // 128 rows of P and 128 of Q
@@ -351,8 +413,9 @@ k_matmul_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__
               const __grid_constant__ Product g) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t full[kPairStages], empty[kPairStages], sums_full[2], sums_empty[2];
+    __shared__ uint64_t scales_full[kScaleSlots], scales_empty[kScaleSlots];
     __shared__ uint32_t tmem_base;
-    __shared__ alignas(16) float scales[2][QROW ? 256 : 4];
+    __shared__ alignas(16) float scales_p[kScaleSlots][128], scales_q[kScaleSlots][QROW ? 256 : 4];
     uint8_t *stages = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint4 *staging = reinterpret_cast<uint4 *>(stages + kPairStages * kPairStageBytes);
@@ -369,6 +432,10 @@ k_matmul_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(sums_full + i, 1);
             ptx::mbar_init(sums_empty + i, 16);  // the warps of both CTAs
+        }
+        for (int i = 0; i < kScaleSlots; ++i) {
+            ptx::mbar_init(scales_full + i, 2);   // those of P and of Q
+            ptx::mbar_init(scales_empty + i, 8);  // this CTA's warps
         }
         ptx::fence_barrier_init();
     }
@@ -420,99 +487,119 @@ k_matmul_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__
             const uint32_t idesc = ptx::f8_idesc(g.p_e5m2, g.q_e5m2, 256, 256);
             int s = 0, b = 0;
             uint32_t phase = 0, sums_phase = 1;
+            bool ready = false;  // the next block's operands and sums were seen ready
             for (int64_t tile = pair; tile < tiles && ok; tile += pairs)
                 for (int i = 0; i < g.blocks; ++i) {
-                    ok = ptx::mbar_wait_bounded(full + s, phase) && ptx::mbar_wait_bounded(sums_empty + b, sums_phase);
+                    if (!ready)
+                        ok = ptx::mbar_wait_bounded(full + s, phase) && ptx::mbar_wait_bounded(sums_empty + b, sums_phase);
                     if (!ok) break;
                     ptx::tc_fence_after();
                     const uint32_t at = ptx::smem_addr(stages + s * kPairStageBytes);
                     const uint64_t dp = ptx::operand_desc(at), dq = ptx::operand_desc(at + kBytesP);
-#pragma unroll
-                    for (int k = 0; k < kBlockK / 32; ++k)
-                        ptx::mma_f8_pair(tmem + b * 256, dp + 2 * k, dq + 2 * k, idesc, k > 0);
-                    ptx::mma_commit_pair(empty + s);
-                    ptx::mma_commit_pair(sums_full + b);
+                    const int used = s, into = b;
                     if (++s == kPairStages) {
                         s = 0;
                         phase ^= 1;
                     }
                     b ^= 1;
                     if (b == 0) sums_phase ^= 1;
+#pragma unroll
+                    for (int k = 0; k < kBlockK / 32; ++k) {
+                        ptx::mma_f8_pair(tmem + into * 256, dp + 2 * k, dq + 2 * k, idesc, k > 0);
+                        // A look at a barrier costs this thread about 100 cycles:
+                        // taken here, while the tensor cores are busy.
+                        
+                    }
+                    ptx::mma_commit_pair(sums_full + into);
+                    ptx::mma_commit_pair(empty + used);
                 }
+        }
+      } else {
+        // Scales, three blocks ahead: warp 2 those of P, warp 3 those of Q.
+        const bool of_p = warp == 2;
+        const float *base = of_p ? g.scale_p : g.scale_q;
+        const int64_t ld = of_p ? g.ld_p : g.ld_q, rows = of_p ? g.p : g.q;
+        const int shift = (of_p ? g.p_block : g.q_block) == 1 ? 0 : 7;  // 2^shift rows to a scale
+        // Scales to take, and the tile's rows from one to the next (block scales of P
+        // are taken once for each row, those of Q once for each 128 columns).
+        const int count = of_p ? 128 : QROW ? 256 : 2, apart = of_p || QROW ? 1 : 128;
+        [[maybe_unused]] const dbg::Side side = dbg::side(base, 1, g.blocks, (rows + (1 << shift) - 1) >> shift, ld, 0, 4);
+        float *ring = of_p ? &scales_p[0][0] : &scales_q[0][0];
+        const int pitch = of_p ? 128 : QROW ? 256 : 4;
+        // Blocks are counted through all tiles of this pair; the copies' cursor
+        // runs kScaleSlots - 1 ahead.
+        const int64_t mine = pair < tiles ? (tiles - 1 - pair) / pairs + 1 : 0, blocks = mine * g.blocks;
+        int64_t tile = pair, r0 = 0;
+        int at = 0;  // the cursor's block of its tile
+        for (int64_t n = -(kScaleSlots - 1); n < blocks; ++n) {
+            if (n >= 0) {
+                ptx::cp_async_wait<kScaleSlots - 2>();  // block n's are here
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(scales_full + n % kScaleSlots);
+            }
+            const int64_t ahead = n + kScaleSlots - 1;
+            if (ahead < blocks) {
+                if (ok && n >= 1) ok = ptx::mbar_wait_bounded(scales_empty + (n - 1) % kScaleSlots, (n - 1) / kScaleSlots & 1);
+                if (at == 0) {
+                    int64_t p0, q0;
+                    tile_at(g, tile, kPairTile, kPairTile, 8, &p0, &q0);
+                    r0 = of_p ? p0 + rank * 128 : q0;
+                }
+                for (int k = lane; k < count; k += 32) {
+                    const int64_t r = r0 + k * apart;
+                    const float *p = base + at * ld + (r >> shift);
+                    ptx::cp_async_4_or_zero(ring + ahead % kScaleSlots * pitch + k, r < rows ? p : base,
+                                            r < rows && TR_LOAD_OK(side, p, 4));
+                }
+                if (++at == g.blocks) {
+                    at = 0;
+                    tile += pairs;
+                }
+            }
+            ptx::cp_async_commit();
         }
       }
     } else {
         ptx::registers_up<kManyRegisters>();
-        const int w = warp & 3, group = (warp - 4) >> 2, th = t & 127;
+        const int w = warp & 3, group = (warp - 4) >> 2, r = w * 32 + lane;
         const uint32_t tsum = tmem + (uint32_t(w * 32) << 16) + group * 128;
         const uint32_t release[2] = {ptx::peer_addr(sums_empty, 0), ptx::peer_addr(sums_empty + 1, 0)};
-        [[maybe_unused]] const dbg::Side side_p = dbg::side(g.scale_p, 1, g.blocks, g.p_block == 1 ? g.p : (g.p + 127) / 128, g.ld_p, 0, 4);
-        [[maybe_unused]] const dbg::Side side_q = dbg::side(g.scale_q, 1, g.blocks, g.q_block == 1 ? g.q : (g.q + 127) / 128, g.ld_q, 0, 4);
         [[maybe_unused]] const dbg::Side so = dbg::side(g.out, 1, g.p, g.q, g.ld_out, 0, g.out_bf16 ? 2 : 4);
-        int b = 0;
-        uint32_t phase = 0;
+        int b = 0, slot = 0;
+        uint32_t phase = 0, slot_phase = 0;
         for (int64_t tile = pair; tile < tiles; tile += pairs) {
             int64_t p0, q0;
             tile_at(g, tile, kPairTile, kPairTile, 8, &p0, &q0);
             p0 += rank * 128;
             q0 += group * 128;
-            const int64_t row = p0 + w * 32 + lane, col = q0 + (QROW ? th : 0);
-            const float *sp = g.scale_p + (g.p_block == 1 ? row : row >> 7);
-            const float *sq = g.scale_q + (g.q_block == 1 ? col : col >> 7);
-            // Scales two blocks ahead: a block takes about as long as a read from L2.
-            auto scale_p = [&](int i) {
-                const float *p = sp + i * g.ld_p;
-                return i < g.blocks && row < g.p && TR_LOAD_OK(side_p, p, 4) ? *p : 0.0f;
-            };
-            auto scale_q = [&](int i) {
-                const float *p = sq + i * g.ld_q;
-                return i < g.blocks && col < g.q && TR_LOAD_OK(side_q, p, 4) ? *p : 0.0f;
-            };
-            float p_now = scale_p(0), p_next = scale_p(1), q_now = scale_q(0), q_next = scale_q(1);
             float2 acc[64];
 #pragma unroll
             for (int c = 0; c < 64; ++c) acc[c] = make_float2(0.0f, 0.0f);
-            // The sums of block i + 1 are waited for, and their first columns on
-            // the way, before the last columns of block i are added up.
             float v[2][32];
-            auto fetch_first = [&](int buffer, uint32_t parity) {
-                // A wait that ran out is not repeated, but the meetings go on.
-                if (ok) ok = ptx::mbar_wait_bounded(sums_full + buffer, parity);
+            for (int i = 0; i < g.blocks; ++i) {
+                // A wait that ran out is not repeated, but the arrivals go on.
+                if (ok) ok = ptx::mbar_wait_bounded(scales_full + slot, slot_phase);
+                const float f = QROW ? scales_p[slot][r] : scales_p[slot][r] * scales_q[slot][group];
+                const float2 f2 = make_float2(f, f);
+                if (ok) ok = ptx::mbar_wait_bounded(sums_full + b, phase);
                 __syncwarp();
                 ptx::tc_fence_after();
-                ptx::tmem_load32(v[0], tsum + buffer * 256);
-            };
-            if (g.blocks > 0) fetch_first(b, phase);
-            for (int i = 0; i < g.blocks; ++i) {
-                const float f = QROW ? p_now : p_now * q_now;
-                const float2 f2 = make_float2(f, f);
-                if constexpr (QROW) {
-                    scales[b][group * 128 + th] = q_now;
-                    ptx::named_sync(1 + group, 128);
-                }
-                p_now = p_next;
-                q_now = q_next;
-                p_next = scale_p(i + 2);
-                q_next = scale_q(i + 2);
-                const int at = b;
+                ptx::tmem_load32(v[0], tsum + b * 256);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     ptx::tmem_wait_load32(v[c & 1]);
                     if (c < 3) {
-                        ptx::tmem_load32(v[(c + 1) & 1], tsum + at * 256 + (c + 1) * 32);
+                        ptx::tmem_load32(v[(c + 1) & 1], tsum + b * 256 + (c + 1) * 32);
                     } else {  // every sum is in registers: the tensor cores may go on
                         ptx::tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive_at(release[at]);
-                        b ^= 1;
-                        if (b == 0) phase ^= 1;
-                        if (i + 1 < g.blocks) fetch_first(b, phase);
+                        if (lane == 0) ptx::mbar_arrive_at(release[b]);
                     }
 #pragma unroll
                     for (int k = 0; k < 32; k += 4) {
                         float2 f01 = f2, f23 = f2;
                         if constexpr (QROW) {
-                            const float4 q = *reinterpret_cast<const float4 *>(&scales[at][group * 128 + c * 32 + k]);
+                            const float4 q = *reinterpret_cast<const float4 *>(&scales_q[slot][group * 128 + c * 32 + k]);
                             f01 = __fmul2_rn(f2, make_float2(q.x, q.y));
                             f23 = __fmul2_rn(f2, make_float2(q.z, q.w));
                         }
@@ -521,6 +608,14 @@ k_matmul_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__
                         a1 = __ffma2_rn(make_float2(v[c & 1][k + 2], v[c & 1][k + 3]), f23, a1);
                     }
                 }
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive_relaxed(scales_empty + slot);
+                if (++slot == kScaleSlots) {
+                    slot = 0;
+                    slot_phase ^= 1;
+                }
+                b ^= 1;
+                if (b == 0) phase ^= 1;
             }
             store_rows(g, p0 + w * 32, q0, staging + (warp - 4) * 256,
                        [&](int j) { return j & 1 ? acc[j >> 1].y : acc[j >> 1].x; }, so);
@@ -582,11 +677,11 @@ cudaError_t launch_kernel(K kern, std::atomic<bool> *opted, int64_t grid, int th
     return e;
 }
 
-template <int BN, bool TURN>
+template <int BN, bool TURN, bool QROW>
 cudaError_t launch_shape(const CUtensorMap &map_p, const CUtensorMap &map_q, const Product &g,
                          cudaStream_t stream) {
     static std::atomic<bool> opted[64];  // per device, zero-initialised (static)
-    return launch_kernel(k_matmul_fp8<BN, TURN>, opted, g.tiles_p * g.tiles_q * g.split, kThreads,
+    return launch_kernel(k_matmul_fp8<BN, TURN, QROW>, opted, g.tiles_p * g.tiles_q * g.split, kThreads,
                          Shape<BN>::kSmem, g.split, map_p, map_q, g, stream);
 }
 
@@ -659,10 +754,14 @@ cudaError_t launch_matmul_fp8(const tr_matmul_fp8_args &a, const char **why) {
     }
     if (pair)
         return g.q_block == 1 ? launch_pair<true>(map_a, map_b, g, stream) : launch_pair<false>(map_a, map_b, g, stream);
-    if (!turn) return launch_shape<128, false>(map_a, map_b, g, stream);
-    if (bn == 16) return launch_shape<16, true>(map_b, map_a, g, stream);
-    if (bn == 32) return launch_shape<32, true>(map_b, map_a, g, stream);
-    return launch_shape<64, true>(map_b, map_a, g, stream);
+#define TR_SHAPE(BN, TURN, P, Q)                                                   \
+    return g.q_block == 1 ? launch_shape<BN, TURN, true>(P, Q, g, stream)          \
+                          : launch_shape<BN, TURN, false>(P, Q, g, stream)
+    if (!turn) TR_SHAPE(128, false, map_a, map_b);
+    if (bn == 16) TR_SHAPE(16, true, map_b, map_a);
+    if (bn == 32) TR_SHAPE(32, true, map_b, map_a);
+    TR_SHAPE(64, true, map_b, map_a);
+#undef TR_SHAPE
 }
 
 }  // namespace tr
