@@ -36,13 +36,18 @@ constexpr int kBlockK = 128;             // bytes, values and the scales' block
 constexpr int kTileP = 128;
 constexpr int kBytesP = kTileP * kBlockK;
 
+constexpr int kScaleSlots = 4;          // blocks whose scales are in shared memory
 constexpr int kSumPitch = 132;           // words to a row of a tile's sums in shared memory
 
 template <int BN>
 struct Shape {
     static constexpr int kStageBytes = kBytesP + BN * kBlockK;
-    static constexpr int kStages = BN == 128 ? 3 : BN == 64 ? 4 : 5;
-    static constexpr int kColumns = BN < 16 ? 32 : 2 * BN;  // two buffers of sums
+    // A tile of 16 columns is bound by P's bytes: four CTAs to an SM with 2 stages each
+    // beat two with 5 (1 x 8192 x 8192: 14.5 against 16.1 us), since one's first
+    // loads and last sums run beside the others' streams.
+    static constexpr int kPerSm = BN == 16 ? 4 : 2;
+    static constexpr int kStages = BN == 16 ? 2 : BN == 128 ? 3 : BN == 64 ? 4 : 5;
+    static constexpr int kColumns = 2 * BN;  // two buffers of sums
     static constexpr size_t kSmem = 1024 + size_t(kStages) * kStageBytes;
 };
 
@@ -109,15 +114,99 @@ __device__ __forceinline__ void put4(const Product &g, int64_t i, int64_t j, flo
     }
 }
 
+// Adds up the sums of a tile that SPLIT CTAs left in shared memory, in rank order, and
+// writes this CTA's share of the tile.  Eight loads go out before the first is
+// used: one from another CTA takes some 450 cycles (one at a time they were
+// three quarters of a 2048^3 product).
+template <int BN, bool TURN, int SPLIT>
+__device__ __forceinline__ void store_tile(const Product &g, const float *red, int64_t p0, int64_t q0, int rank,
+                                           int th, const dbg::Side &s) {
+    uint32_t base[SPLIT];
+#pragma unroll
+    for (int peer = 0; peer < SPLIT; ++peer) base[peer] = ptx::peer_addr(red, uint32_t(SPLIT == 1 ? rank : peer));
+    if constexpr (TURN) {
+        // Threads along the rows of P (neighbouring columns of the output), 8 / SPLIT
+        // rows of the output at a time.
+        constexpr int U = 8 / SPLIT;
+        for (int c0 = rank; c0 < BN && q0 + c0 < g.q; c0 += SPLIT * U) {
+            float v[U][SPLIT];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int peer = 0; peer < SPLIT; ++peer)
+                    v[u][peer] = ptx::load_cluster(base[peer] + 4 * ((c0 + u * SPLIT) % BN * 128 + th));
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int c = c0 + u * SPLIT;
+#pragma unroll
+                for (int peer = 1; peer < SPLIT; ++peer) v[u][0] += v[u][peer];
+                if (c < BN && q0 + c < g.q && p0 + th < g.p) put(g, q0 + c, p0 + th, v[u][0], s);
+            }
+        }
+    } else {
+        // A warp takes rows of the tile: 4 neighbouring columns to a lane where they can
+        // be stored at once, else every 32nd.
+        constexpr int ROWS = 32 / SPLIT, U = ROWS < 8 ? ROWS : 8, PEERS = 8 / U;
+        const int lane = th & 31, es = g.out_bf16 ? 2 : 4;
+        const bool whole = q0 + BN <= g.q && g.ld_out % 4 == 0 && reinterpret_cast<uintptr_t>(g.out) % (4 * es) == 0;
+#pragma unroll 1
+        for (int i = 0; i < ROWS; i += U) {
+            auto row = [&](int u) { return ((i + u) * SPLIT + rank) * 4 + (th >> 5); };
+            float v[U][4] = {};
+#pragma unroll
+            for (int peer = 0; peer < SPLIT; peer += PEERS) {
+                float4 t[PEERS][U];
+#pragma unroll
+                for (int k = 0; k < PEERS; ++k)
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const uint32_t at = base[peer + k] + 4 * (row(u) * kSumPitch);
+                        if (whole) {
+                            t[k][u] = ptx::load_cluster4(at + 16 * lane);
+                        } else {
+                            t[k][u].x = ptx::load_cluster(at + 4 * lane);
+                            t[k][u].y = ptx::load_cluster(at + 4 * lane + 128);
+                            t[k][u].z = ptx::load_cluster(at + 4 * lane + 256);
+                            t[k][u].w = ptx::load_cluster(at + 4 * lane + 384);
+                        }
+                    }
+#pragma unroll
+                for (int k = 0; k < PEERS; ++k)
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        v[u][0] += t[k][u].x;
+                        v[u][1] += t[k][u].y;
+                        v[u][2] += t[k][u].z;
+                        v[u][3] += t[k][u].w;
+                    }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t r = p0 + row(u);
+                if (r >= g.p) continue;
+                if (whole) {
+                    put4(g, r, q0 + lane * 4, v[u], s);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (q0 + lane + k * 32 < g.q) put(g, r, q0 + lane + k * 32, v[u][k], s);
+                }
+            }
+        }
+    }
+}
+
 template <int BN, bool TURN, bool QROW>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, Shape<BN>::kPerSm)
 k_matmul_fp8(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
              const __grid_constant__ Product g) {
     using S = Shape<BN>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t full[S::kStages], empty[S::kStages], sums_full[2], sums_empty[2], drained;
     __shared__ uint32_t tmem_base;
-    __shared__ alignas(16) float scales[2][BN];
+    // Scales, three blocks ahead: each of the 128 threads copies its row's of P and one
+    // of Q (QROW: a column's; else all the same one, each its own copy).
+    __shared__ alignas(16) float scales_p[kScaleSlots][128], scales_q[kScaleSlots][128];
     uint8_t *stages = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
@@ -206,21 +295,21 @@ k_matmul_fp8(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ 
         const float *sq = g.scale_q + (g.q_block == 1 ? col : col >> 7);
         [[maybe_unused]] const dbg::Side side_p = dbg::side(g.scale_p, 1, g.blocks, g.p_block == 1 ? g.p : (g.p + 127) / 128, g.ld_p, 0, 4);
         [[maybe_unused]] const dbg::Side side_q = dbg::side(g.scale_q, 1, g.blocks, g.q_block == 1 ? g.q : (g.q + 127) / 128, g.ld_q, 0, 4);
-        auto scale = [](const float *p, bool has, [[maybe_unused]] const dbg::Side &s) {
-            return has && TR_LOAD_OK(s, p, 4) ? *p : 0.0f;
+        auto copy_scales = [&](int i) {
+            const float *p = sp + int64_t(first + i) * g.ld_p, *q = sq + int64_t(first + i) * g.ld_q;
+            const bool now = i < count;
+            ptx::cp_async_4_or_zero(&scales_p[i % kScaleSlots][th], now && has_p ? p : g.scale_p, now && has_p && TR_LOAD_OK(side_p, p, 4));
+            ptx::cp_async_4_or_zero(&scales_q[i % kScaleSlots][th], now && has_q ? q : g.scale_q, now && has_q && TR_LOAD_OK(side_q, q, 4));
+            ptx::cp_async_commit();
         };
-        float next_p = scale(sp + first * g.ld_p, has_p && count > 0, side_p);
-        float next_q = scale(sq + first * g.ld_q, has_q && count > 0, side_q);
+        for (int i = 0; i < kScaleSlots - 1; ++i) copy_scales(i);
         for (int i = 0; i < count; ++i) {
-            const int b = i & 1;
-            const float f = QROW ? next_p : next_p * next_q;
+            const int b = i & 1, slot = i % kScaleSlots;
+            ptx::cp_async_wait<kScaleSlots - 2>();  // this thread's copies for block i are here
+            if (QROW) ptx::named_sync(1, 128);      // and everybody's; block i - 1's are read
+            const float f = QROW ? scales_p[slot][th] : scales_p[slot][th] * scales_q[slot][th];
             const float2 f2 = make_float2(f, f);
-            if (QROW && th < BN) scales[b][th] = next_q;
-            if (i + 1 < count) {
-                next_p = scale(sp + (first + i + 1) * g.ld_p, has_p, side_p);
-                next_q = scale(sq + (first + i + 1) * g.ld_q, has_q, side_q);
-            }
-            if (QROW) ptx::named_sync(1, 128);
+            copy_scales(i + kScaleSlots - 1);
             // A wait that ran out is not repeated, but the meetings go on.
             if (ok) ok = ptx::mbar_wait_bounded(sums_full + b, (i >> 1) & 1);
             __syncwarp();
@@ -242,7 +331,7 @@ k_matmul_fp8(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ 
                 for (int k = 0; k < 16; k += 4) {
                     float2 f01 = f2, f23 = f2;
                     if constexpr (QROW) {
-                        const float4 q = *reinterpret_cast<const float4 *>(&scales[b][c * 16 + k]);
+                        const float4 q = *reinterpret_cast<const float4 *>(&scales_q[slot][c * 16 + k]);
                         f01 = __fmul2_rn(f2, make_float2(q.x, q.y));
                         f23 = __fmul2_rn(f2, make_float2(q.z, q.w));
                     }
@@ -274,39 +363,14 @@ k_matmul_fp8(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ 
     __syncthreads();
     if (g.split > 1) ptx::cluster_sync();
     if (warp >= 2) {
-        float *red = reinterpret_cast<float *>(stages);
         const int th = t - 64;
         [[maybe_unused]] const dbg::Side so = dbg::side(g.out, 1, TURN ? g.q : g.p, TURN ? g.p : g.q, g.ld_out, 0, g.out_bf16 ? 2 : 4);
-        if constexpr (TURN) {
-            if (p0 + th < g.p)
-                for (int c = rank; c < BN && q0 + c < g.q; c += g.split) {
-                    float v = 0.0f;
-                    for (int r = 0; r < g.split; ++r) v += ptx::load_peer(red + c * 128 + th, uint32_t(r));
-                    put(g, q0 + c, p0 + th, v, so);
-                }
-        } else {
-            // A warp takes a row at a time: 4 neighbouring columns to a lane where they
-            // can be stored at once, else every 32nd.
-            const int es = g.out_bf16 ? 2 : 4;
-            const bool whole = q0 + BN <= g.q && g.ld_out % 4 == 0 && reinterpret_cast<uintptr_t>(g.out) % (4 * es) == 0;
-            const int rows = 32 / g.split;
-#pragma unroll 4
-            for (int i = 0; i < rows; ++i) {
-                const int r = (i * g.split + rank) * 4 + (th >> 5);
-                float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                for (int peer = 0; peer < g.split; ++peer)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        v[k] += ptx::load_peer(red + r * kSumPitch + (whole ? lane * 4 + k : lane + k * 32), uint32_t(peer));
-                if (p0 + r >= g.p) continue;
-                if (whole) {
-                    put4(g, p0 + r, q0 + lane * 4, v, so);
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (q0 + lane + k * 32 < g.q) put(g, p0 + r, q0 + lane + k * 32, v[k], so);
-                }
-            }
+        const float *red = reinterpret_cast<const float *>(stages);
+        switch (g.split) {
+            case 1: store_tile<BN, TURN, 1>(g, red, p0, q0, rank, th, so); break;
+            case 2: store_tile<BN, TURN, 2>(g, red, p0, q0, rank, th, so); break;
+            case 4: store_tile<BN, TURN, 4>(g, red, p0, q0, rank, th, so); break;
+            default: store_tile<BN, TURN, 8>(g, red, p0, q0, rank, th, so); break;
         }
     }
     if (g.split > 1) ptx::cluster_sync();  // no block leaves while another reads its sums
@@ -336,7 +400,6 @@ constexpr int kPairThreads = 384;
 // Registers at launch (168 x 384 = 64512), and how the warpgroups share them:
 // 56 x 128 + 224 x 256 = 64512.
 constexpr int kFewRegisters = 56, kManyRegisters = 224;
-constexpr int kScaleSlots = 4;
 constexpr int kPairTile = 256;
 constexpr int kPairStages = 5;
 constexpr int kPairStageBytes = 2 * kBytesP;       // 128 rows of P and 128 of Q
@@ -716,7 +779,10 @@ cudaError_t launch_matmul_fp8(const tr_matmul_fp8_args &a, const char **why) {
     }
     // Up to 64 rows of a: they are the columns of the tile, and b its 128 rows.
     const bool turn = a.m <= 64;
-    const bool pair = !turn && ((a.m + 255) / 256) * ((a.n + 255) / 256) >= sm_count() / 2;
+// 256 x 256 tiles where they occupy five eighths of the CTA pairs: 1536 x 2048 x 8192
+    // (48 tiles) takes 38.8 us on them and 44.2 on 128 x 128 tiles, 777 x 2049 x 1111
+    // (36 tiles) 15.7 and 12.9.
+    const bool pair = !turn && ((a.m + 255) / 256) * ((a.n + 255) / 256) * 8 >= int64_t(sm_count() / 2) * 5;
     const int bn = pair ? 256 : !turn ? 128 : a.m <= 16 ? 16 : a.m <= 32 ? 32 : 64;
     Product g{};
     g.scale_p = turn ? a.scale_b : a.scale_a;
@@ -736,11 +802,11 @@ cudaError_t launch_matmul_fp8(const tr_matmul_fp8_args &a, const char **why) {
     g.q_e5m2 = (turn ? a.a_dtype : a.b_dtype) == TR_DTYPE_E5M2;
     g.out_bf16 = out_bf16;
     g.accumulate = a.accumulate;
-    // Split the contraction until the tiles fill two CTAs to each SM, each CTA
-    // keeping four blocks or more.
-    const int64_t tiles = g.tiles_p * g.tiles_q;
+    // Split the contraction until the tiles fill what is resident at one time, each
+    // CTA keeping four blocks or more.
+    const int64_t tiles = g.tiles_p * g.tiles_q, resident = int64_t(sm_count()) * (bn == 16 ? Shape<16>::kPerSm : 2);
     g.split = 1;
-    while (!pair && g.split < 8 && tiles * g.split * 2 <= int64_t(sm_count()) * 2 && g.blocks >= g.split * 8)
+    while (!pair && g.split < 8 && tiles * g.split * 2 <= resident && g.blocks >= g.split * 8)
         g.split *= 2;
     if (tiles * g.split > 0x7fffffffll) {
         *why = "matmul: too many tiles for one launch";
