@@ -5,6 +5,8 @@
 namespace tr {
 namespace {
 
+constexpr int kMostRowChunks = 2049;  // of a row whose weights are kept in shared memory, one for the shift
+
 struct Fwd {
     const void *x, *gamma, *beta;
     void *y;
@@ -268,7 +270,8 @@ template <typename K>
 cudaError_t launch_rows(K kern, int threads, int v, const Fwd &a, bool edge, cudaStream_t stream) {
     const int64_t chunks = (a.cols + v - 1) / v + (edge ? 1 : 0);
     const size_t smem = size_t(chunks) * v * 4 * (a.beta ? 2 : 1);
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    // Always the most that any call needs: threads with rows of other lengths set it too.
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostRowChunks * 8 * 4 * 2);
     if (e != cudaSuccess) return e;
     return launch_pdl(kern, dim3(unsigned(sm_count())), dim3(threads), smem, stream, a);
 }
@@ -294,7 +297,7 @@ cudaError_t launch_typed(const tr_layernorm_args &p) {
     if (!alike) return run(k_layernorm_long<T, 1>, 1024, 1);
     const int64_t chunks = (a.cols + (shifted ? V - 1 : 0) + V - 1) / V;
     // Rows for every group of every resident block: the weights' copy pays.
-    if (a.rows >= int64_t(sm_count()) * 32 && chunks <= 2048) {
+    if (a.rows >= int64_t(sm_count()) * 32 && chunks < kMostRowChunks) {
 #define TR_ROWS(G, NCH, BLOCK)                                                            \
     if (chunks <= G * NCH)                                                                \
         return edge ? launch_rows(k_layernorm_rows<T, V, G, NCH, true>, BLOCK, V, a, true, stream) \

@@ -116,14 +116,20 @@ k_ln_backward(const Bwd a, int stages, uint32_t row_bytes) {
             issue(blockIdx.x + int64_t(i) * gridDim.x, i);
     // Column of the thread's value e.
     auto column = [&](int e) { return (t + e / V * nt) * V + e % V; };
-    // Its pair k of a row in shared memory, zeros past the row's end.
-    auto pair = [&](const T *p, int k) {
+    // Piece i of its values of a row in shared memory (a chunk, or two single columns),
+    // zeros past the row's end.
+    constexpr int Q = V < 2 ? 1 : V / 2;  // pairs to a piece
+    auto piece = [&](const T *p, int i, float2 (&v)[Q]) {
         if constexpr (VEC) {
-            if (column(2 * k) >= cols) return make_float2(0.0f, 0.0f);
-            return reinterpret_cast<const Pack<T, V> *>(p + column(2 * k / V * V))->pair(k % (V / 2));
+            const int j = column(i * V);
+            uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+            if (j < cols) raw = *reinterpret_cast<const uint4 *>(p + j);
+            const Pack<T, V> &c = *reinterpret_cast<const Pack<T, V> *>(&raw);
+#pragma unroll
+            for (int q = 0; q < Q; ++q) v[q] = make_float2(c.get(2 * q), c.get(2 * q + 1));
         } else {
-            const int j0 = column(2 * k), j1 = column(2 * k + 1);
-            return make_float2(j0 < cols ? to_f32(p[j0]) : 0.0f, j1 < cols ? to_f32(p[j1]) : 0.0f);
+            const int j0 = column(2 * i), j1 = column(2 * i + 1);
+            v[0] = make_float2(j0 < cols ? to_f32(p[j0]) : 0.0f, j1 < cols ? to_f32(p[j1]) : 0.0f);
         }
     };
     auto kept = [&](int j) {
@@ -177,17 +183,23 @@ k_ln_backward(const Bwd a, int stages, uint32_t row_bytes) {
         const float2 minus_mean = make_float2(-mean, -mean), rstd2 = make_float2(rstd, rstd);
         float2 u[KEEP ? P : 1], g[KEEP ? P : 1], s1 = make_float2(0.0f, 0.0f), s2 = s1;
 #pragma unroll
-        for (int k = 0; k < P; ++k) {
-            const float2 d = pair(pd, k);
-            const float2 uk = __fmul2_rn(__fadd2_rn(pair(px, k), minus_mean), rstd2);
-            const float2 gk = __fmul2_rn(d, KEEP ? w[KEEP ? k : 0] : shared_weights(k));
-            dg[k] = __ffma2_rn(d, uk, dg[k]);
-            db[k] = __fadd2_rn(db[k], d);
-            s1 = __fadd2_rn(s1, gk);
-            s2 = __ffma2_rn(gk, uk, s2);
-            if (KEEP) {
-                u[KEEP ? k : 0] = uk;
-                g[KEEP ? k : 0] = gk;
+        for (int i = 0; i < P / Q; ++i) {
+            float2 x2[Q], d2[Q];
+            piece(px, i, x2);
+            piece(pd, i, d2);
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                const int k = i * Q + q;
+                const float2 uk = __fmul2_rn(__fadd2_rn(x2[q], minus_mean), rstd2);
+                const float2 gk = __fmul2_rn(d2[q], KEEP ? w[KEEP ? k : 0] : shared_weights(k));
+                dg[k] = __ffma2_rn(d2[q], uk, dg[k]);
+                db[k] = __fadd2_rn(db[k], d2[q]);
+                s1 = __fadd2_rn(s1, gk);
+                s2 = __ffma2_rn(gk, uk, s2);
+                if (KEEP) {
+                    u[KEEP ? k : 0] = uk;
+                    g[KEEP ? k : 0] = gk;
+                }
             }
         }
         const float2 s = block_sum2(s1.x + s1.y, s2.x + s2.y, slots[turn]);
@@ -201,27 +213,36 @@ k_ln_backward(const Bwd a, int stages, uint32_t row_bytes) {
         T *out = static_cast<T *>(a.dx) + row * a.ld_dx;
         float v[2 * P];
 #pragma unroll
-        for (int k = 0; k < P; ++k) {
-            float2 uk, gk;
-            if (KEEP) {
-                uk = u[KEEP ? k : 0];
-                gk = g[KEEP ? k : 0];
-            } else {
-                uk = __fmul2_rn(__fadd2_rn(pair(px, k), minus_mean), rstd2);
-                gk = __fmul2_rn(pair(pd, k), shared_weights(k));
+        for (int i = 0; i < P / Q; ++i) {
+            float2 x2[Q], d2[Q];
+            if (!KEEP) {
+                piece(px, i, x2);
+                piece(pd, i, d2);
             }
-            const float2 r = __fmul2_rn(rstd2, __ffma2_rn(uk, minus_c2, __fadd2_rn(gk, minus_c1)));
-            v[2 * k] = r.x;
-            v[2 * k + 1] = r.y;
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                const int k = i * Q + q;
+                float2 uk, gk;
+                if (KEEP) {
+                    uk = u[KEEP ? k : 0];
+                    gk = g[KEEP ? k : 0];
+                } else {
+                    uk = __fmul2_rn(__fadd2_rn(x2[q], minus_mean), rstd2);
+                    gk = __fmul2_rn(d2[q], shared_weights(k));
+                }
+                const float2 r = __fmul2_rn(rstd2, __ffma2_rn(uk, minus_c2, __fadd2_rn(gk, minus_c1)));
+                v[2 * k] = r.x;
+                v[2 * k + 1] = r.y;
+            }
         }
 #pragma unroll
         for (int i = 0; i < 2 * P / V; ++i) {
             if (column(i * V) >= cols) continue;
             Pack<T, V> o;
-            float piece[V];
+            float whole[V];
 #pragma unroll
-            for (int q = 0; q < V; ++q) piece[q] = v[i * V + q];
-            o.round(piece);
+            for (int q = 0; q < V; ++q) whole[q] = v[i * V + q];
+            o.round(whole);
             store_chunk<T, V, false>(out, column(i * V), cols, o, so);
         }
         turn ^= 1;
@@ -413,7 +434,8 @@ cudaError_t launch_ring(Bwd a, bool vec, cudaStream_t stream) {
     if (a.parts > most_parts(a.rows, a.cols)) a.parts = most_parts(a.rows, a.cols);
     const size_t smem = size_t(stages) * 2 * row_bytes + weights;
     auto run = [&](auto kern) {
-        const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+        // Always the most that any call needs: threads with rows of other lengths set it too.
+        const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(ring_room(1)));
         if (err != cudaSuccess) return err;
         return launch_pdl(kern, dim3(unsigned(a.parts)), dim3(unsigned(threads)), smem, stream, a, int(stages), row_bytes);
     };

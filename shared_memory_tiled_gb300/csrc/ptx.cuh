@@ -55,19 +55,6 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity) {
     return done != 0;
 }
 
-// The same without letting the hardware suspend the thread.
-__device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(smem_addr(bar)), "r"(parity)
-        : "memory");
-    return done != 0;
-}
-
 __device__ __forceinline__ uint64_t global_timer_ns() {
     uint64_t t;
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
@@ -88,15 +75,6 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t *bar, uint32_t parity
     return false;
 }
 
-// The same without the timer's cost on a wait that is short: the timer is read
-// after 64 probes, each of which may suspend the thread, and every 64 after that.
-__device__ __forceinline__ bool mbar_wait_fast(uint64_t *bar, uint32_t parity) {
-#pragma unroll 1
-    for (uint32_t n = 0; n < 64; ++n)
-        if (mbar_try_wait(bar, parity)) return true;
-    return mbar_wait_bounded(bar, parity);
-}
-
 // Orders this thread's generic-proxy shared-memory writes before later
 // async-proxy (TMA) reads of the same memory.
 __device__ __forceinline__ void fence_proxy_async_smem() {
@@ -111,14 +89,14 @@ __device__ __forceinline__ void cp_async_16(void *smem_dst, const void *gmem_src
                  : "memory");
 }
 
-// The same of 4 bytes.
-__device__ __forceinline__ void cp_async_4(void *smem_dst, const void *gmem_src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(smem_dst)),
-                 "l"(gmem_src)
+// The first `bytes` (0 to 16) of it; the rest of the 16 is zeroed.
+__device__ __forceinline__ void cp_async_16_or_zero(void *smem_dst, const void *gmem_src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(smem_dst)),
+                 "l"(gmem_src), "r"(bytes)
                  : "memory");
 }
 
-// The same, or zeros (nothing is read) without `have`.
+// 4-byte copy, or zeros (nothing is read) without `have`.
 __device__ __forceinline__ void cp_async_4_or_zero(void *smem_dst, const void *gmem_src, bool have) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_addr(smem_dst)),
                  "l"(gmem_src), "r"(have ? 4 : 0)

@@ -4,7 +4,6 @@
 #include <cuda_fp8.h>
 
 #include <atomic>
-#include <mutex>
 
 #include "bounds.cuh"
 #include "launch.cuh"
@@ -48,15 +47,51 @@ __device__ __forceinline__ void store8(uint8_t *row, int64_t c, int64_t cols, ui
         if (TR_STORE_OK(s, row + c + i, 1)) row[c + i] = uint8_t((i < 4 ? v.x >> (8 * i) : v.y >> (8 * (i - 4))));
 }
 
-// How a tile's values reach the registers.
+// How a tile's values reach the registers.  The two for rows off 16-byte boundaries go
+// through shared memory; each warp copies, and reads back, its own 16 rows.
 enum Load {
     kVector,   // 16-byte loads: base and pitch on 16-byte boundaries
-    kWords,    // fp32 rows off those boundaries: 4-byte copies into a shared tile, coalesced
-    kElements  // bf16 rows off them: one element at a time
+    kWords,    // fp32: 4-byte asynchronous copies, coalesced (12289 x 7919, 128 x 128 blocks, both
+               // ways: 125 us; 16-byte copies of the granules around a row: 152)
+    kGranules  // bf16: 16-byte asynchronous copies of the granules around a row, shifted in
+               // registers (12289 x 7919, both ways: 86 us; one element at a time: 118)
 };
 
-constexpr int kWordPitch = 132;  // words to a row of the shared tile: rows stay 16-byte aligned
-constexpr size_t kWordTileBytes = size_t(128) * kWordPitch * 4;
+constexpr int kWordPitch = 132;    // fp32 words to a row of the shared tile: rows stay 16-byte aligned
+constexpr int kGranulePitch = 72;  // words to a row of 17 granules
+constexpr size_t kTileBytes[3] = {0, size_t(128) * kWordPitch * 4, size_t(128) * kGranulePitch * 4};
+
+// One granule of a bf16 row of `cols` values from `row` on, the one that begins at column
+// col: its bytes inside the row are copied, those past its end zeroed, and those
+// before its start left as they are (nobody reads them).
+__device__ __forceinline__ void copy_granule(uint32_t *dst, const __nv_bfloat16 *row, int64_t col, int64_t cols,
+                                             const dbg::Side &s) {
+    if (col >= 0) {
+        const int64_t left = cols - col;
+        const int bytes = left <= 0 ? 0 : left < 8 ? int(left) * 2 : 16;
+        const bool ok = bytes && TR_LOAD_OK(s, row + col, bytes);
+        ptx::cp_async_16_or_zero(dst, ok ? row + col : row, ok ? bytes : 0);
+    } else {
+        __nv_bfloat16 *e = reinterpret_cast<__nv_bfloat16 *>(dst);
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            if (col + q >= 0) e[q] = col + q < cols && TR_LOAD_OK(s, row + col + q, 2) ? row[col + q] : __nv_bfloat16(0.0f);
+    }
+}
+
+// The 16 bytes from `shift` (even, below 16) on of two granules: whole words move in two
+// selections, half a word in a third.
+__device__ __forceinline__ uint4 pick(const uint32_t *granules, uint32_t shift) {
+    const uint4 a = *reinterpret_cast<const uint4 *>(granules), b = *reinterpret_cast<const uint4 *>(granules + 4);
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int k = 0; k < 6; ++k) w[k] = shift & 8 ? w[k + 2] : w[k];
+#pragma unroll
+    for (int k = 0; k < 5; ++k) w[k] = shift & 4 ? w[k + 1] : w[k];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = shift & 2 ? __byte_perm(w[k], w[k + 1], 0x5432) : w[k];
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
 
 // The 8 x 8 values of one thread.  bf16 stays packed in pairs along the row.
 template <typename T>
@@ -215,7 +250,7 @@ template <typename T, Load LOAD, bool E5M2, bool BLOCK, bool BOTH>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) k_quantize(const Quant a) {
     pdl_prologue();
     using M = Magnitudes<T>;
-    extern __shared__ uint4 word_tile[];
+    extern __shared__ uint4 shared_tile[];
     __shared__ alignas(16) uint8_t col_max[8][128 * M::kBytes];
     __shared__ alignas(16) float col_inv[128];
     __shared__ uint2 turned[BOTH ? 128 * 16 : 1];
@@ -231,27 +266,60 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) k_quantize(c
         const int64_t r0 = tr * 128 + rg * 8, c0 = tc * 128 + cg * 8;
         Values<T> v;
         if constexpr (LOAD == kWords) {
-            float *words = reinterpret_cast<float *>(word_tile);
+            float *words = reinterpret_cast<float *>(shared_tile);
 #pragma unroll 8
             for (int k = 0; k < 64; ++k) {  // a warp copies 16 rows, 32 columns at a time
                 const int r = warp * 16 + (k >> 2), c = (k & 3) * 32 + lane;
                 const int64_t row = tr * 128 + r, col = tc * 128 + c;
                 float *dst = words + r * kWordPitch + c;
                 const T *p = x + row * a.ld_x + col;
-                if (row < a.rows && col < a.cols && TR_LOAD_OK(sx, p, 4)) ptx::cp_async_4(dst, p);
-                else *dst = 0.0f;
+                const bool have = row < a.rows && col < a.cols && TR_LOAD_OK(sx, p, 4);
+                ptx::cp_async_4_or_zero(dst, have ? p : x, have);
             }
             ptx::cp_async_wait_all();
             __syncwarp();  // a warp reads back only what it copied: rows 16*warp ..
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 v.row(i, reinterpret_cast<const uint4 *>(words + (rg * 8 + i) * kWordPitch + cg * 8));
+        } else if constexpr (LOAD == kGranules) {
+            uint32_t *granules = reinterpret_cast<uint32_t *>(shared_tile) + warp * 16 * kGranulePitch;
+            const T *first = x + (tr * 128 + warp * 16) * a.ld_x;  // the warp's first row
+            auto shift = [&](int r) { return uint32_t(reinterpret_cast<uintptr_t>(first + r * a.ld_x + tc * 128) & 15u); };
+            auto copy = [&](int r, int granule) {
+                uint32_t *dst = granules + r * kGranulePitch + granule * 4;
+                if (tr * 128 + warp * 16 + r < a.rows)
+                    copy_granule(dst, first + r * a.ld_x, tc * 128 + granule * 8 - int(shift(r) / 2), a.cols, sx);
+                else
+                    *reinterpret_cast<uint4 *>(dst) = make_uint4(0u, 0u, 0u, 0u);
+            };
+            if (tc > 0 && (tc + 1) * 128 + 8 <= a.cols && tr * 128 + 128 <= a.rows) {
+                // Inside the matrix every granule is whole: two rows to an instruction,
+                // then the last granule of each row.
+                auto whole = [&](int r, int granule) {
+                    const T *src = first + r * a.ld_x + tc * 128 - shift(r) / 2 + granule * 8;
+                    if (TR_LOAD_OK(sx, src, 16)) ptx::cp_async_16(granules + r * kGranulePitch + granule * 4, src);
+                };
+#pragma unroll
+                for (int r = 0; r < 16; r += 2) whole(r + (lane >> 4), lane & 15);
+                if (lane < 16) whole(lane, 16);
+            } else {
+#pragma unroll 1
+                for (int k = lane; k < 16 * 17; k += 32) copy(k / 17, k % 17);
+            }
+            ptx::cp_async_wait_all();
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int r = (rg & 1) * 8 + i;
+                const uint4 raw[1] = {pick(granules + r * kGranulePitch + cg * 4, shift(r))};
+                v.row(i, raw);
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const T *p = x + (r0 + i) * a.ld_x + c0;
                 uint4 raw[sizeof(T) / 2] = {};
-                if (LOAD == kVector && r0 + i < a.rows && c0 + 8 <= a.cols && TR_LOAD_OK(sx, p, int(8 * sizeof(T)))) {
+                if (r0 + i < a.rows && c0 + 8 <= a.cols && TR_LOAD_OK(sx, p, int(8 * sizeof(T)))) {
 #pragma unroll
                     for (int k = 0; k < int(sizeof(T)) / 2; ++k) raw[k] = __ldcs(reinterpret_cast<const uint4 *>(p) + k);
                     v.row(i, raw);
@@ -349,28 +417,24 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) k_quantize(c
             }
         }
         // The shared words are written anew in the next turn.
-        if (tile + gridDim.x < a.tiles_r * a.tiles_c && (BOTH || BLOCK || LOAD == kWords)) __syncthreads();
+        if (tile + gridDim.x < a.tiles_r * a.tiles_c) __syncthreads();
     }
 }
 
 template <typename T, Load LOAD, bool E5M2, bool BLOCK, bool BOTH>
 cudaError_t launch_one(const Quant &a, cudaStream_t stream) {
     auto kern = k_quantize<T, LOAD, E5M2, BLOCK, BOTH>;
-    constexpr size_t smem = LOAD == kWords ? kWordTileBytes : 0;
+    constexpr size_t smem = kTileBytes[LOAD];
     if (smem) {
         static std::atomic<bool> opted[64];  // per device, zero-initialised (static)
-        static std::mutex mu;
         int dev = 0;
         cudaError_t e = cudaGetDevice(&dev);
         if (e != cudaSuccess) return e;
         if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-        if (!opted[dev].load(std::memory_order_acquire)) {
-            std::lock_guard<std::mutex> lock(mu);
-            if (!opted[dev].load(std::memory_order_relaxed)) {
-                e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-                if (e != cudaSuccess) return e;
-                opted[dev].store(true, std::memory_order_release);
-            }
+        if (!opted[dev].load(std::memory_order_acquire)) {  // setting it twice is harmless
+            e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+            if (e != cudaSuccess) return e;
+            opted[dev].store(true, std::memory_order_release);
         }
     }
     const int64_t tiles = a.tiles_r * a.tiles_c, most = int64_t(1) << 30;
@@ -386,7 +450,7 @@ cudaError_t launch_typed(const Quant &a, bool block, cudaStream_t stream) {
 
 template <typename T>
 cudaError_t launch_in(const Quant &a, bool block, bool e5m2, cudaStream_t stream) {
-    constexpr Load kOther = sizeof(T) == 4 ? kWords : kElements;
+    constexpr Load kOther = sizeof(T) == 4 ? kWords : kGranules;
     if (side_aligned16(a.x, a.ld_x, 0, 1, sizeof(T)))
         return e5m2 ? launch_typed<T, kVector, true>(a, block, stream) : launch_typed<T, kVector, false>(a, block, stream);
     return e5m2 ? launch_typed<T, kOther, true>(a, block, stream) : launch_typed<T, kOther, false>(a, block, stream);

@@ -42,7 +42,6 @@ struct alignas(4 * V) Pack<float, V> {
         for (int q = 0; q < V; ++q) e[q] = v[q];
     }
     __device__ __forceinline__ float get(int q, uint32_t) const { return e[q]; }
-    __device__ __forceinline__ float2 pair(int k) const { return make_float2(e[2 * k], e[2 * k + 1]); }
 };
 
 template <>
@@ -66,7 +65,6 @@ struct alignas(16) Pack<__nv_bfloat16, 8> {
             w[k] = *reinterpret_cast<const uint32_t *>(&h);
         }
     }
-    __device__ __forceinline__ float2 pair(int k) const { return make_float2(get(2 * k), get(2 * k + 1)); }
     __device__ __forceinline__ float get(int q, uint32_t z) const {
         return __uint_as_float(__byte_perm(w[q >> 1], z, q & 1 ? 0x3244 : 0x1044));
     }
