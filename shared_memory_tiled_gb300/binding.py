@@ -17,7 +17,6 @@ from __future__ import annotations
 
 import ctypes
 import enum
-import functools
 import os
 import threading
 
@@ -409,17 +408,24 @@ def transpose_(x, stream=None):
 # --- a linear layer in 8-bit floating point: torch conveniences -----------------------
 #
 # Kept short on the host: a call on one token costs the GPU 3-5 us, about what the
-# C entry point costs the host, and each torch lookup here 0.1-2 us on top.
+# C entry point costs the host (3-4 us), and each tensor that torch allocates costs
+# 1.3-2 us, each look at a tensor or import statement 0.1-0.3 us on top.
 
-_KINDS: dict = {}  # {torch dtype: DType value}, filled on first use
-_WIDE, _NARROW = (0, 1), (2, 3)
+_torch = None       # the module, once one of these functions has needed it
+_KINDS: dict = {}   # {torch dtype: DType value}
+_WIDE, _NARROW, _F32 = (0, 1), (2, 3), (0,)
+
+
+def _need_torch():
+    global _torch
+    import torch
+    _KINDS.update({torch.float32: 0, torch.bfloat16: 1, torch.float8_e4m3fn: 2,
+                   torch.float8_e5m2: 3})
+    _torch = torch
+    return torch
 
 
 def _kind(dtype, allowed, name):
-    if not _KINDS:
-        import torch
-        _KINDS.update({torch.float32: 0, torch.bfloat16: 1, torch.float8_e4m3fn: 2,
-                       torch.float8_e5m2: 3})
     k = _KINDS.get(dtype)
     if k not in allowed:
         raise TypeError(f"{name}: unsupported dtype {dtype}")
@@ -430,9 +436,10 @@ def _matrix(t, name, device):
     """(rows, cols, pitch) of a matrix with unit inner stride on a CUDA device."""
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
-    if t.dim() != 2:
+    shape = t.shape
+    if len(shape) != 2:
         raise ValueError(f"{name} must be a matrix")
-    r, c = t.shape
+    r, c = shape
     sr, sc = t.stride()
     if sc != 1 and c > 1:
         raise ValueError(f"the innermost dimension of {name} must be contiguous")
@@ -456,38 +463,31 @@ def _cuda(x):
 def _run(name, args, device):
     """Calls a C entry point with its argument struct on torch's current stream
     of the device."""
-    import torch
     index = device.index
     # torch.cuda.current_stream(device).cuda_stream, without its 2 us of wrapping
-    args.stream = torch._C._cuda_getCurrentRawStream(index)
+    args.stream = _torch._C._cuda_getCurrentRawStream(index)
     f = getattr(_lib or load(), name)
-    if torch.cuda.current_device() == index:
+    if _torch.cuda.current_device() == index:
         status = f(ctypes.byref(args))
     else:
-        with torch.cuda.device(device):  # the library sets kernels up per current device
+        with _torch.cuda.device(device):  # the library sets kernels up per current device
             status = f(ctypes.byref(args))
     if status:
         check(status)
 
 
-def _on_stream(f):
-    """``stream=``: the call, and the allocation of what it returns and works in,
-    happens on that cudaStream_t instead of torch's current stream."""
-    @functools.wraps(f)
-    def call(*args, stream=None, **kw):
-        if stream is None:
-            return f(*args, **kw)
-        import torch
-        device = _cuda(args[0])
-        s = (torch.cuda.ExternalStream(stream, device=device) if stream
-             else torch.cuda.default_stream(device))
-        with torch.cuda.stream(s):
-            return f(*args, **kw)
-    return call
+def _on(stream, x, call):
+    """Makes the call, and so allocates what it returns and works in, on that
+    cudaStream_t instead of torch's current stream."""
+    torch = _torch or _need_torch()
+    device = _cuda(x)
+    s = (torch.cuda.ExternalStream(stream, device=device) if stream
+         else torch.cuda.default_stream(device))
+    with torch.cuda.stream(s):
+        return call()
 
 
-@_on_stream
-def quantize_fp8(x, *, dtype=None, block_rows=1, transposed=False):
+def quantize_fp8(x, *, dtype=None, block_rows=1, transposed=False, stream=None):
     """Quantize a CUDA matrix (fp32 or bf16) to 8-bit floating point.
 
     Returns ``(q, scale)``, and with ``transposed`` ``(q, scale, qt, scale_t)``:
@@ -498,7 +498,9 @@ def quantize_fp8(x, *, dtype=None, block_rows=1, transposed=False):
     and ``scale_t`` are the same of x's transpose, from the same read of x.
     ``stream`` (a cudaStream_t): default torch's current stream.
     """
-    import torch
+    if stream is not None:
+        return _on(stream, x, lambda: quantize_fp8(x, dtype=dtype, block_rows=block_rows, transposed=transposed))
+    torch = _torch or _need_torch()
     dev = _cuda(x)
     rows, cols, ld = _matrix(x, "x", dev)
     if dtype is None:
@@ -506,17 +508,18 @@ def quantize_fp8(x, *, dtype=None, block_rows=1, transposed=False):
     xk, qk = _kind(x.dtype, _WIDE, "x"), _kind(dtype, _NARROW, "dtype")
     if block_rows != 1 and block_rows != 128:
         raise ValueError("block_rows must be 1 or 128")
+    empty, strided, f32 = torch.empty, torch.empty_strided, torch.float32
     cb, rb, ld_q = (cols + 127) // 128, (rows + block_rows - 1) // block_rows, (cols + 15) // 16 * 16
-    q = torch.empty_strided((rows, cols), (ld_q, 1), dtype=dtype, device=dev)
-    scale = torch.empty((cb, rb), dtype=torch.float32, device=dev)
+    q = strided((rows, cols), (ld_q, 1), dtype=dtype, device=dev)
+    scale = empty((cb, rb), dtype=f32, device=dev)
     if not transposed:
         _run("tr_quantize_fp8", QuantizeArgs(
             x.data_ptr(), q.data_ptr(), scale.data_ptr(), None, None, xk, qk, block_rows, 0, rows,
             cols, ld, ld_q, rb, 0, 0), dev)
         return q, scale
     cbt, rbt, ld_t = (rows + 127) // 128, (cols + block_rows - 1) // block_rows, (rows + 15) // 16 * 16
-    qt = torch.empty_strided((cols, rows), (ld_t, 1), dtype=dtype, device=dev)
-    scale_t = torch.empty((cbt, rbt), dtype=torch.float32, device=dev)
+    qt = strided((cols, rows), (ld_t, 1), dtype=dtype, device=dev)
+    scale_t = empty((cbt, rbt), dtype=f32, device=dev)
     _run("tr_quantize_fp8", QuantizeArgs(
         x.data_ptr(), q.data_ptr(), scale.data_ptr(), qt.data_ptr(), scale_t.data_ptr(), xk, qk,
         block_rows, 0, rows, cols, ld, ld_q, rb, ld_t, rbt), dev)
@@ -529,12 +532,11 @@ def _scales(scale, rows, blocks, name, device):
     if kb != blocks or (rb != rows and rb != (rows + 127) // 128):
         raise ValueError(f"{name} has shape {tuple(scale.shape)}, expected "
                          f"[{blocks}, {rows} or {(rows + 127) // 128}]")
-    _kind(scale.dtype, (0,), name)
+    _kind(scale.dtype, _F32, name)
     return (1 if rb == rows else 128), ld
 
 
-@_on_stream
-def matmul_fp8(a, scale_a, b, scale_b, *, out=None, out_dtype=None, accumulate=False):
+def matmul_fp8(a, scale_a, b, scale_b, *, out=None, out_dtype=None, accumulate=False, stream=None):
     """Product ``a @ b.T`` of two 8-bit operands [m, k] and [n, k] with their scales.
 
     The operands are as ``quantize_fp8`` returns them (or its transposed pair):
@@ -544,7 +546,10 @@ def matmul_fp8(a, scale_a, b, scale_b, *, out=None, out_dtype=None, accumulate=F
     ``out_dtype`` (bf16 by default); ``accumulate`` adds to ``out``.
     ``stream`` (a cudaStream_t): default torch's current stream.
     """
-    import torch
+    if stream is not None:
+        return _on(stream, a, lambda: matmul_fp8(a, scale_a, b, scale_b, out=out, out_dtype=out_dtype,
+                                                 accumulate=accumulate))
+    torch = _torch or _need_torch()
     dev = _cuda(a)
     m, k, lda = _matrix(a, "a", dev)
     n, kb, ldb = _matrix(b, "b", dev)
@@ -574,16 +579,14 @@ def matmul_fp8(a, scale_a, b, scale_b, *, out=None, out_dtype=None, accumulate=F
 def _like(out, x, rows, cols, dev):
     """An output of x's shape and type: (tensor, pitch)."""
     if out is None:
-        import torch
-        return torch.empty((rows, cols), dtype=x.dtype, device=dev), cols
+        return _torch.empty((rows, cols), dtype=x.dtype, device=dev), cols
     r, c, ld = _matrix(out, "out", dev)
     if r != rows or c != cols or out.dtype != x.dtype:
         raise ValueError("out must match x in shape and dtype")
     return out, ld
 
 
-@_on_stream
-def layernorm(x, gamma, beta=None, *, eps=1e-5, out=None):
+def layernorm(x, gamma, beta=None, *, eps=1e-5, out=None, stream=None):
     """Layer norm over the rows of a CUDA matrix (fp32 or bf16).
 
     Returns ``(y, mean, rstd)``: y of x's type (``out`` if given), the rows'
@@ -591,7 +594,9 @@ def layernorm(x, gamma, beta=None, *, eps=1e-5, out=None):
     ``gamma`` and ``beta`` are fp32 or bf16, both the same.  ``stream`` (a
     cudaStream_t): default torch's current stream.
     """
-    import torch
+    if stream is not None:
+        return _on(stream, x, lambda: layernorm(x, gamma, beta, eps=eps, out=out))
+    torch = _torch or _need_torch()
     dev = _cuda(x)
     rows, cols, ld = _matrix(x, "x", dev)
     _vector(gamma, "gamma", cols, dev)
@@ -601,20 +606,21 @@ def layernorm(x, gamma, beta=None, *, eps=1e-5, out=None):
             raise TypeError("gamma and beta must have the same dtype")
     xk, wk = _kind(x.dtype, _WIDE, "x"), _kind(gamma.dtype, _WIDE, "gamma")
     out, ld_y = _like(out, x, rows, cols, dev)
-    mean = torch.empty(rows, dtype=torch.float32, device=dev)
-    rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+    empty, f32 = torch.empty, torch.float32
+    mean, rstd = empty(rows, dtype=f32, device=dev), empty(rows, dtype=f32, device=dev)
     _run("tr_layernorm", LayernormArgs(
         x.data_ptr(), gamma.data_ptr(), None if beta is None else beta.data_ptr(), out.data_ptr(),
         mean.data_ptr(), rstd.data_ptr(), xk, wk, rows, cols, ld, ld_y, eps, 0), dev)
     return out, mean, rstd
 
 
-@_on_stream
-def layernorm_backward(dy, x, gamma, mean, rstd, *, bias=True, out=None):
+def layernorm_backward(dy, x, gamma, mean, rstd, *, bias=True, out=None, stream=None):
     """Gradients of ``layernorm``: ``(dx, dgamma, dbeta)``, dx of x's type (``out``
     if given), the others in fp32; without ``bias`` dbeta is None.  ``stream``
     (a cudaStream_t): default torch's current stream."""
-    import torch
+    if stream is not None:
+        return _on(stream, x, lambda: layernorm_backward(dy, x, gamma, mean, rstd, bias=bias, out=out))
+    torch = _torch or _need_torch()
     dev = _cuda(x)
     rows, cols, ld = _matrix(x, "x", dev)
     r, c, ld_dy = _matrix(dy, "dy", dev)
@@ -623,14 +629,15 @@ def layernorm_backward(dy, x, gamma, mean, rstd, *, bias=True, out=None):
     _vector(gamma, "gamma", cols, dev)
     _vector(mean, "mean", rows, dev)
     _vector(rstd, "rstd", rows, dev)
-    _kind(mean.dtype, (0,), "mean")
-    _kind(rstd.dtype, (0,), "rstd")
+    _kind(mean.dtype, _F32, "mean")
+    _kind(rstd.dtype, _F32, "rstd")
     xk, wk = _kind(x.dtype, _WIDE, "x"), _kind(gamma.dtype, _WIDE, "gamma")
     out, ld_dx = _like(out, x, rows, cols, dev)
-    dgamma = torch.empty(cols, dtype=torch.float32, device=dev)
-    dbeta = torch.empty(cols, dtype=torch.float32, device=dev) if bias else None
-    size = tr_layernorm_backward_workspace(rows, cols)
-    workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+    empty, f32 = torch.empty, torch.float32
+    dgamma = empty(cols, dtype=f32, device=dev)
+    dbeta = empty(cols, dtype=f32, device=dev) if bias else None
+    size = (_lib or load()).tr_layernorm_backward_workspace(rows, cols)
+    workspace = empty(size, dtype=torch.uint8, device=dev)
     _run("tr_layernorm_backward", LayernormBackwardArgs(
         dy.data_ptr(), x.data_ptr(), gamma.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
         out.data_ptr(), dgamma.data_ptr(), dbeta.data_ptr() if bias else None,
