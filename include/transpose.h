@@ -1,5 +1,7 @@
 /*
- * libtranspose -- out-of-place matrix transpose for GB300 (sm_103a).
+ * libtranspose -- out-of-place matrix transpose for GB300 (sm_103a), and the
+ * operators of a linear layer in 8-bit floating point that needs its operands
+ * both as they are and transposed (second half of this header).
  *
  * What it computes.  For every batch plane b < batch, input row i < rows and
  * input column j < cols (all sizes and pitches in ELEMENTS):

@@ -15,6 +15,22 @@
 //
 // Few tiles: the blocks of the contraction are split over a cluster of CTAs and
 // their sums joined through distributed shared memory, in rank order.
+//
+// Measured on one GB300 (a bf16 library product reaches 1920 TFLOP/s there; 8-bit
+// instructions run at twice its rate):
+//   8192^3, 1x128 by 128x128 scales, bf16 out        503 us, 2.19 PFLOP/s
+//   8192^3, 1x128 by 1x128                           663 us, 1.66 PFLOP/s
+//   4096 x 2048 x 16384, 1x128 by 1x128, fp32 out    192 us, 1.43 PFLOP/s
+//   2048^3                                            14 us, 1.20 PFLOP/s
+//   777 x 2049 x 1111                               12.8 us
+//   1 x 8192 x 8192                                 14.5 us, 4.6 TB/s of weights (68% of the copy rate)
+//
+// What bounds the large ones is the exchange between the tensor cores and the warps
+// that take the sums out, once for each block of 128: the instructions alone run at
+// 250 us for 8192^3 from operands that are in place, at 322 us with the loads, and the
+// warps' work on a block (tensor memory to registers, 256 columns by 128 rows to an
+// SM) takes 380 cycles by itself, but a buffer of sums goes through both in turn, with
+// some 150 cycles of notice each way, and tensor memory holds two buffers.
 #include <atomic>
 
 #include "bounds.cuh"

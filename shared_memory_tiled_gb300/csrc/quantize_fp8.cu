@@ -1,5 +1,21 @@
 // Quantizing to 8-bit floating point with a scale for each block of 128, row
-// by row and transposed from one read.
+// by row and transposed from one read.  For a block with largest magnitude m and T the
+// type's largest value: a = max(m, 2^-100), scale = a / T, q = round(x * (T / a)).
+//
+// Bound by memory: x is read once and each wanted operand written once, 2 + 1 + 1
+// bytes to a bf16 value both ways.  Two things keep it there: a tile is read into
+// registers once for both directions, and the work on a value is cut to about eight
+// instructions (magnitudes in packed pairs, one division to a row and to a column, two
+// values to a conversion).  With the magnitudes in fp32, a division in each
+// thread and every thread reading eight warps' column maxima, 16384 x 8192 bf16
+// both ways took 277 us.
+//
+// Measured on one GB300 (share of the measured copy rate, 6771 GB/s):
+//   16384 x 8192 bf16, 1 x 128 blocks, both ways   95 us, 5.7 TB/s (85%); rows alone 64 us (92%)
+//   16384 x 8192 bf16, 128 x 128, both ways        87 us, 6.2 TB/s (91%)
+//   12289 x 7919 fp32, 128 x 128, both ways       123 us, 4.7 TB/s (70%)  (rows off 16-byte boundaries)
+//   12288 x 7920 fp32, 128 x 128, both ways       100 us, 5.8 TB/s (86%)
+//   1 x 8192 bf16                                 2.6 us: a launch
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
