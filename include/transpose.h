@@ -333,8 +333,8 @@ typedef struct tr_matmul_fp8_args {
  * Products and sums are held in 32 bits on the tensor cores within a block,
  * in 32-bit registers across blocks, and rounded once to the output's type;
  * with `accumulate` the output's old value is added in 32 bits first.  The
- * order of the sums depends on the sizes alone, so equal calls give equal
- * bits.  a and b are 16-byte aligned with pitches that are multiples of 16
+ * order of the sums is fixed for a call's arguments on a device, so equal calls
+ * give equal bits.  a and b are 16-byte aligned with pitches that are multiples of 16
  * (else TR_ERR_UNSUPPORTED); m, n and k are below 2^31.  k = 0 gives zeros
  * (or leaves out as it is, with `accumulate`). */
 tr_status tr_matmul_fp8(const tr_matmul_fp8_args *args);
@@ -388,9 +388,9 @@ typedef struct tr_layernorm_backward_args {
  *     dx = rstd * (g - sum(g)/cols - u * sum(g u)/cols)         along each row
  *     dgamma[j] = sum over rows of dy u,  dbeta[j] = sum over rows of dy
  *
- * The sums down the rows are held in 32 bits and joined in an order that the
- * sizes alone fix (no atomics), so equal calls give equal bits.  Nothing needs
- * clearing before the call.  TR_ERR_UNSUPPORTED for a workspace that is too
+ * The sums down the rows are held in 32 bits and joined in an order that is
+ * fixed for a call's arguments on a device (no atomics), so equal calls give
+ * equal bits.  Nothing needs clearing before the call.  TR_ERR_UNSUPPORTED for a workspace that is too
  * small or misaligned. */
 tr_status tr_layernorm_backward(const tr_layernorm_backward_args *args);
 

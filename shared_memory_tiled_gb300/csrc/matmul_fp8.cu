@@ -531,113 +531,107 @@ k_matmul_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__
     bool ok = true;
 
     if (warp < 4) {
-      ptx::registers_down<kFewRegisters>();
-      if (warp == 0) {
-        if (lane == 0) {
-            int s = 0;
-            uint32_t phase = 1;  // the first round finds every stage empty
-            for (int64_t tile = pair; tile < tiles && ok; tile += pairs) {
-                int64_t p0, q0;
-                tile_at(g, tile, kPairTile, kPairTile, 8, &p0, &q0);
-                for (int i = 0; i < g.blocks; ++i) {
-                    if (!ptx::mbar_wait_bounded(empty + s, phase)) {
-                        ok = false;
-                        break;
-                    }
-                    uint8_t *dst = stages + s * kPairStageBytes;
-                    if (rank == 0) ptx::mbar_arrive_expect_tx(full + s, 2 * kPairStageBytes);
-                    const uint32_t bar = ptx::peer_addr(full + s, 0);
-                    ptx::tma_load_2d_pair(dst, &map_p, bar, i * kBlockK, int32_t(p0) + int32_t(rank) * 128);
-                    ptx::tma_load_2d_pair(dst + kBytesP, &map_q, bar, i * kBlockK, int32_t(q0) + int32_t(rank) * 128);
-                    if (++s == kPairStages) {
-                        s = 0;
-                        phase ^= 1;
-                    }
-                }
-            }
-            if (!ok) {  // no load may land after the block has gone: they take microseconds
-                const uint64_t t0 = ptx::global_timer_ns();
-                for (uint32_t n = 0; n < 1u << 24 && ptx::global_timer_ns() - t0 < 2000000; ++n) {
-                }
-            }
-        }
-      } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
-            const uint32_t idesc = ptx::f8_idesc(g.p_e5m2, g.q_e5m2, 256, 256);
-            int s = 0, b = 0;
-            uint32_t phase = 0, sums_phase = 1;
-            bool ready = false;  // the next block's operands and sums were seen ready
-            for (int64_t tile = pair; tile < tiles && ok; tile += pairs)
-                for (int i = 0; i < g.blocks; ++i) {
-                    if (!ready)
-                        ok = ptx::mbar_wait_bounded(full + s, phase) && ptx::mbar_wait_bounded(sums_empty + b, sums_phase);
-                    if (!ok) break;
-                    ptx::tc_fence_after();
-                    const uint32_t at = ptx::smem_addr(stages + s * kPairStageBytes);
-                    const uint64_t dp = ptx::operand_desc(at), dq = ptx::operand_desc(at + kBytesP);
-                    const int used = s, into = b;
-                    if (++s == kPairStages) {
-                        s = 0;
-                        phase ^= 1;
-                    }
-                    b ^= 1;
-                    if (b == 0) sums_phase ^= 1;
-#pragma unroll
-                    for (int k = 0; k < kBlockK / 32; ++k) {
-                        ptx::mma_f8_pair(tmem + into * 256, dp + 2 * k, dq + 2 * k, idesc, k > 0);
-                        // A look at a barrier costs this thread about 100 cycles:
-                        // taken here, while the tensor cores are busy.
-                        
-                    }
-                    ptx::mma_commit_pair(sums_full + into);
-                    ptx::mma_commit_pair(empty + used);
-                }
-        }
-      } else {
-        // Scales, three blocks ahead: warp 2 those of P, warp 3 those of Q.
-        const bool of_p = warp == 2;
-        const float *base = of_p ? g.scale_p : g.scale_q;
-        const int64_t ld = of_p ? g.ld_p : g.ld_q, rows = of_p ? g.p : g.q;
-        const int shift = (of_p ? g.p_block : g.q_block) == 1 ? 0 : 7;  // 2^shift rows to a scale
-        // Scales to take, and the tile's rows from one to the next (block scales of P
-        // are taken once for each row, those of Q once for each 128 columns).
-        const int count = of_p ? 128 : QROW ? 256 : 2, apart = of_p || QROW ? 1 : 128;
-        [[maybe_unused]] const dbg::Side side = dbg::side(base, 1, g.blocks, (rows + (1 << shift) - 1) >> shift, ld, 0, 4);
-        float *ring = of_p ? &scales_p[0][0] : &scales_q[0][0];
-        const int pitch = of_p ? 128 : QROW ? 256 : 4;
-        // Blocks are counted through all tiles of this pair; the copies' cursor
-        // runs kScaleSlots - 1 ahead.
-        const int64_t mine = pair < tiles ? (tiles - 1 - pair) / pairs + 1 : 0, blocks = mine * g.blocks;
-        int64_t tile = pair, r0 = 0;
-        int at = 0;  // the cursor's block of its tile
-        for (int64_t n = -(kScaleSlots - 1); n < blocks; ++n) {
-            if (n >= 0) {
-                ptx::cp_async_wait<kScaleSlots - 2>();  // block n's are here
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(scales_full + n % kScaleSlots);
-            }
-            const int64_t ahead = n + kScaleSlots - 1;
-            if (ahead < blocks) {
-                if (ok && n >= 1) ok = ptx::mbar_wait_bounded(scales_empty + (n - 1) % kScaleSlots, (n - 1) / kScaleSlots & 1);
-                if (at == 0) {
+        ptx::registers_down<kFewRegisters>();
+        if (warp == 0) {
+            if (lane == 0) {
+                int s = 0;
+                uint32_t phase = 1;  // the first round finds every stage empty
+                for (int64_t tile = pair; tile < tiles && ok; tile += pairs) {
                     int64_t p0, q0;
                     tile_at(g, tile, kPairTile, kPairTile, 8, &p0, &q0);
-                    r0 = of_p ? p0 + rank * 128 : q0;
+                    for (int i = 0; i < g.blocks; ++i) {
+                        if (!ptx::mbar_wait_bounded(empty + s, phase)) {
+                            ok = false;
+                            break;
+                        }
+                        uint8_t *dst = stages + s * kPairStageBytes;
+                        if (rank == 0) ptx::mbar_arrive_expect_tx(full + s, 2 * kPairStageBytes);
+                        const uint32_t bar = ptx::peer_addr(full + s, 0);
+                        ptx::tma_load_2d_pair(dst, &map_p, bar, i * kBlockK, int32_t(p0) + int32_t(rank) * 128);
+                        ptx::tma_load_2d_pair(dst + kBytesP, &map_q, bar, i * kBlockK, int32_t(q0) + int32_t(rank) * 128);
+                        if (++s == kPairStages) {
+                            s = 0;
+                            phase ^= 1;
+                        }
+                    }
                 }
-                for (int k = lane; k < count; k += 32) {
-                    const int64_t r = r0 + k * apart;
-                    const float *p = base + at * ld + (r >> shift);
-                    ptx::cp_async_4_or_zero(ring + ahead % kScaleSlots * pitch + k, r < rows ? p : base,
-                                            r < rows && TR_LOAD_OK(side, p, 4));
-                }
-                if (++at == g.blocks) {
-                    at = 0;
-                    tile += pairs;
+                if (!ok) {  // no load may land after the block has gone: they take microseconds
+                    const uint64_t t0 = ptx::global_timer_ns();
+                    for (uint32_t n = 0; n < 1u << 24 && ptx::global_timer_ns() - t0 < 2000000; ++n) {
+                    }
                 }
             }
-            ptx::cp_async_commit();
+        } else if (warp == 1) {
+            if (lane == 0 && rank == 0) {
+                const uint32_t idesc = ptx::f8_idesc(g.p_e5m2, g.q_e5m2, 256, 256);
+                int s = 0, b = 0;
+                uint32_t phase = 0, sums_phase = 1;
+                for (int64_t tile = pair; tile < tiles && ok; tile += pairs)
+                    for (int i = 0; i < g.blocks; ++i) {
+                        ok = ptx::mbar_wait_bounded(full + s, phase) && ptx::mbar_wait_bounded(sums_empty + b, sums_phase);
+                        if (!ok) break;
+                        ptx::tc_fence_after();
+                        const uint32_t at = ptx::smem_addr(stages + s * kPairStageBytes);
+                        const uint64_t dp = ptx::operand_desc(at), dq = ptx::operand_desc(at + kBytesP);
+                        const int used = s, into = b;
+                        if (++s == kPairStages) {
+                            s = 0;
+                            phase ^= 1;
+                        }
+                        b ^= 1;
+                        if (b == 0) sums_phase ^= 1;
+#pragma unroll
+                        for (int k = 0; k < kBlockK / 32; ++k)
+                            ptx::mma_f8_pair(tmem + into * 256, dp + 2 * k, dq + 2 * k, idesc, k > 0);
+                        ptx::mma_commit_pair(sums_full + into);
+                        ptx::mma_commit_pair(empty + used);
+                    }
+            }
+        } else {
+            // Scales, three blocks ahead: warp 2 those of P, warp 3 those of Q.
+            const bool of_p = warp == 2;
+            const float *base = of_p ? g.scale_p : g.scale_q;
+            const int64_t ld = of_p ? g.ld_p : g.ld_q, rows = of_p ? g.p : g.q;
+            const int shift = (of_p ? g.p_block : g.q_block) == 1 ? 0 : 7;  // 2^shift rows to a scale
+            // Scales to take, and the tile's rows from one to the next (block scales of P
+            // are taken once for each row, those of Q once for each 128 columns).
+            const int count = of_p ? 128 : QROW ? 256 : 2, apart = of_p || QROW ? 1 : 128;
+            [[maybe_unused]] const dbg::Side side = dbg::side(base, 1, g.blocks, (rows + (1 << shift) - 1) >> shift, ld, 0, 4);
+            float *ring = of_p ? &scales_p[0][0] : &scales_q[0][0];
+            const int pitch = of_p ? 128 : QROW ? 256 : 4;
+            // Blocks are counted through all tiles of this pair; the copies' cursor
+            // runs kScaleSlots - 1 ahead.
+            const int64_t mine = pair < tiles ? (tiles - 1 - pair) / pairs + 1 : 0, blocks = mine * g.blocks;
+            int64_t tile = pair, r0 = 0;
+            int at = 0;  // the cursor's block of its tile
+            for (int64_t n = -(kScaleSlots - 1); n < blocks; ++n) {
+                if (n >= 0) {
+                    ptx::cp_async_wait<kScaleSlots - 2>();  // block n's are here
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(scales_full + n % kScaleSlots);
+                }
+                const int64_t ahead = n + kScaleSlots - 1;
+                if (ahead < blocks) {
+                    if (ok && n >= 1) ok = ptx::mbar_wait_bounded(scales_empty + (n - 1) % kScaleSlots, (n - 1) / kScaleSlots & 1);
+                    if (at == 0) {
+                        int64_t p0, q0;
+                        tile_at(g, tile, kPairTile, kPairTile, 8, &p0, &q0);
+                        r0 = of_p ? p0 + rank * 128 : q0;
+                    }
+                    for (int k = lane; k < count; k += 32) {
+                        const int64_t r = r0 + k * apart;
+                        const float *p = base + at * ld + (r >> shift);
+                        ptx::cp_async_4_or_zero(ring + ahead % kScaleSlots * pitch + k, r < rows ? p : base,
+                                                r < rows && TR_LOAD_OK(side, p, 4));
+                    }
+                    if (++at == g.blocks) {
+                        at = 0;
+                        tile += pairs;
+                    }
+                }
+                ptx::cp_async_commit();
+            }
         }
-      }
     } else {
         ptx::registers_up<kManyRegisters>();
         const int w = warp & 3, group = (warp - 4) >> 2, r = w * 32 + lane;
