@@ -18,19 +18,21 @@
 //
 // Measured on one GB300 (a bf16 library product reaches 1920 TFLOP/s there; 8-bit
 // instructions run at twice its rate):
-//   8192^3, 1x128 by 128x128 scales, bf16 out        503 us, 2.19 PFLOP/s
-//   8192^3, 1x128 by 1x128                           663 us, 1.66 PFLOP/s
-//   4096 x 2048 x 16384, 1x128 by 1x128, fp32 out    192 us, 1.43 PFLOP/s
-//   2048^3                                            14 us, 1.20 PFLOP/s
-//   777 x 2049 x 1111                               12.8 us
-//   1 x 8192 x 8192                                 14.5 us, 4.6 TB/s of weights (68% of the copy rate)
+//   8192^3, 1x128 by 128x128 scales, bf16 out        437 us, 2.52 PFLOP/s
+//   8192^3, 1x128 by 1x128                           641 us, 1.72 PFLOP/s
+//   4096 x 2048 x 16384, 1x128 by 1x128, fp32 out    186 us, 1.48 PFLOP/s
+//   2048^3                                            14 us, 1.25 PFLOP/s
+//   777 x 2049 x 1111                               12.6 us
+//   1 x 8192 x 8192                                 14.4 us, 4.7 TB/s of weights (69% of the copy rate)
 //
 // What bounds the large ones is the exchange between the tensor cores and the warps
 // that take the sums out, once for each block of 128: the instructions alone run at
-// 250 us for 8192^3 from operands that are in place, at 322 us with the loads, and the
-// warps' work on a block (tensor memory to registers, 256 columns by 128 rows to an
-// SM) takes 380 cycles by itself, but a buffer of sums goes through both in turn, with
-// some 150 cycles of notice each way, and tensor memory holds two buffers.
+// 250 us for 8192^3 from operands that are in place, at 322 us with the loads, but a
+// warp's turn on a block takes 900 cycles in a row (its waits about 100 each, 400 for
+// four reads of 32 columns with the additions between them, the rest for the scales,
+// the hand back and the loop) and a buffer of sums, of which tensor memory holds
+// two, goes through instructions and warps in turn.  With a scale to each column it is the
+// multiplications and the reads of those scales: 1400 cycles.
 #include <atomic>
 
 #include "bounds.cuh"
@@ -281,26 +283,30 @@ k_matmul_fp8(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ 
                     ptx::mbar_wait_bounded(full + k % S::kStages, (k / S::kStages) & 1);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            const uint32_t idesc = ptx::f8_idesc(g.p_e5m2, g.q_e5m2, 128, BN);
-            for (int i = 0; i < count; ++i) {
-                const int s = i % S::kStages, b = i & 1;
-                ok = ptx::mbar_wait_bounded(full + s, (i / S::kStages) & 1) &&
-                     (i < 2 || ptx::mbar_wait_bounded(sums_empty + b, ((i >> 1) - 1) & 1));
-                if (!ok) break;
-                ptx::tc_fence_after();
-                const uint32_t at = ptx::smem_addr(stages + s * S::kStageBytes);
-                const uint64_t dp = ptx::operand_desc(at), dq = ptx::operand_desc(at + kBytesP);
+        // The whole warp goes through the loop and one elected lane issues, which leaves
+        // the descriptors in uniform registers: see k_matmul_pair.
+        const bool leader = ptx::elect_one();
+        const uint32_t idesc = ptx::f8_idesc(g.p_e5m2, g.q_e5m2, 128, BN);
+        for (int i = 0; i < count; ++i) {
+            const int s = i % S::kStages, b = i & 1;
+            ok = ptx::mbar_wait_bounded(full + s, (i / S::kStages) & 1) &&
+                 (i < 2 || ptx::mbar_wait_bounded(sums_empty + b, ((i >> 1) - 1) & 1));
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            const uint32_t at = ptx::smem_addr(stages + s * S::kStageBytes);
+            const uint64_t dp = ptx::operand_desc(at), dq = ptx::operand_desc(at + kBytesP);
+            if (leader) {
 #pragma unroll
                 for (int k = 0; k < kBlockK / 32; ++k)
                     ptx::mma_f8(tmem + b * BN, dp + 2 * k, dq + 2 * k, idesc, k > 0);
-                ptx::mma_commit(empty + s);
                 ptx::mma_commit(sums_full + b);
+                ptx::mma_commit(empty + s);
             }
-            if (!ok) {
-                ptx::mma_commit(&drained);
-                ptx::mbar_wait_bounded(&drained, 0);
-            }
+        }
+        if (!ok) {
+            if (leader) ptx::mma_commit(&drained);
+            ptx::mbar_wait_bounded(&drained, 0);
         }
     } else {
         const int w = warp & 3;                       // the quarter of the lanes this warp may read
@@ -417,6 +423,9 @@ constexpr int kPairThreads = 384;
 // 56 x 128 + 224 x 256 = 64512.
 constexpr int kFewRegisters = 56, kManyRegisters = 224;
 constexpr int kPairTile = 256;
+// Blocks whose scales come together, with one notice each way: 8192^3 takes 436 us with
+// batches of 8, 470 with a notice each way for every block.
+constexpr int kBatch = 8;
 constexpr int kPairStages = 5;
 constexpr int kPairStageBytes = 2 * kBytesP;       // 128 rows of P and 128 of Q
 constexpr int kStagingBytes = 8 * 32 * 128;        // 32 rows of 128 bytes to each of 8 warps
@@ -492,9 +501,10 @@ k_matmul_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__
               const __grid_constant__ Product g) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t full[kPairStages], empty[kPairStages], sums_full[2], sums_empty[2];
-    __shared__ uint64_t scales_full[kScaleSlots], scales_empty[kScaleSlots];
+    // Scales of two batches of blocks; one notice each way to a batch.
+    __shared__ uint64_t scales_full[2], scales_empty[2];
     __shared__ uint32_t tmem_base;
-    __shared__ alignas(16) float scales_p[kScaleSlots][128], scales_q[kScaleSlots][QROW ? 256 : 4];
+    __shared__ alignas(16) float scales_p[2 * kBatch][128], scales_q[2 * kBatch][QROW ? 256 : 4];
     uint8_t *stages = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint4 *staging = reinterpret_cast<uint4 *>(stages + kPairStages * kPairStageBytes);
@@ -512,7 +522,7 @@ k_matmul_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__
             ptx::mbar_init(sums_full + i, 1);
             ptx::mbar_init(sums_empty + i, 16);  // the warps of both CTAs
         }
-        for (int i = 0; i < kScaleSlots; ++i) {
+        for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(scales_full + i, 2);   // those of P and of Q
             ptx::mbar_init(scales_empty + i, 8);  // this CTA's warps
         }
@@ -562,13 +572,20 @@ k_matmul_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__
                 }
             }
         } else if (warp == 1) {
-            if (lane == 0 && rank == 0) {
+            if (rank == 0) {
+                // The whole warp goes through the loop and one elected lane issues: the
+                // compiler then keeps descriptors and addresses in uniform registers.
+                // Inside `lane == 0` alone the four instructions of a block took 350
+                // cycles to issue and the loop 1040, which bounded the kernel (8192^3:
+                // 503 us against 470); now they take 120.
+                const bool leader = ptx::elect_one();
                 const uint32_t idesc = ptx::f8_idesc(g.p_e5m2, g.q_e5m2, 256, 256);
                 int s = 0, b = 0;
                 uint32_t phase = 0, sums_phase = 1;
                 for (int64_t tile = pair; tile < tiles && ok; tile += pairs)
                     for (int i = 0; i < g.blocks; ++i) {
                         ok = ptx::mbar_wait_bounded(full + s, phase) && ptx::mbar_wait_bounded(sums_empty + b, sums_phase);
+                        ok = __all_sync(0xffffffffu, ok);
                         if (!ok) break;
                         ptx::tc_fence_after();
                         const uint32_t at = ptx::smem_addr(stages + s * kPairStageBytes);
@@ -580,15 +597,17 @@ k_matmul_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__
                         }
                         b ^= 1;
                         if (b == 0) sums_phase ^= 1;
+                        if (leader) {
 #pragma unroll
-                        for (int k = 0; k < kBlockK / 32; ++k)
-                            ptx::mma_f8_pair(tmem + into * 256, dp + 2 * k, dq + 2 * k, idesc, k > 0);
-                        ptx::mma_commit_pair(sums_full + into);
-                        ptx::mma_commit_pair(empty + used);
+                            for (int k = 0; k < kBlockK / 32; ++k)
+                                ptx::mma_f8_pair(tmem + into * 256, dp + 2 * k, dq + 2 * k, idesc, k > 0);
+                            ptx::mma_commit_pair(sums_full + into);
+                            ptx::mma_commit_pair(empty + used);
+                        }
                     }
             }
         } else {
-            // Scales, three blocks ahead: warp 2 those of P, warp 3 those of Q.
+            // Scales, a batch of blocks ahead: warp 2 those of P, warp 3 those of Q.
             const bool of_p = warp == 2;
             const float *base = of_p ? g.scale_p : g.scale_q;
             const int64_t ld = of_p ? g.ld_p : g.ld_q, rows = of_p ? g.p : g.q;
@@ -599,20 +618,13 @@ k_matmul_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__
             [[maybe_unused]] const dbg::Side side = dbg::side(base, 1, g.blocks, (rows + (1 << shift) - 1) >> shift, ld, 0, 4);
             float *ring = of_p ? &scales_p[0][0] : &scales_q[0][0];
             const int pitch = of_p ? 128 : QROW ? 256 : 4;
-            // Blocks are counted through all tiles of this pair; the copies' cursor
-            // runs kScaleSlots - 1 ahead.
+            // Blocks are counted through all tiles of this pair and copied by batches, one
+            // batch ahead of the one in use.
             const int64_t mine = pair < tiles ? (tiles - 1 - pair) / pairs + 1 : 0, blocks = mine * g.blocks;
             int64_t tile = pair, r0 = 0;
-            int at = 0;  // the cursor's block of its tile
-            for (int64_t n = -(kScaleSlots - 1); n < blocks; ++n) {
-                if (n >= 0) {
-                    ptx::cp_async_wait<kScaleSlots - 2>();  // block n's are here
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(scales_full + n % kScaleSlots);
-                }
-                const int64_t ahead = n + kScaleSlots - 1;
-                if (ahead < blocks) {
-                    if (ok && n >= 1) ok = ptx::mbar_wait_bounded(scales_empty + (n - 1) % kScaleSlots, (n - 1) / kScaleSlots & 1);
+            int at = 0;  // the next block's place in its tile
+            auto copy_batch = [&](int64_t first) {
+                for (int64_t n = first; n < first + kBatch && n < blocks; ++n) {
                     if (at == 0) {
                         int64_t p0, q0;
                         tile_at(g, tile, kPairTile, kPairTile, 8, &p0, &q0);
@@ -621,7 +633,7 @@ k_matmul_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__
                     for (int k = lane; k < count; k += 32) {
                         const int64_t r = r0 + k * apart;
                         const float *p = base + at * ld + (r >> shift);
-                        ptx::cp_async_4_or_zero(ring + ahead % kScaleSlots * pitch + k, r < rows ? p : base,
+                        ptx::cp_async_4_or_zero(ring + n % (2 * kBatch) * pitch + k, r < rows ? p : base,
                                                 r < rows && TR_LOAD_OK(side, p, 4));
                     }
                     if (++at == g.blocks) {
@@ -629,7 +641,20 @@ k_matmul_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__
                         tile += pairs;
                     }
                 }
-                ptx::cp_async_commit();
+            };
+            copy_batch(0);
+            int b = 0;           // of the batch in hand
+            uint32_t phase = 1;  // of the other buffer's release, which the first batch finds free
+            for (int64_t n = 0; n < blocks; n += kBatch) {
+                ptx::cp_async_wait_all();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(scales_full + b);
+                b ^= 1;
+                if (n + kBatch < blocks) {
+                    if (b == 0) phase ^= 1;
+                    if (ok) ok = ptx::mbar_wait_bounded(scales_empty + b, phase);
+                    copy_batch(n + kBatch);
+                }
             }
         }
     } else {
@@ -638,7 +663,7 @@ k_matmul_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__
         const uint32_t tsum = tmem + (uint32_t(w * 32) << 16) + group * 128;
         const uint32_t release[2] = {ptx::peer_addr(sums_empty, 0), ptx::peer_addr(sums_empty + 1, 0)};
         [[maybe_unused]] const dbg::Side so = dbg::side(g.out, 1, g.p, g.q, g.ld_out, 0, g.out_bf16 ? 2 : 4);
-        int b = 0, slot = 0;
+        int b = 0, slot = 0;  // slot: of the block's scales
         uint32_t phase = 0, slot_phase = 0;
         for (int64_t tile = pair; tile < tiles; tile += pairs) {
             int64_t p0, q0;
@@ -651,7 +676,7 @@ k_matmul_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__
             float v[2][32];
             for (int i = 0; i < g.blocks; ++i) {
                 // A wait that ran out is not repeated, but the arrivals go on.
-                if (ok) ok = ptx::mbar_wait_bounded(scales_full + slot, slot_phase);
+                if (slot % kBatch == 0 && ok) ok = ptx::mbar_wait_bounded(scales_full + slot / kBatch, slot_phase);
                 const float f = QROW ? scales_p[slot][r] : scales_p[slot][r] * scales_q[slot][group];
                 const float2 f2 = make_float2(f, f);
                 if (ok) ok = ptx::mbar_wait_bounded(sums_full + b, phase);
@@ -681,11 +706,13 @@ k_matmul_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__
                         a1 = __ffma2_rn(make_float2(v[c & 1][k + 2], v[c & 1][k + 3]), f23, a1);
                     }
                 }
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive_relaxed(scales_empty + slot);
-                if (++slot == kScaleSlots) {
-                    slot = 0;
-                    slot_phase ^= 1;
+                if (++slot % kBatch == 0) {
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive_relaxed(scales_empty + slot / kBatch - 1);
+                    if (slot == 2 * kBatch) {
+                        slot = 0;
+                        slot_phase ^= 1;
+                    }
                 }
                 b ^= 1;
                 if (b == 0) phase ^= 1;
