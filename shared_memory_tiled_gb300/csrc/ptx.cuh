@@ -81,6 +81,16 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// Four words of shared memory, kept in program order.
+__device__ __forceinline__ float4 load_shared_4(const float *p) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(smem_addr(p))
+                 : "memory");
+    return v;
+}
+
 // 16-byte asynchronous copy from global to shared memory, cached in L2 only;
 // complete (and visible to this thread) after cp_async_wait_all.
 __device__ __forceinline__ void cp_async_16(void *smem_dst, const void *gmem_src) {
