@@ -826,10 +826,12 @@ cudaError_t launch_matmul_fp8(const tr_matmul_fp8_args &a, const char **why) {
     }
     // Up to 64 rows of a: they are the columns of the tile, and b its 128 rows.
     const bool turn = a.m <= 64;
-// 256 x 256 tiles where they occupy five eighths of the CTA pairs: 1536 x 2048 x 8192
-    // (48 tiles) takes 38.8 us on them and 44.2 on 128 x 128 tiles, 777 x 2049 x 1111
-    // (36 tiles) 15.7 and 12.9.
-    const bool pair = !turn && ((a.m + 255) / 256) * ((a.n + 255) / 256) * 8 >= int64_t(sm_count() / 2) * 5;
+    // 256 x 256 tiles where 128 x 128 ones leave no room to split the contraction and no
+    // side is inside one of them: 1280 x 2048 x 4096 (160 small tiles) takes 20.5 us on
+    // the large and 26.4 on the small ones, 1280 x 1920 x 4096 (150) 24.7 and 18.6,
+    // 192 x 65536 x 4096 72.6 and 95.9, 128 x 65536 x 4096 72.2 and 57.9.
+    const bool pair = !turn && a.m > 128 && a.n > 128 &&
+                      ((a.m + 127) / 128) * ((a.n + 127) / 128) > int64_t(sm_count());
     const int bn = pair ? 256 : !turn ? 128 : a.m <= 16 ? 16 : a.m <= 32 ? 32 : 64;
     Product g{};
     g.scale_p = turn ? a.scale_b : a.scale_a;
