@@ -18,12 +18,12 @@
 //
 // Measured on one GB300 (a bf16 library product reaches 1920 TFLOP/s there; 8-bit
 // instructions run at twice its rate):
-//   8192^3, 1x128 by 128x128 scales, bf16 out        437 us, 2.52 PFLOP/s
-//   8192^3, 1x128 by 1x128                           624 us, 1.76 PFLOP/s
-//   4096 x 2048 x 16384, 1x128 by 1x128, fp32 out    181 us, 1.52 PFLOP/s
+//   8192^3, 1x128 by 128x128 scales, bf16 out        435 us, 2.53 PFLOP/s
+//   8192^3, 1x128 by 1x128                           620 us, 1.77 PFLOP/s
+//   4096 x 2048 x 16384, 1x128 by 1x128, fp32 out    180 us, 1.53 PFLOP/s
 //   2048^3                                            14 us, 1.25 PFLOP/s
 //   777 x 2049 x 1111                               12.6 us
-//   1 x 8192 x 8192                                 14.4 us, 4.7 TB/s of weights (69% of the copy rate)
+//   1 x 8192 x 8192                                 14.3 us, 4.7 TB/s of weights (69% of the copy rate)
 //
 // What bounds the large ones is the exchange between the tensor cores and the warps
 // that take the sums out, once for each block of 128: the instructions alone run at
@@ -680,7 +680,7 @@ k_matmul_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__
                 const float f = QROW ? scales_p[slot][r] : scales_p[slot][r] * scales_q[slot][group];
                 const float2 f2 = make_float2(f, f);
                 // Scales of the next 8 columns, read in this order: left to itself the
-                // compiler reads each where it is used (8192^3: 641 us against 624; 16
+                // compiler reads each where it is used (8192^3: 640 us against 620; 16
                 // columns ahead 637).
                 [[maybe_unused]] float4 q_next[2];
                 if constexpr (QROW) {
