@@ -362,7 +362,8 @@ typedef struct tr_layernorm_args {
  *
  * The deviations are summed about the row's own mean (a large offset costs no
  * accuracy), in 32 bits; y is rounded once.  A negative, infinite or NaN eps
- * returns TR_ERR_BAD_DIM. */
+ * returns TR_ERR_BAD_DIM.  Without columns nothing is written, mean and rstd
+ * included. */
 tr_status tr_layernorm(const tr_layernorm_args *args);
 
 /* Arguments of tr_layernorm_backward.  Zero-initialise. */

@@ -590,9 +590,9 @@ def layernorm(x, gamma, beta=None, *, eps=1e-5, out=None, stream=None):
     """Layer norm over the rows of a CUDA matrix (fp32 or bf16).
 
     Returns ``(y, mean, rstd)``: y of x's type (``out`` if given), the rows'
-    means and reciprocal deviations in fp32 for ``layernorm_backward``.
-    ``gamma`` and ``beta`` are fp32 or bf16, both the same.  ``stream`` (a
-    cudaStream_t): default torch's current stream.
+    means and reciprocal deviations in fp32 for ``layernorm_backward`` (NaN for a
+    matrix of no columns).  ``gamma`` and ``beta`` are fp32 or bf16, both the
+    same.  ``stream`` (a cudaStream_t): default torch's current stream.
     """
     if stream is not None:
         return _on(stream, x, lambda: layernorm(x, gamma, beta, eps=eps, out=out))
@@ -608,6 +608,9 @@ def layernorm(x, gamma, beta=None, *, eps=1e-5, out=None, stream=None):
     out, ld_y = _like(out, x, rows, cols, dev)
     empty, f32 = torch.empty, torch.float32
     mean, rstd = empty(rows, dtype=f32, device=dev), empty(rows, dtype=f32, device=dev)
+    if not cols:  # the library launches nothing; the statistics of no values are 0 / 0
+        mean.fill_(float("nan"))
+        rstd.fill_(float("nan"))
     _run("tr_layernorm", LayernormArgs(
         x.data_ptr(), gamma.data_ptr(), None if beta is None else beta.data_ptr(), out.data_ptr(),
         mean.data_ptr(), rstd.data_ptr(), xk, wk, rows, cols, ld, ld_y, eps, 0), dev)
