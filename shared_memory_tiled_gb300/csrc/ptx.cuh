@@ -99,7 +99,8 @@ __device__ __forceinline__ void cp_async_16(void *smem_dst, const void *gmem_src
                  : "memory");
 }
 
-// The first `bytes` (0 to 16) of it; the rest of the 16 is zeroed.
+// The first `bytes` (1 to 16) of it, the rest of the 16 zeroed; the source is on a 16-byte
+// boundary whatever their number.
 __device__ __forceinline__ void cp_async_16_or_zero(void *smem_dst, const void *gmem_src, int bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(smem_dst)),
                  "l"(gmem_src), "r"(bytes)

@@ -22,6 +22,7 @@
 #include <atomic>
 
 #include "bounds.cuh"
+#include "granule.cuh"
 #include "launch.cuh"
 #include "ptx.cuh"
 #include "tr_internal.h"
@@ -83,10 +84,9 @@ constexpr size_t kTileBytes[3] = {0, size_t(128) * kWordPitch * 4, size_t(128) *
 __device__ __forceinline__ void copy_granule(uint32_t *dst, const __nv_bfloat16 *row, int64_t col, int64_t cols,
                                              const dbg::Side &s) {
     if (col >= 0) {
-        const int64_t left = cols - col;
-        const int bytes = left <= 0 ? 0 : left < 8 ? int(left) * 2 : 16;
-        const bool ok = bytes && TR_LOAD_OK(s, row + col, bytes);
-        ptx::cp_async_16_or_zero(dst, ok ? row + col : row, ok ? bytes : 0);
+        const GranulePart p = granule_part(row, col, cols);
+        if (p.src && TR_LOAD_OK(s, p.src, p.bytes)) ptx::cp_async_16_or_zero(dst, p.src, p.bytes);
+        else *reinterpret_cast<uint4 *>(dst) = make_uint4(0u, 0u, 0u, 0u);
     } else {
         __nv_bfloat16 *e = reinterpret_cast<__nv_bfloat16 *>(dst);
 #pragma unroll
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) k_quantize(c
         } else if constexpr (LOAD == kGranules) {
             uint32_t *granules = reinterpret_cast<uint32_t *>(shared_tile) + warp * 16 * kGranulePitch;
             const T *first = x + (tr * 128 + warp * 16) * a.ld_x;  // the warp's first row
-            auto shift = [&](int r) { return uint32_t(reinterpret_cast<uintptr_t>(first + r * a.ld_x + tc * 128) & 15u); };
+            auto shift = [&](int r) { return granule_shift(first + r * a.ld_x + tc * 128); };
             auto copy = [&](int r, int granule) {
                 uint32_t *dst = granules + r * kGranulePitch + granule * 4;
                 if (tr * 128 + warp * 16 + r < a.rows)
