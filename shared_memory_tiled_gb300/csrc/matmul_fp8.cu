@@ -37,6 +37,7 @@
 
 #include "bounds.cuh"
 #include "launch.cuh"
+#include "operand_ring.cuh"
 #include "row_chunk.cuh"
 #include "tcgen05.cuh"
 #include "tensor_map.cuh"
@@ -278,9 +279,11 @@ k_matmul_fp8(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ 
                 ptx::tma_load_2d(dst, &map_p, full + s, (first + i) * kBlockK, int32_t(p0));
                 ptx::tma_load_2d(dst + kBytesP, &map_q, full + s, (first + i) * kBlockK, int32_t(q0));
             }
-            if (!ok)  // no load may land after the block has gone
-                for (int k = i > S::kStages ? i - S::kStages : 0; k < i; ++k)
-                    ptx::mbar_wait_bounded(full + k % S::kStages, (k / S::kStages) & 1);
+            // Nothing may arrive after the block has gone.
+            if (!leave_ring<S::kStages>(
+                    i, [&](int s, uint32_t parity) { return ptx::mbar_wait_bounded(empty + s, parity); },
+                    [&](int s, uint32_t parity) { ptx::mbar_wait_bounded(full + s, parity); }))
+                ok = false;
         }
     } else if (warp == 1) {
         // The whole warp goes through the loop and one elected lane issues, which leaves
@@ -363,6 +366,7 @@ k_matmul_fp8(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ 
                 }
             }
         }
+        ptx::cp_async_wait_all();
         // The sums go through shared memory (the stages are free: every product is
         // complete) so that lanes write neighbouring words of the output.
         float *red = reinterpret_cast<float *>(stages);
@@ -545,6 +549,7 @@ k_matmul_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__
         if (warp == 0) {
             if (lane == 0) {
                 int s = 0;
+                int64_t filled = 0;
                 uint32_t phase = 1;  // the first round finds every stage empty
                 for (int64_t tile = pair; tile < tiles && ok; tile += pairs) {
                     int64_t p0, q0;
@@ -559,13 +564,22 @@ k_matmul_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__
                         const uint32_t bar = ptx::peer_addr(full + s, 0);
                         ptx::tma_load_2d_pair(dst, &map_p, bar, i * kBlockK, int32_t(p0) + int32_t(rank) * 128);
                         ptx::tma_load_2d_pair(dst + kBytesP, &map_q, bar, i * kBlockK, int32_t(q0) + int32_t(rank) * 128);
+                        ++filled;
                         if (++s == kPairStages) {
                             s = 0;
                             phase ^= 1;
                         }
                     }
                 }
-                if (!ok) {  // no load may land after the block has gone: they take microseconds
+                // Nothing may arrive after the block has gone: the commits come to both CTAs,
+                // each waits for its own.
+                if (!leave_ring<kPairStages>(
+                        filled, [&](int st, uint32_t parity) { return ptx::mbar_wait_bounded(empty + st, parity); },
+                        [](int, uint32_t) {}))
+                    ok = false;
+                // Where one does not come there may be loads in flight, which complete on rank 0's
+                // barriers: both CTAs give them many times the microseconds that they take.
+                if (!ok) {
                     const uint64_t t0 = ptx::global_timer_ns();
                     for (uint32_t n = 0; n < 1u << 24 && ptx::global_timer_ns() - t0 < 2000000; ++n) {
                     }
