@@ -732,7 +732,7 @@ k_matmul_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__
                 }
                 if (++slot % kBatch == 0) {
                     __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive_relaxed(scales_empty + slot / kBatch - 1);
+                    if (lane == 0) ptx::mbar_arrive(scales_empty + slot / kBatch - 1);  // its reads are done
                     if (slot == 2 * kBatch) {
                         slot = 0;
                         slot_phase ^= 1;
