@@ -38,6 +38,7 @@
 #include "bounds.cuh"
 #include "launch.cuh"
 #include "operand_ring.cuh"
+#include "register_split.cuh"
 #include "row_chunk.cuh"
 #include "tcgen05.cuh"
 #include "tensor_map.cuh"
@@ -422,10 +423,6 @@ k_matmul_fp8(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ 
 // shared memory; else one scale for the group's columns, and one multiplication
 // fewer to each value.
 
-constexpr int kPairThreads = 384;
-// Registers at launch (168 x 384 = 64512), and how the warpgroups share them:
-// 56 x 128 + 224 x 256 = 64512.
-constexpr int kFewRegisters = 56, kManyRegisters = 224;
 constexpr int kPairTile = 256;
 // Blocks whose scales come together, with one notice each way: 8192^3 takes 436 us with
 // batches of 8, 470 with a notice each way for every block.
@@ -812,7 +809,18 @@ cudaError_t launch_shape(const CUtensorMap &map_p, const CUtensorMap &map_q, con
 template <bool QROW>
 cudaError_t launch_pair(const CUtensorMap &map_p, const CUtensorMap &map_q, const Product &g,
                         cudaStream_t stream) {
-    static std::atomic<bool> opted[64];
+    static std::atomic<bool> opted[64], checked[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!checked[dev].load(std::memory_order_acquire)) {
+        cudaFuncAttributes attr;
+        e = cudaFuncGetAttributes(&attr, k_matmul_pair<QROW>);
+        if (e != cudaSuccess) return e;
+        if (!registers_suffice(attr.numRegs)) return cudaErrorLaunchOutOfResources;
+        checked[dev].store(true, std::memory_order_release);
+    }
     const int64_t pairs = sm_count() / 2, tiles = g.tiles_p * g.tiles_q;
     return launch_kernel(k_matmul_pair<QROW>, opted, 2 * (tiles < pairs ? tiles : pairs), kPairThreads, kPairSmem, 2,
                          map_p, map_q, g, stream);
