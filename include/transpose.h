@@ -427,16 +427,18 @@ tr_status tr_plan_ex(const tr_args *args, const tr_options *opts, tr_plan *plan)
 
 /* Reads and clears the device-side fault flag of the CURRENT device after
  * synchronizing it: TR_ERR_TIMEOUT if a bounded in-kernel wait ran out since
- * the last call, TR_OK otherwise (TR_ERR_CUDA if the read itself fails). */
+ * the last call, TR_OK otherwise (TR_ERR_CUDA if the read itself fails).
+ * tr_last_error() then names the kernels that raised it: transpose, matmul_fp8,
+ * layernorm_backward. */
 tr_status tr_device_status(void);
 
 /* Exercises the failure path of the bounded in-kernel waits without any
- * fault: one warp waits on an mbarrier phase that completes only when
- * `arrive` is nonzero.  With arrive == 0 the wait runs out after limit_ns
- * nanoseconds (1 ns .. 2 s, else TR_ERR_BAD_DIM), the kernel raises the same
- * device fault flag the transpose kernels raise and returns, so a following
- * tr_device_status() reports TR_ERR_TIMEOUT; with arrive != 0 it reports TR_OK.
- * Asynchronous on `stream`. */
+ * fault: for each unit whose kernels wait, one after another, one warp waits on
+ * an mbarrier phase that completes only when `arrive` is nonzero.  With
+ * arrive == 0 the wait runs out after limit_ns nanoseconds (1 ns .. 2 s, else
+ * TR_ERR_BAD_DIM), the kernel raises the same device fault flag the unit's
+ * kernels raise and returns, so a following tr_device_status() reports
+ * TR_ERR_TIMEOUT; with arrive != 0 it reports TR_OK.  Asynchronous on `stream`. */
 tr_status tr_selftest_bounded_wait(int32_t arrive, int64_t limit_ns, tr_stream_t stream);
 
 /* Record of the bounds checks of a debug build (see tr_debug_bounds). */

@@ -434,8 +434,10 @@ int32_t tr_plan_variant(const tr_args *args, const tr_options *opts) {
 
 tr_status tr_selftest_bounded_wait(int32_t arrive, int64_t limit_ns, tr_stream_t stream) {
     if (limit_ns <= 0 || limit_ns > 2000000000LL) return TR_ERR_BAD_DIM;
-    const cudaError_t e =
-        tr::launch_wait_selftest(arrive != 0, limit_ns, reinterpret_cast<cudaStream_t>(stream));
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e = tr::launch_wait_selftest(arrive != 0, limit_ns, s);
+    if (e == cudaSuccess) e = tr::launch_wait_selftest_matmul(arrive != 0, limit_ns, s);
+    if (e == cudaSuccess) e = tr::launch_wait_selftest_layernorm(arrive != 0, limit_ns, s);
     if (e != cudaSuccess) {
         tr::set_error("self-test launch failed", e);
         return TR_ERR_CUDA;
@@ -452,7 +454,10 @@ tr_status tr_device_status(void) {
         tr::set_error("reading the device fault flag failed", e);
         return TR_ERR_CUDA;
     }
-    return v | w | u ? TR_ERR_TIMEOUT : TR_OK;
+    if (!(v | w | u)) return TR_OK;
+    const std::string units = std::string(v ? " transpose" : "") + (w ? " matmul_fp8" : "") + (u ? " layernorm_backward" : "");
+    tr::set_error(("a bounded wait ran out in:" + units).c_str(), cudaSuccess);
+    return TR_ERR_TIMEOUT;
 }
 
 tr_status tr_debug_bounds(tr_bounds_report *report) {

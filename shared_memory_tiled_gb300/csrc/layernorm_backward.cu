@@ -20,6 +20,7 @@
 #include "ptx.cuh"
 #include "row_chunk.cuh"
 #include "tr_internal.h"
+#include "wait_selftest.cuh"
 
 namespace tr {
 
@@ -486,6 +487,10 @@ cudaError_t launch_typed(Bwd a, cudaStream_t stream) {
     return e == cudaSuccess ? launch_join(a, stream) : e;
 }
 
+__global__ void k_wait_selftest_layernorm(int arrive, uint64_t limit_ns) {
+    wait_selftest(&g_fault_flag_layernorm, arrive, limit_ns);
+}
+
 }  // namespace
 
 // Debug builds: this unit's record of refused accesses.
@@ -502,6 +507,11 @@ cudaError_t launch_layernorm_backward(const tr_layernorm_backward_args &p) {
           static_cast<float *>(p.workspace), p.rows, p.cols, p.ld_dy, p.ld_x, p.ld_dx,
           0, 0, p.w_dtype == TR_DTYPE_BF16};
     return p.x_dtype == TR_DTYPE_F32 ? launch_typed<float>(a, stream) : launch_typed<__nv_bfloat16>(a, stream);
+}
+
+cudaError_t launch_wait_selftest_layernorm(bool arrive, int64_t limit_ns, cudaStream_t stream) {
+    k_wait_selftest_layernorm<<<1, 32, 0, stream>>>(arrive ? 1 : 0, uint64_t(limit_ns));
+    return cudaGetLastError();
 }
 
 cudaError_t read_and_clear_fault_layernorm(unsigned *value) {

@@ -43,6 +43,7 @@
 #include "tcgen05.cuh"
 #include "tensor_map.cuh"
 #include "tr_internal.h"
+#include "wait_selftest.cuh"
 
 namespace tr {
 
@@ -826,10 +827,19 @@ cudaError_t launch_pair(const CUtensorMap &map_p, const CUtensorMap &map_q, cons
                          map_p, map_q, g, stream);
 }
 
+__global__ void k_wait_selftest_matmul(int arrive, uint64_t limit_ns) {
+    wait_selftest(&g_fault_flag_matmul, arrive, limit_ns);
+}
+
 }  // namespace
 
 // Debug builds: this unit's record of refused accesses.
 TR_BOUNDS_READER(read_bounds_matmul_fp8)
+
+cudaError_t launch_wait_selftest_matmul(bool arrive, int64_t limit_ns, cudaStream_t stream) {
+    k_wait_selftest_matmul<<<1, 32, 0, stream>>>(arrive ? 1 : 0, uint64_t(limit_ns));
+    return cudaGetLastError();
+}
 
 cudaError_t read_and_clear_fault_matmul(unsigned *value) {
     cudaError_t e = cudaMemcpyFromSymbol(value, g_fault_flag_matmul, sizeof(unsigned));

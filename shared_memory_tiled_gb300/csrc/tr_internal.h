@@ -66,7 +66,10 @@ cudaError_t launch_inplace(void *data, int esize, int64_t batch, int64_t n, int6
 
 // One warp waiting on an mbarrier that completes only when `arrive` is set;
 // otherwise the bounded wait runs out after limit_ns and raises the fault flag.
+// Each unit whose kernels wait has one, and raises its own flag.
 cudaError_t launch_wait_selftest(bool arrive, int64_t limit_ns, cudaStream_t stream);
+cudaError_t launch_wait_selftest_matmul(bool arrive, int64_t limit_ns, cudaStream_t stream);
+cudaError_t launch_wait_selftest_layernorm(bool arrive, int64_t limit_ns, cudaStream_t stream);
 
 // Device-side fault flag (bounded waits that ran out).  Reads and clears it;
 // the units of the linear layer keep one of their own each (read after it).
