@@ -332,11 +332,15 @@ typedef struct tr_matmul_fp8_args {
  *
  * Products and sums are held in 32 bits on the tensor cores within a block,
  * in 32-bit registers across blocks, and rounded once to the output's type;
- * with `accumulate` the output's old value is added in 32 bits first.  The
- * order of the sums is fixed for a call's arguments on a device, so equal calls
- * give equal bits.  a and b are 16-byte aligned with pitches that are multiples of 16
- * (else TR_ERR_UNSUPPORTED); m, n and k are below 2^31.  k = 0 gives zeros
- * (or leaves out as it is, with `accumulate`). */
+ * with `accumulate` the output's old value is added in 32 bits first.  A
+ * block's term leaves the normal numbers of 32 bits only if all three factors
+ * together do, not where scale_a * scale_b alone does.  (Left out are a block's
+ * scales of one operand that lie more than 2^190 apart, and blocks of magnitudes
+ * up to 2^-100, whose scale is that of zeros.)  The order of the sums
+ * is fixed for a call's arguments on a device, so equal calls give equal bits.
+ * a and b are 16-byte aligned with pitches that are multiples of 16 (else
+ * TR_ERR_UNSUPPORTED); m, n and k are below 2^31.  k = 0 gives zeros (or
+ * leaves out as it is, with `accumulate`). */
 tr_status tr_matmul_fp8(const tr_matmul_fp8_args *args);
 
 /* Arguments of tr_layernorm.  Zero-initialise. */
@@ -391,8 +395,8 @@ typedef struct tr_layernorm_backward_args {
  *
  * The sums down the rows are held in 32 bits and joined in an order that is
  * fixed for a call's arguments on a device (no atomics), so equal calls give
- * equal bits.  Nothing needs clearing before the call.  TR_ERR_UNSUPPORTED for a workspace that is too
- * small or misaligned. */
+ * equal bits; without rows they are zero.  Nothing needs clearing before the
+ * call.  TR_ERR_UNSUPPORTED for a workspace that is too small or misaligned. */
 tr_status tr_layernorm_backward(const tr_layernorm_backward_args *args);
 
 /* Bytes of workspace that tr_layernorm_backward needs for these sizes on any

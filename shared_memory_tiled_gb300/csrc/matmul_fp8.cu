@@ -34,6 +34,7 @@
 // two, goes through instructions and warps in turn.  With a scale to each column it is the
 // multiplications and the reads of those scales: 1400 cycles.
 #include <atomic>
+#include <type_traits>
 
 #include "bounds.cuh"
 #include "launch.cuh"
@@ -57,7 +58,6 @@ constexpr int kBlockK = 128;             // bytes, values and the scales' block
 constexpr int kTileP = 128;
 constexpr int kBytesP = kTileP * kBlockK;
 
-constexpr int kScaleSlots = 4;          // blocks whose scales are in shared memory
 constexpr int kSumPitch = 132;           // words to a row of a tile's sums in shared memory
 
 template <int BN>
@@ -69,6 +69,11 @@ struct Shape {
     static constexpr int kPerSm = BN == 16 ? 4 : 2;
     static constexpr int kStages = BN == 16 ? 2 : BN == 128 ? 3 : BN == 64 ? 4 : 5;
     static constexpr int kColumns = 2 * BN;  // two buffers of sums
+    // Blocks whose scales are in shared memory or on their way.  Four to the small tile, whose
+    // few blocks would wait for the first copies (1 x 4096 x 4096: 7.5 us, 7.7 with
+    // eight); with four the larger ones wait for a block's copies (32 x 8192 x 8192:
+    // 17.3 us, 16.4 with eight).
+    static constexpr int kScaleSlots = BN == 16 ? 4 : 8;
     static constexpr size_t kSmem = 1024 + size_t(kStages) * kStageBytes;
 };
 
@@ -83,17 +88,22 @@ struct Product {
     int32_t p_block, q_block;            // rows to a scale: 1 or 128
     int32_t p_e5m2, q_e5m2;
     int32_t out_bf16, accumulate;
+    // The least scale that the quantizer gives, which is that of a block of zeros: the sums
+    // with it are zero, whatever the factor, or those of magnitudes up to 2^-100.
+    float floor_p, floor_q;
 };
 
 // Rows of P and of Q at which a tile of bp x bq begins; `most` tiles of P go with
 // each tile of Q before the next, so that the operands in use at one time stay
-// in L2.
-__device__ __forceinline__ void tile_at(const Product &g, int64_t tile, int bp, int bq, int most,
+// in L2.  In 32 bits: there are fewer than 2^31 tiles, and a 64-bit division is a call, around
+// which k_matmul_pair's warps with few registers would spill.
+__device__ __forceinline__ void tile_at(const Product &g, int64_t tile, int bp, int bq, uint32_t most,
                                         int64_t *p0, int64_t *q0) {
-    const int64_t group = tile / (most * g.tiles_q), at = tile - group * most * g.tiles_q;
-    const int64_t left = g.tiles_p - group * most, tall = left < most ? left : most;
-    *p0 = (group * most + at % tall) * bp;
-    *q0 = at / tall * bq;
+    const uint32_t tiles_p = uint32_t(g.tiles_p), tiles_q = uint32_t(g.tiles_q);
+    const uint32_t group = uint32_t(tile) / (most * tiles_q), at = uint32_t(tile) - group * most * tiles_q;
+    const uint32_t left = tiles_p - group * most, tall = left < most ? left : most;
+    *p0 = int64_t(group * most + at % tall) * bp;
+    *q0 = int64_t(at / tall) * bq;
 }
 
 // out[i][j] = v, or += v; `s` is the output's logical extent.
@@ -133,6 +143,69 @@ __device__ __forceinline__ void put4(const Product &g, int64_t i, int64_t j, flo
         if (g.accumulate) old = *o;
         *o = make_float4(v[0] + old.x, v[1] + old.y, v[2] + old.z, v[3] + old.w);
     }
+}
+
+// Least (zeros left out) and largest magnitude of some scales, as bits, which order alike
+// (a NaN is the largest); `least` one lower, so that a zero is the largest number there.
+struct ScaleRange {
+    uint32_t below_least, most;
+    __device__ __forceinline__ void add(float v) {
+        const uint32_t m = __float_as_uint(v) & 0x7fffffffu;
+        below_least = min(below_least, m - 1);
+        most = max(most, m);
+    }
+    __device__ __forceinline__ void add_but(float floor, float v) {
+        if (v != floor) add(v);
+    }
+    __device__ __forceinline__ void join_warp() {
+        below_least = __reduce_min_sync(0xffffffffu, below_least);
+        most = __reduce_max_sync(0xffffffffu, most);
+    }
+    __device__ __forceinline__ float least() const { return __uint_as_float(below_least + 1); }
+    __device__ __forceinline__ float largest() const { return __uint_as_float(most); }
+};
+constexpr uint32_t kNoneYet = 0x7f7fffffu;  // below infinity: no factor is small with it
+
+// Whether the product of two scales of these ranges may leave the normal numbers of 32 bits.
+__device__ __forceinline__ bool out_of_range(const ScaleRange &a, const ScaleRange &b) {
+    return a.largest() * b.largest() > 3.402823466e38f || a.least() * b.least() < 1.175494351e-38f;
+}
+
+// A row's scale where its product with the columns' scales leaves the normal numbers:
+// block sums are below 2^39 and, if not zero, above 2^-33, so sums times two such scales
+// may well be finite, and zero times both is zero.  A power of two then moves from the
+// scale to `pre`, which multiplies the sums first; both steps are exact while a block's
+// column scales are within 2^190 of one another.  Elsewhere `pre` is 1.  The bits are
+// those of the plain factor wherever that is in range.
+//
+// Such blocks have a loop of their own, and what finds them stays out of the way of the
+// warps that add: in the pair kernel the warps that copy the scales take a batch's range
+// (and copy with few instructions, since a late batch stops everything), in the other
+// each thread looks at its own two scales a block ahead.  A look at the block in hand,
+// with both forms of the sum behind a branch, took 8192^3 from 433 to 477 us (1x128 by
+// 1x128: 621 to 727); so it is 428 (600).  Blocks of zeros, as masked rows have, do not
+// count: with them a tenth of the rows zero in e5m2 took 591 us, without 430.
+struct RowScale {
+    float f, pre;
+};
+__device__ __forceinline__ RowScale row_scale(float sp, float floor, const ScaleRange &q) {
+    const float m = fabsf(sp);
+    if (m * q.largest() > 3.402823466e38f) return RowScale{sp * 0x1p-60f, 0x1p60f};
+    if (m != 0.0f && m != floor && m * q.least() < 1.175494351e-38f) return RowScale{sp * 0x1p60f, 0x1p-60f};
+    return RowScale{sp, 1.0f};
+}
+// The range of N columns' scales (0: of the one that they share), for row_scale.
+template <int N>
+__device__ __forceinline__ ScaleRange column_range(const float *q, float floor, int lane) {
+    ScaleRange r{kNoneYet, 0};
+    if constexpr (N == 0) {
+        r.add_but(floor, q[0]);
+    } else {
+#pragma unroll
+        for (int c = lane; c < N; c += 32) r.add_but(floor, q[c]);
+        r.join_warp();
+    }
+    return r;
 }
 
 // Adds up the sums of a tile that SPLIT CTAs left in shared memory, in rank order, and
@@ -225,9 +298,9 @@ k_matmul_fp8(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ 
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t full[S::kStages], empty[S::kStages], sums_full[2], sums_empty[2], drained;
     __shared__ uint32_t tmem_base;
-    // Scales, three blocks ahead: each of the 128 threads copies its row's of P and one
+    // Scales, all slots but one ahead: each of the 128 threads copies its row's of P and one
     // of Q (QROW: a column's; else all the same one, each its own copy).
-    __shared__ alignas(16) float scales_p[kScaleSlots][128], scales_q[kScaleSlots][128];
+    __shared__ alignas(16) float scales_p[S::kScaleSlots][128], scales_q[S::kScaleSlots][128];
     uint8_t *stages = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
@@ -325,18 +398,37 @@ k_matmul_fp8(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ 
         auto copy_scales = [&](int i) {
             const float *p = sp + int64_t(first + i) * g.ld_p, *q = sq + int64_t(first + i) * g.ld_q;
             const bool now = i < count;
-            ptx::cp_async_4_or_zero(&scales_p[i % kScaleSlots][th], now && has_p ? p : g.scale_p, now && has_p && TR_LOAD_OK(side_p, p, 4));
-            ptx::cp_async_4_or_zero(&scales_q[i % kScaleSlots][th], now && has_q ? q : g.scale_q, now && has_q && TR_LOAD_OK(side_q, q, 4));
+            ptx::cp_async_4_or_zero(&scales_p[i % S::kScaleSlots][th], now && has_p ? p : g.scale_p, now && has_p && TR_LOAD_OK(side_p, p, 4));
+            ptx::cp_async_4_or_zero(&scales_q[i % S::kScaleSlots][th], now && has_q ? q : g.scale_q, now && has_q && TR_LOAD_OK(side_q, q, 4));
             ptx::cp_async_commit();
         };
-        for (int i = 0; i < kScaleSlots - 1; ++i) copy_scales(i);
-        for (int i = 0; i < count; ++i) {
-            const int b = i & 1, slot = i % kScaleSlots;
-            ptx::cp_async_wait<kScaleSlots - 2>();  // this thread's copies for block i are here
-            if (QROW) ptx::named_sync(1, 128);      // and everybody's; block i - 1's are read
-            const float f = QROW ? scales_p[slot][th] : scales_p[slot][th] * scales_q[slot][th];
+        for (int i = 0; i < S::kScaleSlots - 1; ++i) copy_scales(i);
+        // Whether block i's factors may leave the range, from this thread's own two scales:
+        // by their product, or (QROW, where each meets the others') one by one.
+        auto strays = [&](int i) {
+            const float a = fabsf(scales_p[i % S::kScaleSlots][th]), b = fabsf(scales_q[i % S::kScaleSlots][th]);
+            const bool some_a = a != 0.0f && a != g.floor_p, some_b = b != 0.0f && b != g.floor_q;
+            if constexpr (QROW) return a > 0x1p63f || b > 0x1p63f || (a < 0x1p-63f && some_a) || (b < 0x1p-63f && some_b);
+            return a * b > 3.402823466e38f || (a * b < 1.175494351e-38f && some_a && some_b);
+        };
+        ptx::cp_async_wait<S::kScaleSlots - 2>();
+        bool apart = QROW ? ptx::named_any(1, 128, strays(0)) : __any_sync(0xffffffffu, strays(0));
+        // Adds block i's sums; `first`: with factors that may leave the range.
+        auto take = [&](int i, auto first) {
+            const int b = i & 1, slot = i % S::kScaleSlots;
+            ptx::cp_async_wait<S::kScaleSlots - 3>();  // this thread's copies for block i + 1 are here
+            // Everybody's are, and block i - 1's are read.
+            if constexpr (QROW) apart = ptx::named_any(1, 128, strays(i + 1));
+            const float own_p = scales_p[slot][th], all_q = QROW ? 1.0f : scales_q[slot][th];
+            float f = own_p * all_q;
+            [[maybe_unused]] float pre = 1.0f;
+            if constexpr (decltype(first)::value) {
+                const RowScale own = row_scale(own_p, g.floor_p, column_range<QROW ? BN : 0>(&scales_q[slot][QROW ? 0 : th], g.floor_q, lane));
+                f = own.f * all_q;
+                pre = own.pre;
+            }
             const float2 f2 = make_float2(f, f);
-            copy_scales(i + kScaleSlots - 1);
+            copy_scales(i + S::kScaleSlots - 1);
             // A wait that ran out is not repeated, but the meetings go on.
             if (ok) ok = ptx::mbar_wait_bounded(sums_full + b, (i >> 1) & 1);
             __syncwarp();
@@ -354,6 +446,14 @@ k_matmul_fp8(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ 
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive_relaxed(sums_empty + b);
                 }
+                if constexpr (decltype(first)::value) {
+#pragma unroll
+                    for (int k = 0; k < 16; k += 2) {
+                        const float2 two = __fmul2_rn(make_float2(v[c & 1][k], v[c & 1][k + 1]), make_float2(pre, pre));
+                        v[c & 1][k] = two.x;
+                        v[c & 1][k + 1] = two.y;
+                    }
+                }
 #pragma unroll
                 for (int k = 0; k < 16; k += 4) {
                     float2 f01 = f2, f23 = f2;
@@ -367,7 +467,11 @@ k_matmul_fp8(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ 
                     a1 = __ffma2_rn(make_float2(v[c & 1][k + 2], v[c & 1][k + 3]), f23, a1);
                 }
             }
-        }
+            if constexpr (!QROW && !decltype(first)::value) apart = __any_sync(0xffffffffu, strays(i + 1));
+        };
+        int i = 0;
+        for (; i < count && !apart; ++i) take(i, std::false_type());
+        for (; i < count; ++i) take(i, std::true_type());  // the rest of the tile with it
         ptx::cp_async_wait_all();
         // The sums go through shared memory (the stages are free: every product is
         // complete) so that lanes write neighbouring words of the output.
@@ -507,6 +611,7 @@ k_matmul_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__
     __shared__ uint64_t scales_full[2], scales_empty[2];
     __shared__ uint32_t tmem_base;
     __shared__ alignas(16) float scales_p[2 * kBatch][128], scales_q[2 * kBatch][QROW ? 256 : 4];
+    __shared__ ScaleRange ranges[2][2];  // of a batch's scales of P and of Q
     uint8_t *stages = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint4 *staging = reinterpret_cast<uint4 *>(stages + kPairStages * kPairStageBytes);
@@ -622,6 +727,7 @@ k_matmul_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__
             // Scales, a batch of blocks ahead: warp 2 those of P, warp 3 those of Q.
             const bool of_p = warp == 2;
             const float *base = of_p ? g.scale_p : g.scale_q;
+            const float floor = of_p ? g.floor_p : g.floor_q;
             const int64_t ld = of_p ? g.ld_p : g.ld_q, rows = of_p ? g.p : g.q;
             const int shift = (of_p ? g.p_block : g.q_block) == 1 ? 0 : 7;  // 2^shift rows to a scale
             // Scales to take, and the tile's rows from one to the next (block scales of P
@@ -632,22 +738,30 @@ k_matmul_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__
             const int pitch = of_p ? 128 : QROW ? 256 : 4;
             // Blocks are counted through all tiles of this pair and copied by batches, one
             // batch ahead of the one in use.
-            const int64_t mine = pair < tiles ? (tiles - 1 - pair) / pairs + 1 : 0, blocks = mine * g.blocks;
-            int64_t tile = pair, r0 = 0;
-            int at = 0;  // the next block's place in its tile
+            const uint32_t mine = pair < tiles ? uint32_t(tiles - 1 - pair) / uint32_t(pairs) + 1 : 0;
+            const int64_t blocks = int64_t(mine) * g.blocks;
+            int64_t tile = pair;
+            int at = 0;         // the next block's place in its tile
+            const float *row;   // the scale of its first row, and how many of `count` there are
+            int have = 0;
+            const int step = of_p && shift ? 0 : 1;  // from one scale to the next
             auto copy_batch = [&](int64_t first) {
-                for (int64_t n = first; n < first + kBatch && n < blocks; ++n) {
+                const int held = blocks - first < kBatch ? int(blocks - first) : kBatch;
+                float *dst = ring + int(first % (2 * kBatch)) * pitch;
+                for (int n = 0; n < held; ++n, dst += pitch) {
                     if (at == 0) {
                         int64_t p0, q0;
                         tile_at(g, tile, kPairTile, kPairTile, 8, &p0, &q0);
-                        r0 = of_p ? p0 + rank * 128 : q0;
+                        const int64_t r0 = of_p ? p0 + rank * 128 : q0, left = apart == 1 ? rows - r0 : (rows - r0 + 127) >> 7;
+                        row = base + (r0 >> shift);
+                        have = left < count ? int(left) : count;
                     }
                     for (int k = lane; k < count; k += 32) {
-                        const int64_t r = r0 + k * apart;
-                        const float *p = base + at * ld + (r >> shift);
-                        ptx::cp_async_4_or_zero(ring + n % (2 * kBatch) * pitch + k, r < rows ? p : base,
-                                                r < rows && TR_LOAD_OK(side, p, 4));
+                        const float *p = row + k * step;
+                        const bool in = k < have && TR_LOAD_OK(side, p, 4);
+                        ptx::cp_async_4_or_zero(dst + k, in ? p : base, in);
                     }
+                    row += ld;
                     if (++at == g.blocks) {
                         at = 0;
                         tile += pairs;
@@ -659,6 +773,40 @@ k_matmul_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__
             uint32_t phase = 1;  // of the other buffer's release, which the first batch finds free
             for (int64_t n = 0; n < blocks; n += kBatch) {
                 ptx::cp_async_wait_all();
+                __syncwarp();
+                const int held = blocks - n < kBatch ? int(blocks - n) : kBatch;
+                const float *batch = ring + b * kBatch * pitch;
+                ScaleRange range{kNoneYet, 0};
+                if (count == 2) {
+                    if (lane < held) {
+                        range.add(batch[lane * pitch]);
+                        range.add(batch[lane * pitch + 1]);
+                    }
+                } else {
+#pragma unroll 2
+                    for (int k = lane * 4; k < held * count; k += 128) {  // count is the pitch
+                        const float4 four = *reinterpret_cast<const float4 *>(batch + k);
+                        range.add(four.x);
+                        range.add(four.y);
+                        range.add(four.z);
+                        range.add(four.w);
+                    }
+                }
+                range.join_warp();
+                if (range.least() < 0x1p-90f) {  // blocks of zeros, most likely: again without them
+                    range.below_least = kNoneYet;
+#pragma unroll 1
+                    for (int k = lane * 4; k < held * pitch; k += 128) {
+                        const float4 four = *reinterpret_cast<const float4 *>(batch + k);
+                        range.add_but(floor, four.x);
+                        range.add_but(floor, four.y);
+                        if (count == 2) continue;  // the other two words of that pitch hold nothing
+                        range.add_but(floor, four.z);
+                        range.add_but(floor, four.w);
+                    }
+                    range.join_warp();
+                }
+                if (lane == 0) ranges[b][of_p ? 0 : 1] = range;
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(scales_full + b);
                 b ^= 1;
@@ -677,6 +825,7 @@ k_matmul_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__
         [[maybe_unused]] const dbg::Side so = dbg::side(g.out, 1, g.p, g.q, g.ld_out, 0, g.out_bf16 ? 2 : 4);
         int b = 0, slot = 0;  // slot: of the block's scales
         uint32_t phase = 0, slot_phase = 0;
+        bool apart = false;  // the batch has factors out of range
         for (int64_t tile = pair; tile < tiles; tile += pairs) {
             int64_t p0, q0;
             tile_at(g, tile, kPairTile, kPairTile, 8, &p0, &q0);
@@ -686,10 +835,24 @@ k_matmul_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__
 #pragma unroll
             for (int c = 0; c < 64; ++c) acc[c] = make_float2(0.0f, 0.0f);
             float v[2][32];
-            for (int i = 0; i < g.blocks; ++i) {
-                // A wait that ran out is not repeated, but the arrivals go on.
-                if (slot % kBatch == 0 && ok) ok = ptx::mbar_wait_bounded(scales_full + slot / kBatch, slot_phase);
-                const float f = QROW ? scales_p[slot][r] : scales_p[slot][r] * scales_q[slot][group];
+            // Adds a block's sums; `first`: with factors that may leave the range of 32 bits.
+            auto take = [&](auto first) {
+                const float own_p = scales_p[slot][r], all_q = QROW ? 1.0f : scales_q[slot][group];
+                float f = own_p * all_q;
+                [[maybe_unused]] float pre = 1.0f;
+                if constexpr (decltype(first)::value) {
+                    ScaleRange cols{kNoneYet, 0};
+                    if constexpr (QROW) {
+#pragma unroll
+                        for (int c = lane; c < 128; c += 32) cols.add(scales_q[slot][group * 128 + c]);
+                        cols.join_warp();
+                    } else {
+                        cols.add(all_q);
+                    }
+                    const RowScale own = row_scale(own_p, 0.0f, cols);
+                    f = own.f * all_q;
+                    pre = own.pre;
+                }
                 const float2 f2 = make_float2(f, f);
                 // Scales of the next 8 columns, read in this order: left to itself the
                 // compiler reads each where it is used (8192^3: 640 us against 620; 16
@@ -713,6 +876,14 @@ k_matmul_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__
                         __syncwarp();
                         if (lane == 0) ptx::mbar_arrive_at(release[b]);
                     }
+                    if constexpr (decltype(first)::value) {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2) {
+                            const float2 two = __fmul2_rn(make_float2(v[c & 1][k], v[c & 1][k + 1]), make_float2(pre, pre));
+                            v[c & 1][k] = two.x;
+                            v[c & 1][k + 1] = two.y;
+                        }
+                    }
 #pragma unroll
                     for (int k = 0; k < 32; k += 4) {
                         float2 f01 = f2, f23 = f2;
@@ -728,7 +899,24 @@ k_matmul_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__
                         a1 = __ffma2_rn(make_float2(v[c & 1][k + 2], v[c & 1][k + 3]), f23, a1);
                     }
                 }
-                if (++slot % kBatch == 0) {
+                ++slot;
+                b ^= 1;
+                if (b == 0) phase ^= 1;
+            };
+            for (int i = 0; i < g.blocks;) {
+                // The blocks of this tile that the batch in hand still holds.
+                const int left = kBatch - slot % kBatch, end = i + left < g.blocks ? i + left : g.blocks;
+                if (left == kBatch) {
+                    // A wait that ran out is not repeated, but the arrivals go on.
+                    if (ok) ok = ptx::mbar_wait_bounded(scales_full + slot / kBatch, slot_phase);
+                    apart = out_of_range(ranges[slot / kBatch][0], ranges[slot / kBatch][1]);
+                }
+                if (apart) {
+                    for (; i < end; ++i) take(std::true_type());
+                } else {
+                    for (; i < end; ++i) take(std::false_type());
+                }
+                if (slot % kBatch == 0) {
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(scales_empty + slot / kBatch - 1);  // its reads are done
                     if (slot == 2 * kBatch) {
@@ -736,8 +924,6 @@ k_matmul_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__
                         slot_phase ^= 1;
                     }
                 }
-                b ^= 1;
-                if (b == 0) phase ^= 1;
             }
             store_rows(g, p0 + w * 32, q0, staging + (warp - 4) * 256,
                        [&](int j) { return j & 1 ? acc[j >> 1].y : acc[j >> 1].x; }, so);
@@ -881,6 +1067,8 @@ cudaError_t launch_matmul_fp8(const tr_matmul_fp8_args &a, const char **why) {
     g.q_block = turn ? a.a_block_rows : a.b_block_rows;
     g.p_e5m2 = (turn ? a.b_dtype : a.a_dtype) == TR_DTYPE_E5M2;
     g.q_e5m2 = (turn ? a.a_dtype : a.b_dtype) == TR_DTYPE_E5M2;
+    g.floor_p = g.p_e5m2 ? 0x1p-100f / 57344.0f : 0x1p-100f / 448.0f;
+    g.floor_q = g.q_e5m2 ? 0x1p-100f / 57344.0f : 0x1p-100f / 448.0f;
     g.out_bf16 = out_bf16;
     g.accumulate = a.accumulate;
     // Split the contraction until the tiles fill what is resident at one time, each

@@ -226,6 +226,19 @@ __device__ __forceinline__ float4 load_cluster4(uint32_t addr) {
 __device__ __forceinline__ void named_sync(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
+// The same; whether `value` holds in any of them.
+__device__ __forceinline__ bool named_any(int id, int threads, bool value) {
+    uint32_t any;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %3, 0;\n\t"
+        "bar.red.or.pred q, %1, %2, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(any)
+        : "r"(id), "r"(threads), "r"(uint32_t(value))
+        : "memory");
+    return any != 0;
+}
 
 }  // namespace ptx
 }  // namespace tr
