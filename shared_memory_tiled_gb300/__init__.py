@@ -1,5 +1,7 @@
 """libtranspose for GB300 (sm_103a): out-of-place matrix transpose staged
-through bank-conflict-free shared-memory tiles.
+through bank-conflict-free shared-memory tiles, and the operators of a linear
+layer in 8-bit floating point (``binding.quantize_fp8``, ``matmul_fp8``,
+``layernorm``, ``layernorm_backward``; ``train_linear`` runs them together).
 
 The compute path is the C-ABI shared library ``libtranspose.so`` built from
 ``csrc/``; ``binding`` marshals arguments into it with ctypes.  Importing this

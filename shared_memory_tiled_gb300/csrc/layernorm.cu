@@ -10,8 +10,11 @@
 //   16384 x 8192 bf16, fp32 weights   88 us, 6.1 TB/s (91%)
 //   16384 x 8192 fp32                181 us, 5.9 TB/s (88%)
 //   65536 x 1024 bf16                 45 us, 5.9 TB/s (88%)
-//   12289 x 7919 fp32 (rows off 16-byte boundaries)  156 us, 5.0 TB/s (74%)
-//   1 x 8192 bf16                    4.2 us: a launch and three trips to memory
+//   12289 x 7919 fp32 (rows off 16-byte boundaries)  155 us, 5.0 TB/s (74%)
+//   1 x 8192 bf16                    4.1 us: a launch and three trips to memory
+//   1024, 2048, 4096 x 8192 bf16     11.6, 17.7, 32.0 us: 2.9, 3.8, 4.2 TB/s (weights from L1)
+//   4096 x 32768 bf16 / fp32         168 / 278 us, 3.2 / 3.9 TB/s (the row is walked three times)
+//   8192 x 5003 bf16, x padded and y not  192 us, 0.9 TB/s (one value to an access)
 #include "launch.cuh"
 #include "row_chunk.cuh"
 #include "tr_internal.h"
@@ -315,7 +318,9 @@ cudaError_t launch_typed(const tr_layernorm_args &p) {
     };
     if (!alike) return run(k_layernorm_long<T, 1>, 1024, 1);
     const int64_t chunks = (a.cols + (shifted ? V - 1 : 0) + V - 1) / V;
-    // Rows for every group of every resident block: the weights' copy pays.
+    // Rows for every group of every resident block, counted in the shape with most groups:
+    // the weights' copy pays (8192 bf16: 4864 rows 32.1 us with it, 4863 rows 38.2 without;
+    // where it begins to pay for the other shapes was not measured).
     if (a.rows >= int64_t(sm_count()) * 32 && chunks < kMostRowChunks) {
 #define TR_ROWS(G, NCH, BLOCK)                                                            \
     if (chunks <= G * NCH)                                                                \

@@ -6,13 +6,18 @@
 // Bound by memory: one read of x and dy, one write of dx.  The column sums come from
 // the same read (k_ln_backward); two kernels, one along the rows and one down the
 // columns, take five passes over the matrices instead of three and serve the rows
-// that the ring below does not hold (over 16384 columns, fp32 over about 14400).
+// that the ring below does not hold: over 16384 columns, and fp32 over 11568, where two
+// rows of x and dy (16 bytes to a column) beside the weights (4) pass its 231424 bytes.
 //
 // Measured on one GB300 (share of the measured copy rate, 6771 GB/s), both kernels:
 //   16384 x 8192 bf16   139 us, 5.8 TB/s (86%); row sums and column sums apart: 574 us
 //   12289 x 7919 fp32   178 us, 6.6 TB/s (97%)  (rows off 16-byte boundaries)
 //   32768 x 4096 bf16   136 us, 5.9 TB/s (87%)
 //   16384 x 8192 fp32   266 us, 6.0 TB/s (89%): three rows in flight fill the ring
+//   8192 x 9000, 12288, 16384 bf16   257, 283, 338 us: 1.7, 2.1, 2.4 TB/s (values read twice
+//                                    from the ring, weights from shared memory)
+//   8192 x 11568 / 11572 fp32        274 / 481 us, 4.2 / 2.4 TB/s: the last that the ring holds, and past it
+//   8192 x 20480 bf16                713 us, 1.4 TB/s
 //   256 x 1024 bf16       9 us: two launches
 // The bf16 rows are bound by what a row costs beside its bytes: 0.48 instructions
 // a cycle and scheduler, and a meeting of the block per row.

@@ -17,13 +17,16 @@
 // their sums joined through distributed shared memory, in rank order.
 //
 // Measured on one GB300 (a bf16 library product reaches 1920 TFLOP/s there; 8-bit
-// instructions run at twice its rate):
-//   8192^3, 1x128 by 128x128 scales, bf16 out        435 us, 2.53 PFLOP/s
-//   8192^3, 1x128 by 1x128                           620 us, 1.77 PFLOP/s
-//   4096 x 2048 x 16384, 1x128 by 1x128, fp32 out    180 us, 1.53 PFLOP/s
-//   2048^3                                            14 us, 1.25 PFLOP/s
-//   777 x 2049 x 1111                               12.6 us
-//   1 x 8192 x 8192                                 14.3 us, 4.7 TB/s of weights (69% of the copy rate)
+// instructions run at twice its rate), ten calls in a row at 2070 MHz:
+//   8192^3, 1x128 by 128x128 scales, bf16 out        427 us, 2.57 PFLOP/s
+//     the same for a second on end (1930 MHz under the power cap)  458 us, 2.40 PFLOP/s
+//   8192^3, 1x128 by 1x128                           600 us, 1.83 PFLOP/s
+//   4096 x 2048 x 16384, 1x128 by 1x128, fp32 out    174 us, 1.58 PFLOP/s
+//   2048^3                                          13.5 us, 1.27 PFLOP/s
+//   777 x 2049 x 1111                               13.2 us
+//   1, 16 and 64 x 8192 x 8192                14.1, 14.9, 19.0 us: 4.8, 4.5, 3.6 TB/s
+//   with `accumulate`, 1x128 by 1x128, fp32: 8192^3 1471 us (618 without), 4096 x 2048 x
+//     16384 293 us (174): the large tiles then read, add and write value by value
 //
 // What bounds the large ones is the exchange between the tensor cores and the warps
 // that take the sums out, once for each block of 128: the instructions alone run at
@@ -32,7 +35,7 @@
 // four reads of 32 columns with the additions between them, the rest for the scales,
 // the hand back and the loop) and a buffer of sums, of which tensor memory holds
 // two, goes through instructions and warps in turn.  With a scale to each column it is the
-// multiplications and the reads of those scales: 1400 cycles.
+// multiplications and the reads of those scales as well: 0.67 us a block, 0.48 without.
 #include <atomic>
 #include <type_traits>
 
@@ -520,6 +523,7 @@ k_matmul_fp8(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ 
 //
 //   warp 0     TMA of its 128 rows of P and of its half of Q
 //   warp 1     (rank 0) matrix instructions of both CTAs, 4 per stage
+//   warps 2, 3 scales of P and of Q, a batch of blocks ahead, and the batch's range
 //   warps 4-11 two groups of 128 threads, 128 columns each: a thread takes its row's
 //              block sums out of tensor memory, 32 columns at a time with the next
 //              32 on the way, and adds them, scaled, to 128 sums in registers

@@ -13,8 +13,11 @@
 // Measured on one GB300 (share of the measured copy rate, 6771 GB/s):
 //   16384 x 8192 bf16, 1 x 128 blocks, both ways   95 us, 5.7 TB/s (85%); rows alone 64 us (92%)
 //   16384 x 8192 bf16, 128 x 128, both ways        87 us, 6.2 TB/s (91%)
-//   12289 x 7919 fp32, 128 x 128, both ways       123 us, 4.7 TB/s (70%)  (rows off 16-byte boundaries)
-//   12288 x 7920 fp32, 128 x 128, both ways       100 us, 5.8 TB/s (86%)
+//   12289 x 7919 fp32, 128 x 128, both ways       124 us, 4.7 TB/s (70%)  (rows off 16-byte boundaries)
+//   12288 x 7920 fp32, 128 x 128, both ways       101 us, 5.8 TB/s (85%)
+//   12289 x 7919 bf16, 1 x 128, both ways          87 us, 4.5 TB/s (66%)  (rows off 16-byte boundaries)
+// Rows off boundaries go through shared memory, and a block waits for all of a tile's
+// copies before it works on any: nothing of the next tile is in flight meanwhile.
 //   1 x 8192 bf16                                 2.6 us: a launch
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
