@@ -63,3 +63,45 @@ def test_one_block_out_of_range_leaves_the_others_as_they_are():
             same = torch.ones(m, dtype=torch.bool)
             same[7::9] = same[3::9] = False
             assert torch.equal(got[same.cuda()], first[same.cuda()])
+
+
+@pytest.mark.parametrize("m,n", [(3, 200), (40, 129), (150, 333), (2304, 2304)])
+@pytest.mark.parametrize("bb", [1, 128])
+def test_masked_rows_are_zero_and_the_others_right(m, n, bb):
+    """Rows and blocks of zeros as the quantizer leaves them, in e5m2: their scale times a
+    weight's is below the normal numbers."""
+    import torch
+    k = 1000
+    rng = np.random.default_rng(m)
+    x = rng.standard_normal((m, k)).astype(np.float32)
+    x[rng.random(m) < 0.3] = 0
+    x[1, 128:256] = 0
+    w = (0.01 * rng.standard_normal((n, k))).astype(np.float32)
+    w[:, 256:384] = 0
+    a, sa = B.quantize_fp8(torch.from_numpy(x).cuda(), dtype=torch.float8_e5m2)
+    b, sb = B.quantize_fp8(torch.from_numpy(w).cuda(), block_rows=bb)
+    qa, ha = R.quantize(x, "e5m2", 1)
+    qb, hb = R.quantize(w, "e4m3", bb)
+    want, bound = R.matmul(qa, ha, "e5m2", 1, qb, hb, "e4m3", bb)
+    got = host(B.matmul_fp8(a, sa, b, sb, out_dtype=torch.float32))
+    close(got, want, bound)
+    assert not got[(x == 0).all(1)].any()
+
+
+@pytest.mark.parametrize("m,n", [(40, 129), (150, 333), (2304, 2304)])
+def test_scales_of_every_size_in_one_tile(m, n):
+    """Each row and column with an exponent of its own, so that products of scales run from
+    2^-170 to 2^171 in one block: whatever is finite is right, down to the spacing of the
+    subnormal numbers."""
+    import torch
+    for codes in (SMALL, WIDE):
+        a, sa, qa, ha = operand(m, 128, 1, codes, 0, m)
+        b, sb, qb, hb = operand(n, 128, 1, codes, 0, n + 1)
+        rng = np.random.default_rng(5)
+        ha = np.ldexp(ha, rng.integers(-85, 86, ha.shape)).astype(np.float32)
+        hb = np.ldexp(hb, rng.integers(-85, 86, hb.shape)).astype(np.float32)
+        want, bound = R.matmul(qa, ha, "e4m3", 1, qb, hb, "e4m3", 1)
+        got = host(B.matmul_fp8(a, torch.from_numpy(ha).cuda(), b, torch.from_numpy(hb).cuda(), out_dtype=torch.float32))
+        finite = np.abs(want) + bound < 2.0 ** 127
+        close(got[finite], want[finite], bound[finite] + 2.0 ** -148)
+        assert not np.isnan(got).any()
