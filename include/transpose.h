@@ -1,7 +1,8 @@
 /*
  * libtranspose -- out-of-place matrix transpose for GB300 (sm_103a), and the
  * operators of a linear layer in 8-bit floating point that needs its operands
- * both as they are and transposed (second half of this header).
+ * both as they are and transposed, with the norms before it and the low-rank
+ * adapters beside it (second half of this header).
  *
  * What it computes.  For every batch plane b < batch, input row i < rows and
  * input column j < cols (all sizes and pitches in ELEMENTS):
@@ -402,6 +403,133 @@ tr_status tr_layernorm_backward(const tr_layernorm_backward_args *args);
 /* Bytes of workspace that tr_layernorm_backward needs for these sizes on any
  * device (0 for empty sizes, -1 for negative ones).  Host only. */
 int64_t tr_layernorm_backward_workspace(int64_t rows, int64_t cols);
+
+/* Arguments of tr_rmsnorm.  Zero-initialise. */
+typedef struct tr_rmsnorm_args {
+    const void *x;          /* rows x cols, row pitch ld_x >= cols                               */
+    const void *residual;   /* rows x cols of x's type, row pitch ld_residual >= cols; NULL: none */
+    const void *gamma;      /* cols weights                                                      */
+    void *h;                /* rows x cols of x's type, row pitch ld_h >= cols: x + residual.
+                               Wanted with a residual (it may be the residual itself, with the
+                               same pitch), NULL without                                         */
+    void *y;                /* rows x cols of x's type, row pitch ld_y >= cols; NULL: not wanted */
+    float *rstd;            /* rows values, for the backward pass; NULL: not wanted              */
+    void *q;                /* rows x cols bytes, row pitch ld_q >= cols; NULL: not wanted       */
+    float *scale;           /* with q: ceil(cols/128) x rows, row pitch ld_scale >= rows         */
+    void *qt;               /* cols x rows bytes, row pitch ld_qt >= rows; NULL: not wanted, else
+                               q and rstd are wanted too                                         */
+    float *scale_t;         /* with qt: ceil(rows/128) x cols, row pitch ld_scale_t >= cols      */
+    int32_t x_dtype;        /* TR_DTYPE_F32 or TR_DTYPE_BF16, of x, residual, h and y            */
+    int32_t w_dtype;        /* the same choice, of gamma                                         */
+    int32_t q_dtype;        /* TR_DTYPE_E4M3 or TR_DTYPE_E5M2, of q and qt                       */
+    int32_t reserved;       /* must be zero                                                      */
+    int64_t rows, cols;
+    int64_t ld_x, ld_residual, ld_h, ld_y, ld_q, ld_scale, ld_qt, ld_scale_t;
+    float eps;              /* >= 0                                                              */
+    int32_t reserved2;      /* must be zero                                                      */
+    tr_stream_t stream;
+} tr_rmsnorm_args;
+
+/* Root-mean-square norm over the rows of a matrix with a residual added first,
+ * and its rows in 8-bit floating point: with
+ *
+ *     h = x + residual, rounded to x's type (without a residual h = x)
+ *     rstd = 1 / sqrt(sum(h^2) / cols + eps)               along each row
+ *     y[i][j] = h[i][j] * rstd[i] * gamma[j]
+ *
+ * y is the output `y`, rounded once, and in 32 bits what q, scale, qt and scale_t
+ * quantize, as tr_quantize_fp8 does with block_rows = 1: q by rows in blocks of 1 x 128,
+ * qt the transpose in blocks of 128 rows (alignment and pitches as there).  Squares are
+ * summed in 32 bits.  A negative, infinite or NaN eps returns TR_ERR_BAD_DIM.  Empty
+ * matrices write nothing, rstd included. */
+tr_status tr_rmsnorm(const tr_rmsnorm_args *args);
+
+/* Arguments of tr_rmsnorm_backward.  Zero-initialise. */
+typedef struct tr_rmsnorm_backward_args {
+    const void *dy;         /* rows x cols of h's type, row pitch ld_dy >= cols                  */
+    const void *h;          /* rows x cols, row pitch ld_h >= cols: what was normed              */
+    const void *gamma;      /* cols weights                                                      */
+    const float *rstd;      /* rows values, from tr_rmsnorm                                      */
+    const void *dresidual;  /* rows x cols of h's type, row pitch ld_dresidual >= cols: the
+                               gradient that reaches h past the norm; NULL: none                 */
+    void *dx;               /* rows x cols of h's type, row pitch ld_dx >= cols; it may be
+                               dresidual itself, with the same pitch                             */
+    float *dgamma;          /* cols values                                                       */
+    void *workspace;        /* tr_rmsnorm_backward_workspace bytes, 16-byte aligned              */
+    int64_t workspace_bytes;
+    int32_t x_dtype;        /* TR_DTYPE_F32 or TR_DTYPE_BF16, of dy, h, dresidual and dx         */
+    int32_t w_dtype;        /* the same choice, of gamma                                         */
+    int64_t rows, cols;
+    int64_t ld_dy, ld_h, ld_dresidual, ld_dx;
+    tr_stream_t stream;
+} tr_rmsnorm_backward_args;
+
+/* Gradients of tr_rmsnorm.  With u = h * rstd and g = dy * gamma,
+ *
+ *     dx = rstd * (g - u * sum(g u)/cols) + dresidual      along each row
+ *     dgamma[j] = sum over rows of dy u
+ *
+ * dx is the gradient of h, and so of x and of the residual alike.  The sums down the
+ * rows are held in 32 bits and joined in an order that is fixed for a call's arguments on a
+ * device (no atomics), so equal calls give equal bits; without rows they are zero.
+ * Nothing needs clearing before the call.  TR_ERR_UNSUPPORTED for a workspace that is
+ * too small or misaligned. */
+tr_status tr_rmsnorm_backward(const tr_rmsnorm_backward_args *args);
+
+/* Bytes of workspace that tr_rmsnorm_backward needs for these sizes on any
+ * device (0 for empty sizes, -1 for negative ones).  Host only. */
+int64_t tr_rmsnorm_backward_workspace(int64_t rows, int64_t cols);
+
+/* Arguments of tr_adapter_plan.  Zero-initialise. */
+typedef struct tr_adapter_plan_args {
+    const int32_t *index;   /* tokens values: the adapter of each token; one outside
+                               [0, adapters) has none                                            */
+    void *plan;             /* tr_adapter_plan_bytes bytes, 16-byte aligned                      */
+    int64_t plan_bytes;
+    int64_t tokens;         /* below 2^31                                                        */
+    int64_t adapters;       /* below 2^15                                                        */
+    tr_stream_t stream;
+} tr_adapter_plan_args;
+
+/* Groups the tokens of a batch by their adapter, in the tokens' order within an adapter:
+ * what tr_adapters walks.  A batch needs one plan, which serves all of its projections;
+ * plans of two batches in flight at once need memory of their own.  TR_ERR_UNSUPPORTED
+ * for a plan that is too small or misaligned. */
+tr_status tr_adapter_plan(const tr_adapter_plan_args *args);
+
+/* Bytes of a plan (-1 for sizes that tr_adapter_plan refuses).  Host only. */
+int64_t tr_adapter_plan_bytes(int64_t tokens, int64_t adapters);
+
+/* Arguments of tr_adapters.  Zero-initialise. */
+typedef struct tr_adapters_args {
+    const void *x;          /* tokens x k, bf16, row pitch ld_x >= k                             */
+    const void *a;          /* adapters planes of rank x k, bf16, row pitch ld_a >= k            */
+    const void *b;          /* adapters planes of n x rank, bf16, row pitch ld_b >= rank         */
+    const float *scale;     /* adapters values; NULL: all 1                                      */
+    const void *plan;       /* of these tokens and adapters, from tr_adapter_plan                */
+    const void *base;       /* tokens x n of out's type, row pitch ld_base >= n; NULL: zeros     */
+    void *out;              /* tokens x n, row pitch ld_out >= n; it may be base itself, with
+                               the same pitch                                                    */
+    int64_t plan_bytes;
+    int32_t out_dtype;      /* TR_DTYPE_F32 or TR_DTYPE_BF16, of out and base                    */
+    int32_t reserved;       /* must be zero                                                      */
+    int64_t tokens, adapters, k, n;
+    int64_t rank;           /* 1 .. 128; adapters of a lower rank are filled up with zeros       */
+    int64_t ld_x, ld_a, stride_a, ld_b, stride_b, ld_base, ld_out;
+    tr_stream_t stream;
+} tr_adapters_args;
+
+/* Low-rank adapters of many requests at once beside a projection that they share: for
+ * each token i with the adapter g of the plan
+ *
+ *     v[r] = scale[g] * sum over l of x[i][l] * a[g][r][l]
+ *     out[i][j] = base[i][j] + sum over r of v[r] * b[g][j][r]
+ *
+ * and out[i] = base[i] for a token without one.  Sums are held in 32 bits, v in
+ * 16 significant bits or more, out is rounded once.  Equal calls give equal bits.  x, a
+ * and b are 16-byte aligned, their row pitches and strides multiples of 8 values (else
+ * TR_ERR_UNSUPPORTED); tokens, k and n are below 2^31. */
+tr_status tr_adapters(const tr_adapters_args *args);
 
 /* Host-only planning: the variant tr_transpose_ex would run for these
  * arguments and options (a tr_variant value, never AUTO), or a negative

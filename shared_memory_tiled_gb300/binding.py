@@ -10,7 +10,8 @@ The library is opened on first use.  If it has not been built, or cannot be
 loaded, every call raises ``LibraryMissing``: there is no fallback path.
 
 ``transpose`` / ``copy`` and ``quantize_fp8`` / ``matmul_fp8`` / ``layernorm`` /
-``layernorm_backward`` are conveniences for torch tensors: they read sizes and
+``layernorm_backward`` / ``rmsnorm`` / ``rmsnorm_fp8`` / ``rmsnorm_backward`` /
+``adapter_plan`` / ``adapters`` are conveniences for torch tensors: they read sizes and
 pitches off the tensors' strides and call the same entry points.
 """
 from __future__ import annotations
@@ -115,6 +116,38 @@ class LayernormBackwardArgs(ctypes.Structure):
                 ("cols", I64), ("ld_dy", I64), ("ld_x", I64), ("ld_dx", I64), ("stream", VP)]
 
 
+class RmsnormArgs(ctypes.Structure):
+    _fields_ = [("x", VP), ("residual", VP), ("gamma", VP), ("h", VP), ("y", VP), ("rstd", VP),
+                ("q", VP), ("scale", VP), ("qt", VP), ("scale_t", VP),
+                ("x_dtype", ctypes.c_int32), ("w_dtype", ctypes.c_int32),
+                ("q_dtype", ctypes.c_int32), ("reserved", ctypes.c_int32), ("rows", I64),
+                ("cols", I64), ("ld_x", I64), ("ld_residual", I64), ("ld_h", I64), ("ld_y", I64),
+                ("ld_q", I64), ("ld_scale", I64), ("ld_qt", I64), ("ld_scale_t", I64),
+                ("eps", ctypes.c_float), ("reserved2", ctypes.c_int32), ("stream", VP)]
+
+
+class RmsnormBackwardArgs(ctypes.Structure):
+    _fields_ = [("dy", VP), ("h", VP), ("gamma", VP), ("rstd", VP), ("dresidual", VP), ("dx", VP),
+                ("dgamma", VP), ("workspace", VP), ("workspace_bytes", I64),
+                ("x_dtype", ctypes.c_int32), ("w_dtype", ctypes.c_int32), ("rows", I64),
+                ("cols", I64), ("ld_dy", I64), ("ld_h", I64), ("ld_dresidual", I64),
+                ("ld_dx", I64), ("stream", VP)]
+
+
+class AdapterPlanArgs(ctypes.Structure):
+    _fields_ = [("index", VP), ("plan", VP), ("plan_bytes", I64), ("tokens", I64),
+                ("adapters", I64), ("stream", VP)]
+
+
+class AdaptersArgs(ctypes.Structure):
+    _fields_ = [("x", VP), ("a", VP), ("b", VP), ("scale", VP), ("plan", VP), ("base", VP),
+                ("out", VP), ("plan_bytes", I64), ("out_dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("tokens", I64), ("adapters", I64), ("k", I64),
+                ("n", I64), ("rank", I64), ("ld_x", I64), ("ld_a", I64), ("stride_a", I64),
+                ("ld_b", I64), ("stride_b", I64), ("ld_base", I64), ("ld_out", I64),
+                ("stream", VP)]
+
+
 class LibraryMissing(RuntimeError):
     pass
 
@@ -146,6 +179,12 @@ SIGNATURES = {
     "tr_layernorm": ([ctypes.POINTER(LayernormArgs)], ctypes.c_int),
     "tr_layernorm_backward": ([ctypes.POINTER(LayernormBackwardArgs)], ctypes.c_int),
     "tr_layernorm_backward_workspace": ([I64, I64], I64),
+    "tr_rmsnorm": ([ctypes.POINTER(RmsnormArgs)], ctypes.c_int),
+    "tr_rmsnorm_backward": ([ctypes.POINTER(RmsnormBackwardArgs)], ctypes.c_int),
+    "tr_rmsnorm_backward_workspace": ([I64, I64], I64),
+    "tr_adapter_plan": ([ctypes.POINTER(AdapterPlanArgs)], ctypes.c_int),
+    "tr_adapter_plan_bytes": ([I64, I64], I64),
+    "tr_adapters": ([ctypes.POINTER(AdaptersArgs)], ctypes.c_int),
     "tr_device_status": ([], ctypes.c_int),
     "tr_selftest_bounded_wait": ([ctypes.c_int32, I64, VP], ctypes.c_int),
     "tr_debug_bounds": ([ctypes.POINTER(BoundsReport)], ctypes.c_int),
@@ -272,6 +311,30 @@ def tr_layernorm_backward(args: LayernormBackwardArgs) -> int:
 
 def tr_layernorm_backward_workspace(rows, cols) -> int:
     return _call("tr_layernorm_backward_workspace", rows, cols)
+
+
+def tr_rmsnorm(args: RmsnormArgs) -> int:
+    return _call("tr_rmsnorm", ctypes.byref(args) if args is not None else None)
+
+
+def tr_rmsnorm_backward(args: RmsnormBackwardArgs) -> int:
+    return _call("tr_rmsnorm_backward", ctypes.byref(args) if args is not None else None)
+
+
+def tr_rmsnorm_backward_workspace(rows, cols) -> int:
+    return _call("tr_rmsnorm_backward_workspace", rows, cols)
+
+
+def tr_adapter_plan(args: AdapterPlanArgs) -> int:
+    return _call("tr_adapter_plan", ctypes.byref(args) if args is not None else None)
+
+
+def tr_adapter_plan_bytes(tokens, adapters) -> int:
+    return _call("tr_adapter_plan_bytes", tokens, adapters)
+
+
+def tr_adapters(args: AdaptersArgs) -> int:
+    return _call("tr_adapters", ctypes.byref(args) if args is not None else None)
 
 
 def tr_selftest_bounded_wait(arrive, limit_ns, stream=0) -> int:
@@ -646,3 +709,230 @@ def layernorm_backward(dy, x, gamma, mean, rstd, *, bias=True, out=None, stream=
         out.data_ptr(), dgamma.data_ptr(), dbeta.data_ptr() if bias else None,
         workspace.data_ptr(), size, xk, wk, rows, cols, ld_dy, ld, ld_dx), dev)
     return out, dgamma, dbeta
+
+
+def _stream_of(x, residual, residual_out, rows, cols, dev):
+    """(address and pitch of the residual, tensor, address and pitch of the new stream)"""
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out needs a residual: without one the stream is x")
+        return None, 0, x, None, 0
+    r, c, ld = _matrix(residual, "residual", dev)
+    if r != rows or c != cols or residual.dtype != x.dtype:
+        raise ValueError("residual must match x in shape and dtype")
+    h, ld_h = _like(residual_out, x, rows, cols, dev)
+    return residual.data_ptr(), ld, h, h.data_ptr(), ld_h
+
+
+def rmsnorm(x, gamma, residual=None, *, eps=1e-6, out=None, residual_out=None, stream=None):
+    """Root-mean-square norm over the rows of a CUDA matrix (fp32 or bf16), with
+    ``residual`` added to it first.
+
+    Returns ``(y, h, rstd)``: y of x's type (``out`` if given), the stream ``h = x +
+    residual`` (``residual_out`` if given, which may be ``residual`` itself; without
+    a residual x) and the rows' reciprocal root mean squares in fp32 for
+    ``rmsnorm_backward`` (NaN for a matrix of no columns).  ``gamma`` is fp32 or bf16.
+    ``stream`` (a cudaStream_t): default torch's current stream.
+    """
+    if stream is not None:
+        return _on(stream, x, lambda: rmsnorm(x, gamma, residual, eps=eps, out=out, residual_out=residual_out))
+    torch = _torch or _need_torch()
+    dev = _cuda(x)
+    rows, cols, ld = _matrix(x, "x", dev)
+    _vector(gamma, "gamma", cols, dev)
+    xk, wk = _kind(x.dtype, _WIDE, "x"), _kind(gamma.dtype, _WIDE, "gamma")
+    res, ld_r, h, at_h, ld_h = _stream_of(x, residual, residual_out, rows, cols, dev)
+    out, ld_y = _like(out, x, rows, cols, dev)
+    rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+    if not cols:  # the library launches nothing; the mean of no squares is 0 / 0
+        rstd.fill_(float("nan"))
+    _run("tr_rmsnorm", RmsnormArgs(
+        x.data_ptr(), res, gamma.data_ptr(), at_h, out.data_ptr(), rstd.data_ptr(), None, None, None, None,
+        xk, wk, 0, 0, rows, cols, ld, ld_r, ld_h, ld_y, 0, 0, 0, 0, eps, 0), dev)
+    return out, h, rstd
+
+
+def rmsnorm_fp8(x, gamma, residual=None, *, eps=1e-6, dtype=None, transposed=False, out=None, residual_out=None,
+                stream=None):
+    """``rmsnorm`` with its rows in 8-bit floating point, as ``quantize_fp8`` leaves them with
+    ``block_rows=1``, from the same read of x.
+
+    Returns ``(q, scale, h, rstd)``, and with ``transposed`` ``(q, scale, qt, scale_t, h,
+    rstd)``.  ``out``, a matrix of x's shape and type, receives the rows that are
+    not quantized as well.  The rest is as for ``rmsnorm``.
+    """
+    if stream is not None:
+        return _on(stream, x, lambda: rmsnorm_fp8(x, gamma, residual, eps=eps, dtype=dtype, transposed=transposed,
+                                                  out=out, residual_out=residual_out))
+    torch = _torch or _need_torch()
+    dev = _cuda(x)
+    rows, cols, ld = _matrix(x, "x", dev)
+    _vector(gamma, "gamma", cols, dev)
+    if dtype is None:
+        dtype = torch.float8_e4m3fn
+    xk, wk, qk = _kind(x.dtype, _WIDE, "x"), _kind(gamma.dtype, _WIDE, "gamma"), _kind(dtype, _NARROW, "dtype")
+    res, ld_r, h, at_h, ld_h = _stream_of(x, residual, residual_out, rows, cols, dev)
+    y, ld_y = None, 0
+    if out is not None:
+        out, ld_y = _like(out, x, rows, cols, dev)
+        y = out.data_ptr()
+    empty, strided, f32 = torch.empty, torch.empty_strided, torch.float32
+    ld_q, cb = (cols + 15) // 16 * 16, (cols + 127) // 128
+    q = strided((rows, cols), (ld_q, 1), dtype=dtype, device=dev)
+    scale, rstd = empty((cb, rows), dtype=f32, device=dev), empty(rows, dtype=f32, device=dev)
+    if not cols:
+        rstd.fill_(float("nan"))
+    if not transposed:
+        _run("tr_rmsnorm", RmsnormArgs(
+            x.data_ptr(), res, gamma.data_ptr(), at_h, y, rstd.data_ptr(), q.data_ptr(), scale.data_ptr(), None, None,
+            xk, wk, qk, 0, rows, cols, ld, ld_r, ld_h, ld_y, ld_q, rows, 0, 0, eps, 0), dev)
+        return q, scale, h, rstd
+    ld_t = (rows + 15) // 16 * 16
+    qt = strided((cols, rows), (ld_t, 1), dtype=dtype, device=dev)
+    scale_t = empty(((rows + 127) // 128, cols), dtype=f32, device=dev)
+    _run("tr_rmsnorm", RmsnormArgs(
+        x.data_ptr(), res, gamma.data_ptr(), at_h, y, rstd.data_ptr(), q.data_ptr(), scale.data_ptr(), qt.data_ptr(),
+        scale_t.data_ptr(), xk, wk, qk, 0, rows, cols, ld, ld_r, ld_h, ld_y, ld_q, rows, ld_t, cols, eps, 0), dev)
+    return q, scale, qt, scale_t, h, rstd
+
+
+def rmsnorm_backward(dy, h, gamma, rstd, *, dresidual=None, out=None, stream=None):
+    """Gradients of ``rmsnorm``: ``(dx, dgamma)``.
+
+    dx is the gradient of the stream ``h``, and so of x and of the residual alike, of h's
+    type (``out`` if given); ``dresidual``, the gradient that reaches h past the norm, is
+    added to it (``out`` may be ``dresidual`` itself).  dgamma is fp32.  ``stream`` (a
+    cudaStream_t): default torch's current stream.
+    """
+    if stream is not None:
+        return _on(stream, h, lambda: rmsnorm_backward(dy, h, gamma, rstd, dresidual=dresidual, out=out))
+    torch = _torch or _need_torch()
+    dev = _cuda(h)
+    rows, cols, ld = _matrix(h, "h", dev)
+    r, c, ld_dy = _matrix(dy, "dy", dev)
+    if r != rows or c != cols or dy.dtype != h.dtype:
+        raise ValueError("dy must match h in shape and dtype")
+    _vector(gamma, "gamma", cols, dev)
+    _vector(rstd, "rstd", rows, dev)
+    _kind(rstd.dtype, _F32, "rstd")
+    xk, wk = _kind(h.dtype, _WIDE, "h"), _kind(gamma.dtype, _WIDE, "gamma")
+    res, ld_r = None, 0
+    if dresidual is not None:
+        r, c, ld_r = _matrix(dresidual, "dresidual", dev)
+        if r != rows or c != cols or dresidual.dtype != h.dtype:
+            raise ValueError("dresidual must match h in shape and dtype")
+        res = dresidual.data_ptr()
+    out, ld_dx = _like(out, h, rows, cols, dev)
+    dgamma = torch.empty(cols, dtype=torch.float32, device=dev)
+    size = (_lib or load()).tr_rmsnorm_backward_workspace(rows, cols)
+    workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+    _run("tr_rmsnorm_backward", RmsnormBackwardArgs(
+        dy.data_ptr(), h.data_ptr(), gamma.data_ptr(), rstd.data_ptr(), res, out.data_ptr(), dgamma.data_ptr(),
+        workspace.data_ptr(), size, xk, wk, rows, cols, ld_dy, ld, ld_r, ld_dx), dev)
+    return out, dgamma
+
+
+class AdapterPlan:
+    """The tokens of a batch grouped by their adapter, on the GPU (``adapter_plan``)."""
+    __slots__ = ("words", "tokens", "adapters")
+
+    def __init__(self, words, tokens, adapters):
+        self.words, self.tokens, self.adapters = words, tokens, adapters
+
+
+def adapter_plan(index, adapters, *, stream=None):
+    """Group the tokens of a batch by their adapter.
+
+    ``index`` is a CUDA vector of int32, the adapter of each token; a token whose index is
+    outside [0, adapters) has none.  Returns the plan that ``adapters`` takes: a batch
+    needs one for all of its projections.  ``stream`` (a cudaStream_t): default torch's
+    current stream.
+    """
+    if stream is not None:
+        return _on(stream, index, lambda: adapter_plan(index, adapters))
+    torch = _torch or _need_torch()
+    dev = _cuda(index)
+    if index.dtype != torch.int32:
+        raise TypeError(f"index: unsupported dtype {index.dtype}")
+    tokens = index.numel()
+    _vector(index, "index", tokens, dev)
+    size = (_lib or load()).tr_adapter_plan_bytes(tokens, adapters)
+    if size < 0:
+        raise ValueError(f"{adapters} adapters: expected 0 to 32767")
+    words = torch.empty(size, dtype=torch.uint8, device=dev)
+    _run("tr_adapter_plan", AdapterPlanArgs(index.data_ptr(), words.data_ptr(), size, tokens, adapters), dev)
+    return AdapterPlan(words, tokens, adapters)
+
+
+def _planes(t, name, device):
+    """(planes, rows, cols, pitch, stride) of matrices with unit inner stride on a CUDA device."""
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    shape = t.shape
+    if len(shape) != 3:
+        raise ValueError(f"{name} must have three dimensions")
+    p, r, c = shape
+    sp, sr, sc = t.stride()
+    if sc != 1 and c > 1:
+        raise ValueError(f"the innermost dimension of {name} must be contiguous")
+    if r <= 1:
+        sr = (c + 7) // 8 * 8
+    return p, r, c, sr, sp if p > 1 else 0
+
+
+def adapters(x, a, b, plan, *, scale=None, base=None, out=None, out_dtype=None, stream=None):
+    """Low-rank adapters of many requests at once: ``base + scale_g * (x a_g^T) b_g^T`` for each
+    row of x with the adapter g of the plan, ``base`` for a row without one.
+
+    ``x`` [tokens, k], ``a`` [adapters, rank, k] and ``b`` [adapters, n, rank] are bf16 with rows
+    on 16-byte boundaries, ``scale`` (optional) one fp32 value for each adapter, ``base``
+    (optional: zeros) [tokens, n] what the projection that all share gave.  The output is
+    ``out`` (fp32 or bf16, may be a strided view, or ``base`` itself) or a new matrix of
+    base's type (of ``out_dtype``, bf16 by default, without one).  ``stream`` (a
+    cudaStream_t): default torch's current stream.
+    """
+    if stream is not None:
+        return _on(stream, x, lambda: adapters(x, a, b, plan, scale=scale, base=base, out=out, out_dtype=out_dtype))
+    torch = _torch or _need_torch()
+    dev = _cuda(x)
+    tokens, k, ld_x = _matrix(x, "x", dev)
+    count, rank, ka, ld_a, stride_a = _planes(a, "a", dev)
+    count_b, n, rank_b, ld_b, stride_b = _planes(b, "b", dev)
+    bf16 = torch.bfloat16
+    if x.dtype != bf16 or a.dtype != bf16 or b.dtype != bf16:
+        raise TypeError("x, a and b must be bf16")
+    if ka != k or rank_b != rank or count_b != count:
+        raise ValueError(f"a of shape {tuple(a.shape)} and b of shape {tuple(b.shape)} do not go with rows of {k}")
+    words = plan.words
+    if plan.tokens != tokens or plan.adapters != count or words.device != dev:
+        raise ValueError(f"a plan of {plan.tokens} tokens and {plan.adapters} adapters, expected {tokens} and {count}")
+    if tokens <= 1:
+        ld_x = (k + 7) // 8 * 8
+    at_scale = None
+    if scale is not None:
+        _vector(scale, "scale", count, dev)
+        _kind(scale.dtype, _F32, "scale")
+        at_scale = scale.data_ptr()
+    at_base, ld_base = None, 0
+    if base is not None:
+        bt, bn, ld_base = _matrix(base, "base", dev)
+        if bt != tokens or bn != n:
+            raise ValueError(f"base has shape {(bt, bn)}, expected {(tokens, n)}")
+        at_base = base.data_ptr()
+    if out is None:
+        kind = out_dtype or (bf16 if base is None else base.dtype)
+        out = torch.empty((tokens, n), dtype=kind, device=dev)
+        ld_out = n
+    else:
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError("out_dtype is not out's dtype")
+        ot, on, ld_out = _matrix(out, "out", dev)
+        if ot != tokens or on != n:
+            raise ValueError(f"out has shape {(ot, on)}, expected {(tokens, n)}")
+    if base is not None and base.dtype != out.dtype:
+        raise TypeError("base and out must have the same dtype")
+    _run("tr_adapters", AdaptersArgs(
+        x.data_ptr(), a.data_ptr(), b.data_ptr(), at_scale, words.data_ptr(), at_base, out.data_ptr(),
+        words.numel(), _kind(out.dtype, _WIDE, "out"), 0, tokens, count, k, n, rank, ld_x, ld_a, stride_a, ld_b,
+        stride_b, ld_base, ld_out), dev)
+    return out

@@ -37,7 +37,7 @@ SOURCES = ["api.cu", "copy.cu", "tile_lsu.cu", "tile_vec.cu", "tile_vec_u32.cu",
            "tile_vec_u32_prefetch.cu", "tile_vec_u16.cu", "tile_vec_u16_prefetch.cu",
            "tile_tma.cu", "inplace.cu", "bank_probe.cu", "operand_tiles.cu", "bounds.cu",
            "linear_api.cu", "quantize_fp8.cu", "matmul_fp8.cu", "layernorm.cu",
-           "layernorm_backward.cu"]
+           "layernorm_backward.cu", "rmsnorm.cu", "rmsnorm_backward.cu", "adapters.cu"]
 
 
 def nvcc() -> str:

@@ -22,6 +22,9 @@ cudaError_t read_bounds_quantize(dbg::Record *r);
 cudaError_t read_bounds_matmul_fp8(dbg::Record *r);
 cudaError_t read_bounds_layernorm(dbg::Record *r);
 cudaError_t read_bounds_layernorm_backward(dbg::Record *r);
+cudaError_t read_bounds_rmsnorm(dbg::Record *r);
+cudaError_t read_bounds_rmsnorm_backward(dbg::Record *r);
+cudaError_t read_bounds_adapters(dbg::Record *r);
 
 namespace {
 
@@ -80,7 +83,8 @@ cudaError_t read_and_clear_bounds(BoundsSummary *sum) {
         read_bounds_vec_u16_prefetch, read_bounds_lsu, read_bounds_tma, read_bounds_inplace,
         read_bounds_copy, read_bounds_operand_tiles, read_bounds_bank_probe,
         read_bounds_quantize, read_bounds_matmul_fp8, read_bounds_layernorm,
-        read_bounds_layernorm_backward,
+        read_bounds_layernorm_backward, read_bounds_rmsnorm, read_bounds_rmsnorm_backward,
+        read_bounds_adapters,
         read_bounds_selftest};
     for (auto read : readers) {
         dbg::Record r{};

@@ -20,11 +20,11 @@
 // copies before it works on any: nothing of the next tile is in flight meanwhile.
 //   1 x 8192 bf16                                 2.6 us: a launch
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
 
 #include <atomic>
 
 #include "bounds.cuh"
+#include "fp8.cuh"
 #include "granule.cuh"
 #include "launch.cuh"
 #include "ptx.cuh"
@@ -34,7 +34,6 @@ namespace tr {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr uint32_t kFloorBits = 0x0D800000u;  // 2^-100
 
 struct Quant {
     const void *x;
@@ -44,28 +43,6 @@ struct Quant {
     int64_t tiles_r, tiles_c;
     float top;  // the 8-bit type's largest finite value
 };
-
-// Eight values times r as eight bytes, the first lowest.
-template <bool E5M2>
-__device__ __forceinline__ uint2 to_bytes(const float (&v)[8], float r) {
-    constexpr __nv_fp8_interpretation_t K = E5M2 ? __NV_E5M2 : __NV_E4M3;
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        w[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i] * r, v[2 * i + 1] * r), __NV_SATFINITE, K);
-    return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
-}
-
-// Eight bytes of one row at column c (a multiple of 8), those below `cols` only.
-__device__ __forceinline__ void store8(uint8_t *row, int64_t c, int64_t cols, uint2 v,
-                                       const dbg::Side &s) {
-    if (c + 8 <= cols) {
-        if (TR_STORE_OK(s, row + c, 8)) *reinterpret_cast<uint2 *>(row + c) = v;
-        return;
-    }
-    for (int i = 0; i < 8 && c + i < cols; ++i)
-        if (TR_STORE_OK(s, row + c + i, 1)) row[c + i] = uint8_t((i < 4 ? v.x >> (8 * i) : v.y >> (8 * (i - 4))));
-}
 
 // How a tile's values reach the registers.  The two for rows off 16-byte boundaries go
 // through shared memory; each warp copies, and reads back, its own 16 rows.

@@ -19,6 +19,11 @@ namespace tr {
 
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+// The same, rounded to the type of the second argument; and a value stored in the type's way.
+__device__ __forceinline__ float round_to(float v, float) { return v; }
+__device__ __forceinline__ float round_to(float v, __nv_bfloat16) { return __bfloat162float(__float2bfloat16_rn(v)); }
+__device__ __forceinline__ void put_value(float *p, float v) { *p = v; }
+__device__ __forceinline__ void put_value(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 
 // V values of type T: 16 bytes, or one value.  bf16 stays packed in words.  A row in
 // registers is unpacked once in every walk over it: the compiler would rather

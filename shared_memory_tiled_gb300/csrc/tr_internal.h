@@ -82,6 +82,10 @@ cudaError_t launch_quantize(const tr_quantize_args &a);
 cudaError_t launch_matmul_fp8(const tr_matmul_fp8_args &a, const char **why);
 cudaError_t launch_layernorm(const tr_layernorm_args &a);
 cudaError_t launch_layernorm_backward(const tr_layernorm_backward_args &a);
+cudaError_t launch_rmsnorm(const tr_rmsnorm_args &a);
+cudaError_t launch_rmsnorm_backward(const tr_rmsnorm_backward_args &a);
+cudaError_t launch_adapter_plan(const tr_adapter_plan_args &a);
+cudaError_t launch_adapters(const tr_adapters_args &a);
 
 // Message behind tr_last_error() for this host thread (e: cudaSuccess = none).
 void set_error(const char *what, cudaError_t e);
