@@ -187,6 +187,7 @@ SIGNATURES = {
     "tr_adapters": ([ctypes.POINTER(AdaptersArgs)], ctypes.c_int),
     "tr_device_status": ([], ctypes.c_int),
     "tr_selftest_bounded_wait": ([ctypes.c_int32, I64, VP], ctypes.c_int),
+    "tr_selftest_bounded_wait_in": ([ctypes.c_char_p, ctypes.c_int32, I64, VP], ctypes.c_int),
     "tr_debug_bounds": ([ctypes.POINTER(BoundsReport)], ctypes.c_int),
     "tr_debug_bounds_selftest": ([ctypes.c_uint64, VP], ctypes.c_int),
     "tr_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -339,6 +340,10 @@ def tr_adapters(args: AdaptersArgs) -> int:
 
 def tr_selftest_bounded_wait(arrive, limit_ns, stream=0) -> int:
     return _call("tr_selftest_bounded_wait", arrive, limit_ns, stream)
+
+
+def tr_selftest_bounded_wait_in(unit, arrive, limit_ns, stream=0) -> int:
+    return _call("tr_selftest_bounded_wait_in", unit.encode() if unit is not None else None, arrive, limit_ns, stream)
 
 
 def tr_debug_bounds(report: BoundsReport) -> int:

@@ -281,6 +281,26 @@ int sm_count() {
 
 }  // namespace tr
 
+namespace tr {
+namespace {
+
+// The units whose kernels wait, by the names that tr_device_status gives them.
+struct WaitUnit {
+    const char *name;
+    cudaError_t (*selftest)(bool arrive, int64_t limit_ns, cudaStream_t stream);
+    cudaError_t (*read)(unsigned *value);
+};
+const WaitUnit kWaitUnits[] = {
+    {"transpose", launch_wait_selftest, read_and_clear_fault},
+    {"matmul_fp8", launch_wait_selftest_matmul, read_and_clear_fault_matmul},
+    {"layernorm_backward", launch_wait_selftest_layernorm, read_and_clear_fault_layernorm},
+    {"rmsnorm", launch_wait_selftest_rmsnorm, read_and_clear_fault_rmsnorm},
+    {"rmsnorm_backward", launch_wait_selftest_rmsnorm_backward, read_and_clear_fault_rmsnorm_backward},
+};
+
+}  // namespace
+}  // namespace tr
+
 extern "C" {
 
 tr_status tr_transpose_f32(const float *in, float *out, int64_t rows, int64_t cols, int64_t ld_in,
@@ -445,17 +465,32 @@ tr_status tr_selftest_bounded_wait(int32_t arrive, int64_t limit_ns, tr_stream_t
     return TR_OK;
 }
 
-tr_status tr_device_status(void) {
-    unsigned v = 0, w = 0, u = 0;
-    cudaError_t e = tr::read_and_clear_fault(&v);
-    if (e == cudaSuccess) e = tr::read_and_clear_fault_matmul(&w);
-    if (e == cudaSuccess) e = tr::read_and_clear_fault_layernorm(&u);
-    if (e != cudaSuccess) {
-        tr::set_error("reading the device fault flag failed", e);
+tr_status tr_selftest_bounded_wait_in(const char *unit, int32_t arrive, int64_t limit_ns, tr_stream_t stream) {
+    if (!unit) return TR_ERR_NULL;
+    if (limit_ns <= 0 || limit_ns > 2000000000LL) return TR_ERR_BAD_DIM;
+    for (const tr::WaitUnit &u : tr::kWaitUnits) {
+        if (std::strcmp(u.name, unit) != 0) continue;
+        const cudaError_t e = u.selftest(arrive != 0, limit_ns, reinterpret_cast<cudaStream_t>(stream));
+        if (e == cudaSuccess) return TR_OK;
+        tr::set_error("self-test launch failed", e);
         return TR_ERR_CUDA;
     }
-    if (!(v | w | u)) return TR_OK;
-    const std::string units = std::string(v ? " transpose" : "") + (w ? " matmul_fp8" : "") + (u ? " layernorm_backward" : "");
+    tr::set_error("no unit of that name has kernels that wait", cudaSuccess);
+    return TR_ERR_UNSUPPORTED;
+}
+
+tr_status tr_device_status(void) {
+    std::string units;
+    for (const tr::WaitUnit &u : tr::kWaitUnits) {
+        unsigned v = 0;
+        const cudaError_t e = u.read(&v);
+        if (e != cudaSuccess) {
+            tr::set_error("reading the device fault flag failed", e);
+            return TR_ERR_CUDA;
+        }
+        if (v) units += std::string(" ") + u.name;
+    }
+    if (units.empty()) return TR_OK;
     tr::set_error(("a bounded wait ran out in:" + units).c_str(), cudaSuccess);
     return TR_ERR_TIMEOUT;
 }

@@ -70,12 +70,16 @@ cudaError_t launch_inplace(void *data, int esize, int64_t batch, int64_t n, int6
 cudaError_t launch_wait_selftest(bool arrive, int64_t limit_ns, cudaStream_t stream);
 cudaError_t launch_wait_selftest_matmul(bool arrive, int64_t limit_ns, cudaStream_t stream);
 cudaError_t launch_wait_selftest_layernorm(bool arrive, int64_t limit_ns, cudaStream_t stream);
+cudaError_t launch_wait_selftest_rmsnorm(bool arrive, int64_t limit_ns, cudaStream_t stream);
+cudaError_t launch_wait_selftest_rmsnorm_backward(bool arrive, int64_t limit_ns, cudaStream_t stream);
 
 // Device-side fault flag (bounded waits that ran out).  Reads and clears it;
 // the units of the linear layer keep one of their own each (read after it).
 cudaError_t read_and_clear_fault(unsigned *value);
 cudaError_t read_and_clear_fault_matmul(unsigned *value);
 cudaError_t read_and_clear_fault_layernorm(unsigned *value);
+cudaError_t read_and_clear_fault_rmsnorm(unsigned *value);
+cudaError_t read_and_clear_fault_rmsnorm_backward(unsigned *value);
 
 // The linear layer's operators; their arguments are checked (linear_api.cu).
 cudaError_t launch_quantize(const tr_quantize_args &a);
