@@ -561,7 +561,7 @@ tr_status tr_plan_ex(const tr_args *args, const tr_options *opts, tr_plan *plan)
  * synchronizing it: TR_ERR_TIMEOUT if a bounded in-kernel wait ran out since
  * the last call, TR_OK otherwise (TR_ERR_CUDA if the read itself fails).
  * tr_last_error() then names the kernels that raised it: transpose, matmul_fp8,
- * layernorm_backward, rmsnorm, rmsnorm_backward. */
+ * layernorm_backward, rmsnorm, rmsnorm_backward, adapters. */
 tr_status tr_device_status(void);
 
 /* Exercises the failure path of the bounded in-kernel waits without any

@@ -2,10 +2,18 @@
 // each token i with its own adapter g.
 #include "adapter_plan.cuh"
 #include "launch.cuh"
+#include "operand_ring.cuh"
 #include "row_chunk.cuh"
+#include "tcgen05.cuh"
+#include "tensor_map.cuh"
 #include "tr_internal.h"
+#include "wait_selftest.cuh"
 
 namespace tr {
+
+// Set when a bounded in-kernel wait ran out; read and cleared by the host.
+__device__ unsigned g_fault_flag_adapters = 0;
+
 namespace {
 
 // --- the plan: tokens in the order of their adapters, cut into tiles -----------------------
@@ -108,59 +116,470 @@ __global__ void __launch_bounds__(kPlanThreads) k_adapter_plan(const int32_t *in
 // --- the adapters ---------------------------------------------------------------------------
 
 struct Adapt {
-    const __nv_bfloat16 *x, *a, *b;
     const float *scale;
     const int32_t *plan;
     const void *base;
     void *out;
-    int64_t tokens, adapters, k, n;
-    int64_t ld_x, ld_a, stride_a, ld_b, stride_b, ld_base, ld_out;
-    int rank;
+    int64_t tokens, adapters, n;
+    int64_t ld_base, ld_out;
+    int32_t rank, chunks;  // chunks of 64 of the contraction over k
+    int32_t split;         // CTAs that share a tile
 };
 
-// One token to a block.
+constexpr int kThreads = 192;
+constexpr int kTileX = 128 * 128;       // bytes of 128 rows x 64 values
+constexpr int kColumns = 128;           // of the output, worked on together
+constexpr int kStaging = 4 * 32 * 128;  // 32 rows of 32 sums to each of four warps
+
+// RP: the rank, filled up with zeros; TERMS: bf16 values to an inner value.
+template <int RP, int TERMS>
+struct Shape {
+    static constexpr int kStageBytes = kTileX + RP * 128;            // of x and a, or a tile of b
+    static constexpr int kPitch = RP + 4;                            // words to a row of inner values
+    static constexpr int kInner = 128 * kPitch * 4, kTerms = (RP * TERMS + 63) / 64 * kTileX;
+    static constexpr int kRegion = (kInner > kTerms ? kInner + 1023 : kTerms) / 1024 * 1024;
+    // Two CTAs to an SM where two stages leave room (each then has what two halves of tensor memory
+    // allow; a third would wait for columns that the others' clusters may need to go on).
+    static constexpr int kHalf = 111 * 1024, kWhole = 222 * 1024;
+    static constexpr int kPerSm = 2 * kStageBytes + kRegion + kStaging <= kHalf ? 2 : 1;
+    static constexpr int kFit = ((kPerSm == 2 ? kHalf : kWhole) - kRegion - kStaging) / kStageBytes;
+    static constexpr int kStages = kFit < 6 ? kFit : 6;
+    static constexpr size_t kSmem = 1024 + size_t(kStages) * kStageBytes + kRegion + kStaging;
+    static_assert(kStages >= 2 && (kPerSm == 1 || 3 * kSmem > 228 * 1024), "two CTAs to an SM at most");
+};
+
+// Copies `count` rows of columns [j0, j1) from base to out, or zeros.
 template <typename T>
-__global__ void __launch_bounds__(256) k_adapters_any(const Adapt a) {
-    pdl_prologue();
-    __shared__ float v[128];
-    [[maybe_unused]] const dbg::Side sx = dbg::side(a.x, 1, a.tokens, a.k, a.ld_x, 0, 2);
-    [[maybe_unused]] const dbg::Side sa = dbg::side(a.a, a.adapters, a.rank, a.k, a.ld_a, a.stride_a, 2);
-    [[maybe_unused]] const dbg::Side sb = dbg::side(a.b, a.adapters, a.n, a.rank, a.ld_b, a.stride_b, 2);
-    [[maybe_unused]] const dbg::Side ss = dbg::side(a.base, 1, a.tokens, a.n, a.ld_base, 0, sizeof(T));
-    [[maybe_unused]] const dbg::Side so = dbg::side(a.out, 1, a.tokens, a.n, a.ld_out, 0, sizeof(T));
+__device__ __forceinline__ void copy_rows(const Adapt &g, const int32_t *rows, int count, int64_t j0, int64_t j1, bool whole,
+                                          const dbg::Side &sb, const dbg::Side &so) {
+    constexpr int V = 16 / int(sizeof(T));
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (a.plan[1] != a.tokens || a.plan[2] != a.adapters) return;  // not these tokens' plan
-    const int tiles = a.plan[0];
-    const int32_t *order = a.plan + plan_order_at(a.tokens, a.adapters);
-    for (int64_t at = blockIdx.x; at < int64_t(tiles) * kPlanTile; at += gridDim.x) {
-        const int4 tile = *reinterpret_cast<const int4 *>(a.plan + plan_tiles_at() + 4 * (at / kPlanTile));
-        if (at % kPlanTile >= tile.z) continue;
-        const int64_t token = order[tile.y + at % kPlanTile], g = tile.x;
-        const bool bare = g >= a.adapters;
-        for (int r = warp; r < a.rank && !bare; r += 8) {
-            const __nv_bfloat16 *x = a.x + token * a.ld_x, *row = a.a + g * a.stride_a + r * a.ld_a;
-            float s = 0.0f;
-            for (int64_t l = lane; l < a.k; l += 32)
-                if (TR_LOAD_OK(sx, x + l, 2) && TR_LOAD_OK(sa, row + l, 2)) s = fmaf(to_f32(x[l]), to_f32(row[l]), s);
-            s = warp_sum(s);
-            if (lane == 0) v[r] = a.scale ? s * a.scale[g] : s;
+    for (int r = warp; r < count; r += kThreads / 32) {
+        const T *p = static_cast<const T *>(g.base) + rows[r] * g.ld_base;
+        T *o = static_cast<T *>(g.out) + rows[r] * g.ld_out;
+        if (whole) {
+            for (int64_t j = j0 + lane * V; j < j1; j += 32 * V) {
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                if (g.base && TR_LOAD_OK(sb, p + j, 16)) v = *reinterpret_cast<const uint4 *>(p + j);
+                if (TR_STORE_OK(so, o + j, 16)) *reinterpret_cast<uint4 *>(o + j) = v;
+            }
+        } else {
+            for (int64_t j = j0 + lane; j < j1; j += 32) {
+                T v = T(0.0f);
+                if (g.base && TR_LOAD_OK(sb, p + j, int(sizeof(T)))) v = p[j];
+                if (TR_STORE_OK(so, o + j, int(sizeof(T)))) o[j] = v;
+            }
         }
-        __syncthreads();
-        for (int64_t j = threadIdx.x; j < a.n; j += 256) {
-            float s = 0.0f;
-            const __nv_bfloat16 *row = a.b + g * a.stride_b + j * a.ld_b;
-            for (int r = 0; r < a.rank && !bare; ++r)
-                if (TR_LOAD_OK(sb, row + r, 2)) s = fmaf(v[r], to_f32(row[r]), s);
-            const T *p = static_cast<const T *>(a.base) + token * a.ld_base + j;
-            if (a.base && TR_LOAD_OK(ss, p, int(sizeof(T)))) s = bare ? to_f32(*p) : to_f32(*p) + s;
-            T *o = static_cast<T *>(a.out) + token * a.ld_out + j;
-            if (TR_STORE_OK(so, o, int(sizeof(T)))) put_value(o, s);
-        }
-        __syncthreads();
     }
 }
 
+// One tile of up to 128 tokens of one adapter to a cluster.  Each CTA contracts its part of k on the tensor
+// cores, D[token][r] = X A^T; the parts are joined through distributed shared memory, in rank order, each CTA
+// joining some of the tokens and fetching the others; then each CTA makes its part of the output's columns,
+// D[token][column] = V B^T, 128 at a time, with the inner values V in TERMS bf16 terms.
+//
+//   warp 0     TMA: keeps the ring full, first with x and a, then with b
+//   warp 1     matrix instructions
+//   warps 2-5  lane = token: inner values, then base + sums, with base one tile ahead in registers
+//
+// EDGE: rows of base and out that are off 16-byte boundaries or end off them.
+template <int RP, typename T, bool EDGE>
+__global__ void __launch_bounds__(kThreads, Shape<RP, sizeof(T) == 2 ? 2 : 3>::kPerSm)
+k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_rows,
+           const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const __grid_constant__ Adapt g) {
+    constexpr int TERMS = sizeof(T) == 2 ? 2 : 3;
+    using S = Shape<RP, TERMS>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t full[S::kStages], empty[S::kStages], inner_full, inner_ready, sums_full[2], sums_empty[2], drained;
+    __shared__ uint32_t tmem_base;
+    __shared__ int32_t rows[128];
+    uint8_t *stages = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *region = stages + S::kStages * S::kStageBytes;  // inner values in 32 bits, then their terms
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    if (t == 0) {
+        for (int i = 0; i < S::kStages; ++i) {
+            ptx::mbar_init(full + i, 1);
+            ptx::mbar_init(empty + i, 1);
+        }
+        ptx::mbar_init(&inner_full, 1);
+        ptx::mbar_init(&inner_ready, 4);
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(sums_full + i, 1);
+            ptx::mbar_init(sums_empty + i, 4);
+        }
+        ptx::mbar_init(&drained, 1);
+        ptx::fence_barrier_init();
+        ptx::prefetch_tensormap(&map_a);
+        ptx::prefetch_tensormap(&map_b);
+    }
+    if (warp == 1) ptx::tmem_alloc(&tmem_base, 2 * kColumns);
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = tmem_base;
+    pdl_prologue();  // after the tensor memory is taken, as in the product
+
+    const int64_t tile = blockIdx.x / unsigned(g.split);
+    const int rank = int(blockIdx.x % unsigned(g.split));
+    const bool mine = g.plan[1] == g.tokens && g.plan[2] == g.adapters && tile < g.plan[0];
+    int4 at = make_int4(0, 0, 0, 0);
+    if (mine) at = *reinterpret_cast<const int4 *>(g.plan + plan_tiles_at() + 4 * tile);
+    const int count = at.z;
+    const int64_t columns = (g.n + kColumns - 1) / kColumns;
+    const int64_t first_tile = columns * rank / g.split, last_tile = columns * (rank + 1) / g.split;
+    [[maybe_unused]] const dbg::Side sb = dbg::side(g.base, 1, g.tokens, g.n, g.ld_base, 0, sizeof(T));
+    [[maybe_unused]] const dbg::Side so = dbg::side(g.out, 1, g.tokens, g.n, g.ld_out, 0, sizeof(T));
+    if (t < count) rows[t] = g.plan[plan_order_at(g.tokens, g.adapters) + at.y + t];
+    __syncthreads();
+    bool ok = true;
+
+    if (!mine || at.x >= g.adapters || g.chunks == 0) {
+        const int64_t j1 = last_tile * kColumns;
+        if (mine && g.base != g.out) copy_rows<T>(g, rows, count, first_tile * kColumns, j1 < g.n ? j1 : g.n, !EDGE, sb, so);
+    } else {
+        const int first = int(int64_t(g.chunks) * rank / g.split), chunks = int(int64_t(g.chunks) * (rank + 1) / g.split) - first;
+        const int tiles = int(last_tile - first_tile);
+        if (warp == 0) {
+            int filled = 0;
+            // Tokens that lie side by side are one box, others four rows to a load (the last one's row fills up).
+            const bool together = rows[count - 1] - rows[0] == count - 1;
+            const int fours = (count + 3) / 4;
+            auto next = [&](auto load, uint32_t bytes) {  // lane 0
+                const int s = filled % S::kStages;
+                if (filled >= S::kStages && !ptx::mbar_wait_bounded(empty + s, ((filled / S::kStages) - 1) & 1)) ok = false;
+                if (!ok) return;
+                ptx::mbar_arrive_expect_tx(full + s, bytes);
+                load(stages + s * S::kStageBytes, full + s);
+                ++filled;
+            };
+            auto load_b = [&](int i) {
+                next([&](uint8_t *dst, uint64_t *bar) {
+                    for (int c = 0; c < RP; c += 64) ptx::tma_load_3d(dst + c / 64 * kTileX, &map_b, bar, c, int32_t((first_tile + i) * kColumns), at.x);
+                }, (RP + 63) / 64 * kTileX);
+            };
+            int i = 0;
+            if (lane == 0) {
+                for (int c = 0; c < chunks && ok; ++c)
+                    next([&](uint8_t *dst, uint64_t *bar) {
+                        const int32_t k0 = (first + c) * 64;
+                        ptx::tma_load_3d(dst + kTileX, &map_a, bar, k0, 0, at.x);
+                        if (together) {
+                            ptx::tma_load_2d(dst, &map_x, bar, k0, rows[0]);
+                        } else {
+                            for (int q = 0; q < fours; ++q) {
+                                const int last = count - 1, r = 4 * q;
+                                ptx::tma_gather4(dst + q * 512, &map_rows, bar, k0, rows[r], rows[r + 1 < last ? r + 1 : last],
+                                                 rows[r + 2 < last ? r + 2 : last], rows[r + 3 < last ? r + 3 : last]);
+                            }
+                        }
+                    }, RP * 128 + (together ? kTileX : fours * 512));
+                for (; i < tiles && i < S::kStages && ok; ++i) load_b(i);
+            }
+            __syncwarp();
+            if (g.split > 1)
+                for (int k = 0; k < 3; ++k) ptx::cluster_sync();
+            if (lane == 0) {
+                for (; i < tiles && ok; ++i) load_b(i);
+                // Nothing may arrive after the block has gone.
+                if (!leave_ring<S::kStages>(
+                        filled, [&](int s, uint32_t parity) { return ptx::mbar_wait_bounded(empty + s, parity); },
+                        [&](int s, uint32_t parity) { ptx::mbar_wait_bounded(full + s, parity); }))
+                    ok = false;
+            }
+        } else if (warp == 1) {
+            const bool leader = ptx::elect_one();
+            int used = 0;
+            auto operands = [&]() {  // the next stage's
+                const int s = used % S::kStages;
+                ok = ok && ptx::mbar_wait_bounded(full + s, (used / S::kStages) & 1);
+                ok = __all_sync(0xffffffffu, ok);
+                return s;
+            };
+            const uint32_t idesc_a = ptx::bf16_idesc(128, RP), idesc_b = ptx::bf16_idesc(128, kColumns);
+            for (int c = 0; c < chunks && ok; ++c) {
+                const int s = operands();
+                if (!ok) break;
+                ++used;
+                ptx::tc_fence_after();
+                const uint32_t p = ptx::smem_addr(stages + s * S::kStageBytes);
+                const uint64_t dx = ptx::operand_desc(p), da = ptx::operand_desc(p + kTileX);
+                if (leader) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) ptx::mma_bf16(tmem, dx + 2 * k, da + 2 * k, idesc_a, c > 0 || k > 0);
+                    ptx::mma_commit(empty + s);
+                    if (c + 1 == chunks) ptx::mma_commit(&inner_full);
+                }
+            }
+            __syncwarp();
+            if (g.split > 1)
+                for (int k = 0; k < 3; ++k) ptx::cluster_sync();
+            ok = ok && ptx::mbar_wait_bounded(&inner_ready, 0);
+            const uint32_t v = ptx::smem_addr(region);
+            for (int i = 0; i < tiles && ok; ++i) {
+                const int s = operands(), b = i & 1;
+                ok = ok && (i < 2 || ptx::mbar_wait_bounded(sums_empty + b, ((i >> 1) - 1) & 1));
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                ++used;
+                ptx::tc_fence_after();
+                const uint32_t p = ptx::smem_addr(stages + s * S::kStageBytes);
+                if (leader) {
+#pragma unroll
+                    for (int k = 0; k < TERMS * RP; k += 16) {
+                        const int kb = k % RP;
+                        ptx::mma_bf16(tmem + b * kColumns, ptx::operand_desc(v + k / 64 * kTileX) + 2 * (k % 64 / 16),
+                                      ptx::operand_desc(p + kb / 64 * kTileX) + 2 * (kb % 64 / 16), idesc_b, k > 0);
+                    }
+                    ptx::mma_commit(sums_full + b);
+                    ptx::mma_commit(empty + s);
+                }
+            }
+            if (!ok) {
+                if (leader) ptx::mma_commit(&drained);
+                ptx::mbar_wait_bounded(&drained, 0);
+            }
+        } else {
+            const int w = warp & 3;  // the quarter of the lanes this warp may read
+            const int row = w * 32 + lane, th = t - 64;
+            const uint32_t lanes = uint32_t(w * 32) << 16;
+            const float scale = g.scale ? g.scale[at.x] : 1.0f;
+            float v[RP];
+            // Inner values of this lane's token, from this CTA's part of k.
+            if (chunks) {
+                if (ok) ok = ptx::mbar_wait_bounded(&inner_full, 0);
+                __syncwarp();
+                ptx::tc_fence_after();
+                if constexpr (RP == 16) {
+                    ptx::tmem_load16(v, tmem + lanes);
+                    ptx::tmem_wait_load16(v);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < RP; c += 32) {
+                        float part[32];
+                        ptx::tmem_load32(part, tmem + lanes + c);
+                        ptx::tmem_wait_load32(part);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) v[c + k] = part[k];
+                    }
+                }
+                ptx::tc_fence_before();
+            } else {
+#pragma unroll
+                for (int c = 0; c < RP; ++c) v[c] = 0.0f;
+            }
+            if (g.split > 1) {
+                float *inner = reinterpret_cast<float *>(region);
+#pragma unroll
+                for (int c = 0; c < RP; c += 4)
+                    *reinterpret_cast<float4 *>(inner + row * S::kPitch + c) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
+                __syncwarp();
+                ptx::cluster_sync();
+                // Join the parts of 128 / split tokens, in rank order, in their place here: nobody else reads it.
+                const int share = 128 / g.split;
+                for (int k = th; k < share * (RP / 4); k += 128) {
+                    const int r = rank * share + k / (RP / 4), c = k % (RP / 4) * 4;
+                    float *p = inner + r * S::kPitch + c;
+                    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (r < count) {
+                        float4 f[8];  // all on their way before the first is used
+#pragma unroll
+                        for (int peer = 0; peer < 8; ++peer)
+                            if (peer < g.split) f[peer] = ptx::load_cluster4(ptx::peer_addr(p, uint32_t(peer)));
+#pragma unroll
+                        for (int peer = 0; peer < 8; ++peer)
+                            if (peer < g.split) sum = make_float4(sum.x + f[peer].x, sum.y + f[peer].y, sum.z + f[peer].z, sum.w + f[peer].w);
+                    }
+                    *reinterpret_cast<float4 *>(p) = sum;
+                }
+                __syncwarp();
+                ptx::cluster_sync();
+                const uint32_t from = ptx::peer_addr(inner + row * S::kPitch, uint32_t(row / share));
+#pragma unroll
+                for (int c = 0; c < RP; c += 4) {
+                    const float4 f = ptx::load_cluster4(from + 4 * c);
+                    v[c] = f.x;
+                    v[c + 1] = f.y;
+                    v[c + 2] = f.z;
+                    v[c + 3] = f.w;
+                }
+                __syncwarp();
+                ptx::cluster_sync();  // every CTA has what it needs of the others: the region is free
+            }
+            // The terms of the inner values, 8 to a 16-byte chunk of a row in the 128-byte swizzle: hi + lo (+ a
+            // third) stand for 16 (24) significant bits, in products with b that are exact in 32 bits.  An
+            // infinity is all in the first.
+#pragma unroll
+            for (int c = 0; c < RP; c += 8) {
+                float left[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) left[k] = c + k < g.rank ? v[c + k] * scale : 0.0f;
+#pragma unroll
+                for (int term = 0; term < TERMS; ++term) {
+                    uint32_t word[4];
+#pragma unroll
+                    for (int k = 0; k < 8; k += 2) {
+                        const __nv_bfloat162 two = __floats2bfloat162_rn(left[k], left[k + 1]);
+                        const float2 f = __bfloat1622float2(two);
+                        left[k] = fabsf(f.x) == INFINITY ? 0.0f : left[k] - f.x;
+                        left[k + 1] = fabsf(f.y) == INFINITY ? 0.0f : left[k + 1] - f.y;
+                        word[k / 2] = *reinterpret_cast<const uint32_t *>(&two);
+                    }
+                    const int col = term * RP + c;
+                    *reinterpret_cast<uint4 *>(region + col / 64 * kTileX + row * 128 + ((col % 64 * 2) ^ ((row & 7) << 4))) =
+                        make_uint4(word[0], word[1], word[2], word[3]);
+                }
+            }
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&inner_ready);
+            // base + sums: a quarter of the columns at a time goes through shared memory, so that lanes take
+            // neighbouring columns of a row.
+            uint4 *staging = reinterpret_cast<uint4 *>(region + S::kRegion) + w * 256;
+            constexpr int V = 16 / int(sizeof(T)), LANES = 32 / V, ROWS = 32 / LANES, LOADS = 32 / ROWS, AHEAD = 16 / LOADS;
+            uint4 old[AHEAD][LOADS];
+            auto place = [&](int l, int i, int q, int *r, int64_t *j) {  // of load l of quarter q of tile i
+                *r = w * 32 + l * ROWS + lane / LANES;
+                *j = (first_tile + i) * kColumns + q * 32 + lane % LANES * V;
+                return *r < count && *j < g.n;
+            };
+            auto fetch = [&](uint4 (&o)[LOADS], int i, int q) {
+#pragma unroll
+                for (int l = 0; l < LOADS; ++l) {
+                    int r;
+                    int64_t j;
+                    o[l] = make_uint4(0u, 0u, 0u, 0u);
+                    if (i < tiles && place(l, i, q, &r, &j) && g.base) {
+                        const T *p = static_cast<const T *>(g.base) + rows[r] * g.ld_base + j;
+                        if (TR_LOAD_OK(sb, p, 16)) o[l] = *reinterpret_cast<const uint4 *>(p);
+                    }
+                }
+            };
+            if constexpr (!EDGE)
+#pragma unroll
+                for (int q = 0; q < AHEAD; ++q) fetch(old[q], 0, q);
+            for (int i = 0; i < tiles; ++i) {
+                const int b = i & 1;
+                if (ok) ok = ptx::mbar_wait_bounded(sums_full + b, (i >> 1) & 1);
+                __syncwarp();
+                ptx::tc_fence_after();
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float sums[32];
+                    ptx::tmem_load32(sums, tmem + lanes + b * kColumns + q * 32);
+                    ptx::tmem_wait_load32(sums);
+                    if (q == 3) {  // the tensor cores may go on
+                        ptx::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive_relaxed(sums_empty + b);
+                    }
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        staging[lane * 8 + (c ^ (lane & 7))] = make_uint4(__float_as_uint(sums[4 * c]), __float_as_uint(sums[4 * c + 1]),
+                                                                          __float_as_uint(sums[4 * c + 2]), __float_as_uint(sums[4 * c + 3]));
+                    __syncwarp();
+                    if constexpr (!EDGE) {
+#pragma unroll
+                        for (int l = 0; l < LOADS; ++l) {
+                            int r;
+                            int64_t j;
+                            if (!place(l, i, q, &r, &j)) continue;
+                            const Pack<T, V> was = *reinterpret_cast<const Pack<T, V> *>(&old[q % AHEAD][l]);
+                            float f[V];
+#pragma unroll
+                            for (int c = 0; c < V / 4; ++c) {
+                                const uint4 s = staging[(r & 31) * 8 + ((lane % LANES * (V / 4) + c) ^ (r & 7))];
+                                f[4 * c] = __uint_as_float(s.x);
+                                f[4 * c + 1] = __uint_as_float(s.y);
+                                f[4 * c + 2] = __uint_as_float(s.z);
+                                f[4 * c + 3] = __uint_as_float(s.w);
+                            }
+#pragma unroll
+                            for (int k = 0; k < V; ++k) f[k] += was.get(k);
+                            Pack<T, V> o;
+                            o.round(f);
+                            T *p = static_cast<T *>(g.out) + rows[r] * g.ld_out + j;
+                            if (TR_STORE_OK(so, p, 16)) *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<const uint4 *>(&o);
+                        }
+                        fetch(old[q % AHEAD], i + (q + AHEAD) / 4, (q + AHEAD) % 4);
+                    } else {
+                        const float *f = reinterpret_cast<const float *>(staging);
+                        const int64_t j = (first_tile + i) * kColumns + q * 32 + lane;
+#pragma unroll 8
+                        for (int r = 0; r < 32; ++r) {
+                            if (w * 32 + r >= count || j >= g.n) continue;
+                            float s = f[(r * 8 + ((lane >> 2) ^ (r & 7))) * 4 + (lane & 3)];
+                            const T *p = static_cast<const T *>(g.base) + rows[w * 32 + r] * g.ld_base + j;
+                            T *o = static_cast<T *>(g.out) + rows[w * 32 + r] * g.ld_out + j;
+                            if (g.base && TR_LOAD_OK(sb, p, int(sizeof(T)))) s += to_f32(*p);
+                            if (TR_STORE_OK(so, o, int(sizeof(T)))) put_value(o, s);
+                        }
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+    }
+    if (!ok) atomicExch(&g_fault_flag_adapters, 1u);
+    __syncwarp();
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_free(tmem, 2 * kColumns);
+    }
+}
+
+// bf16 planes of rows x cols, or a matrix (planes 0): boxes of 64 columns x box_rows.
+bool encode(CUtensorMap *map, const void *base, int64_t planes, int64_t rows, int64_t cols, int64_t ld, int64_t stride, int box_rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {cuuint64_t(cols), cuuint64_t(rows), cuuint64_t(planes)};
+    const cuuint64_t strides[2] = {cuuint64_t(ld) * 2, cuuint64_t(planes > 1 ? stride : rows * ld) * 2};
+    const cuuint32_t box[3] = {64, cuuint32_t(box_rows), 1}, estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, planes ? 3 : 2, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int RP, typename T, bool EDGE>
+cudaError_t launch_one(const CUtensorMap (&maps)[4], Adapt g, int64_t tiles, cudaStream_t stream) {
+    using S = Shape<RP, sizeof(T) == 2 ? 2 : 3>;
+    auto kern = k_adapters<RP, T, EDGE>;
+    // Always the same value: setting it again is harmless.
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(S::kSmem));
+    if (e != cudaSuccess) return e;
+    // CTAs to a tile until the tiles fill what is resident at one time, each keeping two chunks of k or more.
+    const int64_t resident = int64_t(sm_count()) * S::kPerSm;
+    g.split = 1;
+    while (g.split < 8 && tiles * g.split * 2 <= resident && g.chunks >= g.split * 4) g.split *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(tiles * g.split));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = unsigned(g.split);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, kern, maps[0], maps[1], maps[2], maps[3], g);
+    if (e != cudaSuccess) (void)cudaGetLastError();
+    return e;
+}
+
+template <int RP>
+cudaError_t launch_rank(const CUtensorMap (&maps)[4], const Adapt &g, bool f32, bool edge, int64_t tiles, cudaStream_t stream) {
+    if (f32) return edge ? launch_one<RP, float, true>(maps, g, tiles, stream) : launch_one<RP, float, false>(maps, g, tiles, stream);
+    return edge ? launch_one<RP, __nv_bfloat16, true>(maps, g, tiles, stream) : launch_one<RP, __nv_bfloat16, false>(maps, g, tiles, stream);
+}
+
 }  // namespace
+
+TR_WAIT_UNIT(adapters)
 
 // Debug builds: this unit's record of refused accesses.
 TR_BOUNDS_READER(read_bounds_adapters)
@@ -179,15 +598,27 @@ cudaError_t launch_adapter_plan(const tr_adapter_plan_args &p) {
                       p.index, static_cast<int32_t *>(p.plan), int(p.tokens), int(p.adapters), int(warps));
 }
 
-cudaError_t launch_adapters(const tr_adapters_args &p) {
-    const Adapt a{static_cast<const __nv_bfloat16 *>(p.x), static_cast<const __nv_bfloat16 *>(p.a), static_cast<const __nv_bfloat16 *>(p.b),
-                  p.scale, static_cast<const int32_t *>(p.plan), p.base, p.out, p.tokens, p.adapters, p.k, p.n,
-                  p.ld_x, p.ld_a, p.stride_a, p.ld_b, p.stride_b, p.ld_base, p.ld_out, int(p.rank)};
-    const int64_t most = int64_t(1) << 30, work = plan_tiles(p.tokens, p.adapters) * kPlanTile;
-    const dim3 grid(unsigned(work < most ? work : most));
+cudaError_t launch_adapters(const tr_adapters_args &p, const char **why) {
+    const bool f32 = p.out_dtype == TR_DTYPE_F32;
+    const int es = f32 ? 4 : 2;
+    const bool edge = (p.n * es) % 16 != 0 || !side_aligned16(p.out, p.ld_out, 0, 1, es) || (p.base && !side_aligned16(p.base, p.ld_base, 0, 1, es));
+    const bool none = p.adapters == 0 || p.k == 0;  // nothing to add: base alone
+    const Adapt g{p.scale, static_cast<const int32_t *>(p.plan), p.base, p.out, p.tokens, p.adapters, p.n, p.ld_base, p.ld_out,
+                  int32_t(p.rank), none ? 0 : int32_t((p.k + 63) / 64), 1};
+    const int rp = p.rank <= 16 ? 16 : p.rank <= 32 ? 32 : p.rank <= 64 ? 64 : 128;
+    CUtensorMap maps[4] = {};
+    if (!none && (!encode(maps, p.x, 0, p.tokens, p.k, p.ld_x, 0, 128) || !encode(maps + 1, p.x, 0, p.tokens, p.k, p.ld_x, 0, 1) ||
+                  !encode(maps + 2, p.a, p.adapters, p.rank, p.k, p.ld_a, p.stride_a, rp) ||
+                  !encode(maps + 3, p.b, p.adapters, p.n, p.rank, p.ld_b, p.stride_b, kColumns))) {
+        *why = "adapters: cuTensorMapEncodeTiled rejected the operands (a pitch of 2^40 bytes or more)";
+        return cudaErrorInvalidValue;
+    }
+    const int64_t tiles = plan_tiles(p.tokens, p.adapters);
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(p.stream);
-    return p.out_dtype == TR_DTYPE_F32 ? launch_pdl(k_adapters_any<float>, grid, dim3(256), 0, stream, a)
-                                       : launch_pdl(k_adapters_any<__nv_bfloat16>, grid, dim3(256), 0, stream, a);
+    if (rp == 16) return launch_rank<16>(maps, g, f32, edge, tiles, stream);
+    if (rp == 32) return launch_rank<32>(maps, g, f32, edge, tiles, stream);
+    if (rp == 64) return launch_rank<64>(maps, g, f32, edge, tiles, stream);
+    return launch_rank<128>(maps, g, f32, edge, tiles, stream);
 }
 
 }  // namespace tr

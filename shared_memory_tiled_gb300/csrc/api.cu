@@ -296,6 +296,7 @@ const WaitUnit kWaitUnits[] = {
     {"layernorm_backward", launch_wait_selftest_layernorm, read_and_clear_fault_layernorm},
     {"rmsnorm", launch_wait_selftest_rmsnorm, read_and_clear_fault_rmsnorm},
     {"rmsnorm_backward", launch_wait_selftest_rmsnorm_backward, read_and_clear_fault_rmsnorm_backward},
+    {"adapters", launch_wait_selftest_adapters, read_and_clear_fault_adapters},
 };
 
 }  // namespace

@@ -277,7 +277,10 @@ tr_status adapters(const tr_adapters_args *a) {
     TR_TRY(side_range(a->out, a->tokens, a->n, a->ld_out, es, es, &out));
     if (a->base && same_side(a->base, a->ld_base, a->out, a->ld_out)) in[5] = Range{0, 0};
     if (outputs_overlap(&out, 1, in, 6)) return TR_ERR_OVERLAP;
-    return cuda_status("adapters launch failed", launch_adapters(*a));
+    const char *why = nullptr;
+    const cudaError_t e = launch_adapters(*a, &why);
+    if (e != cudaSuccess && why) return unsupported(why);
+    return cuda_status("adapters launch failed", e);
 }
 
 }  // namespace

@@ -72,6 +72,7 @@ cudaError_t launch_wait_selftest_matmul(bool arrive, int64_t limit_ns, cudaStrea
 cudaError_t launch_wait_selftest_layernorm(bool arrive, int64_t limit_ns, cudaStream_t stream);
 cudaError_t launch_wait_selftest_rmsnorm(bool arrive, int64_t limit_ns, cudaStream_t stream);
 cudaError_t launch_wait_selftest_rmsnorm_backward(bool arrive, int64_t limit_ns, cudaStream_t stream);
+cudaError_t launch_wait_selftest_adapters(bool arrive, int64_t limit_ns, cudaStream_t stream);
 
 // Device-side fault flag (bounded waits that ran out).  Reads and clears it;
 // the units of the linear layer keep one of their own each (read after it).
@@ -80,6 +81,7 @@ cudaError_t read_and_clear_fault_matmul(unsigned *value);
 cudaError_t read_and_clear_fault_layernorm(unsigned *value);
 cudaError_t read_and_clear_fault_rmsnorm(unsigned *value);
 cudaError_t read_and_clear_fault_rmsnorm_backward(unsigned *value);
+cudaError_t read_and_clear_fault_adapters(unsigned *value);
 
 // The linear layer's operators; their arguments are checked (linear_api.cu).
 cudaError_t launch_quantize(const tr_quantize_args &a);
@@ -89,7 +91,7 @@ cudaError_t launch_layernorm_backward(const tr_layernorm_backward_args &a);
 cudaError_t launch_rmsnorm(const tr_rmsnorm_args &a);
 cudaError_t launch_rmsnorm_backward(const tr_rmsnorm_backward_args &a);
 cudaError_t launch_adapter_plan(const tr_adapter_plan_args &a);
-cudaError_t launch_adapters(const tr_adapters_args &a);
+cudaError_t launch_adapters(const tr_adapters_args &a, const char **why);
 
 // Message behind tr_last_error() for this host thread (e: cudaSuccess = none).
 void set_error(const char *what, cudaError_t e);

@@ -1,10 +1,10 @@
-"""The fault flags of the norm's kernels, without any fault: a wait that nothing completes runs
+"""The fault flags of the norm's and the adapters' kernels, without any fault: a wait that nothing completes runs
 out, tr_device_status names the unit and clears its flag, and its kernels run as before."""
 import pytest
 
 from shared_memory_tiled_gb300 import binding as B
 
-UNITS = ["transpose", "matmul_fp8", "layernorm_backward", "rmsnorm", "rmsnorm_backward"]
+UNITS = ["transpose", "matmul_fp8", "layernorm_backward", "rmsnorm", "rmsnorm_backward", "adapters"]
 
 
 @pytest.fixture(scope="module", autouse=True)
