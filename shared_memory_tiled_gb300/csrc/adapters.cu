@@ -126,26 +126,25 @@ struct Adapt {
     int32_t split;         // CTAs that share a tile
 };
 
-constexpr int kThreads = 192;
+constexpr int kGroups = 3;              // of four warps that take sums out of tensor memory, each with its own
+constexpr int kThreads = 64 + 128 * kGroups;
 constexpr int kTileX = 128 * 128;       // bytes of 128 rows x 64 values
 constexpr int kColumns = 128;           // of the output, worked on together
-constexpr int kStaging = 4 * 32 * 128;  // 32 rows of 32 sums to each of four warps
+constexpr int kStaging = 4 * kGroups * 32 * 128;  // 32 rows of 32 sums to each warp
 
 // RP: the rank, filled up with zeros; TERMS: bf16 values to an inner value.
 template <int RP, int TERMS>
 struct Shape {
     static constexpr int kStageBytes = kTileX + RP * 128;            // of x and a, or a tile of b
+    static constexpr int kHalves = RP > 32 ? 2 : 1;                  // groups of warps that share the inner values
     static constexpr int kPitch = RP + 4;                            // words to a row of inner values
     static constexpr int kInner = 128 * kPitch * 4, kTerms = (RP * TERMS + 63) / 64 * kTileX;
     static constexpr int kRegion = (kInner > kTerms ? kInner + 1023 : kTerms) / 1024 * 1024;
-    // Two CTAs to an SM where two stages leave room (each then has what two halves of tensor memory
-    // allow; a third would wait for columns that the others' clusters may need to go on).
-    static constexpr int kHalf = 111 * 1024, kWhole = 222 * 1024;
-    static constexpr int kPerSm = 2 * kStageBytes + kRegion + kStaging <= kHalf ? 2 : 1;
-    static constexpr int kFit = ((kPerSm == 2 ? kHalf : kWhole) - kRegion - kStaging) / kStageBytes;
-    static constexpr int kStages = kFit < 6 ? kFit : 6;
+    static constexpr int kFit = (222 * 1024 - kRegion - kStaging) / kStageBytes;
+    static constexpr int kStages = kFit < 8 ? kFit : 8;
     static constexpr size_t kSmem = 1024 + size_t(kStages) * kStageBytes + kRegion + kStaging;
-    static_assert(kStages >= 2 && (kPerSm == 1 || 3 * kSmem > 228 * 1024), "two CTAs to an SM at most");
+    // One CTA to an SM: a second would wait for tensor memory that the first's cluster may need to go on.
+    static_assert(kStages >= 2 && 2 * kSmem > 228 * 1024, "one CTA to an SM");
 };
 
 // Copies `count` rows of columns [j0, j1) from base to out, or zeros.
@@ -180,17 +179,18 @@ __device__ __forceinline__ void copy_rows(const Adapt &g, const int32_t *rows, i
 //
 //   warp 0     TMA: keeps the ring full, first with x and a, then with b
 //   warp 1     matrix instructions
-//   warps 2-5  lane = token: inner values, then base + sums, with base one tile ahead in registers
+//   warps 2-   groups of four that take the tiles of columns in turn, lane = token: inner values (the first),
+//              then base + sums, with base of the group's next tile in registers
 //
 // EDGE: rows of base and out that are off 16-byte boundaries or end off them.
 template <int RP, typename T, bool EDGE>
-__global__ void __launch_bounds__(kThreads, Shape<RP, sizeof(T) == 2 ? 2 : 3>::kPerSm)
+__global__ void __launch_bounds__(kThreads, 1)
 k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_rows,
            const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const __grid_constant__ Adapt g) {
     constexpr int TERMS = sizeof(T) == 2 ? 2 : 3;
     using S = Shape<RP, TERMS>;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t full[S::kStages], empty[S::kStages], inner_full, inner_ready, sums_full[2], sums_empty[2], drained;
+    __shared__ uint64_t full[S::kStages], empty[S::kStages], inner_full, inner_ready, sums_full[kGroups], sums_empty[kGroups], drained;
     __shared__ uint32_t tmem_base;
     __shared__ int32_t rows[128];
     uint8_t *stages = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -202,8 +202,8 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
             ptx::mbar_init(empty + i, 1);
         }
         ptx::mbar_init(&inner_full, 1);
-        ptx::mbar_init(&inner_ready, 4);
-        for (int i = 0; i < 2; ++i) {
+        ptx::mbar_init(&inner_ready, 4 * S::kHalves);
+        for (int i = 0; i < kGroups; ++i) {
             ptx::mbar_init(sums_full + i, 1);
             ptx::mbar_init(sums_empty + i, 4);
         }
@@ -212,7 +212,7 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
         ptx::prefetch_tensormap(&map_a);
         ptx::prefetch_tensormap(&map_b);
     }
-    if (warp == 1) ptx::tmem_alloc(&tmem_base, 2 * kColumns);
+    if (warp == 1) ptx::tmem_alloc(&tmem_base, 512);
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
@@ -225,7 +225,7 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
     int4 at = make_int4(0, 0, 0, 0);
     if (mine) at = *reinterpret_cast<const int4 *>(g.plan + plan_tiles_at() + 4 * tile);
     const int count = at.z;
-    const int64_t columns = (g.n + kColumns - 1) / kColumns;
+    const int64_t columns = (g.n + kColumns - 1) / kColumns;  // tiles of them
     const int64_t first_tile = columns * rank / g.split, last_tile = columns * (rank + 1) / g.split;
     [[maybe_unused]] const dbg::Side sb = dbg::side(g.base, 1, g.tokens, g.n, g.ld_base, 0, sizeof(T));
     [[maybe_unused]] const dbg::Side so = dbg::side(g.out, 1, g.tokens, g.n, g.ld_out, 0, sizeof(T));
@@ -316,8 +316,8 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
             ok = ok && ptx::mbar_wait_bounded(&inner_ready, 0);
             const uint32_t v = ptx::smem_addr(region);
             for (int i = 0; i < tiles && ok; ++i) {
-                const int s = operands(), b = i & 1;
-                ok = ok && (i < 2 || ptx::mbar_wait_bounded(sums_empty + b, ((i >> 1) - 1) & 1));
+                const int s = operands(), b = i % kGroups;
+                ok = ok && (i < kGroups || ptx::mbar_wait_bounded(sums_empty + b, (i / kGroups - 1) & 1));
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 ++used;
@@ -340,182 +340,187 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
             }
         } else {
             const int w = warp & 3;  // the quarter of the lanes this warp may read
-            const int row = w * 32 + lane, th = t - 64;
+            const int row = w * 32 + lane, th = t - 64, group = (warp - 2) / 4;
             const uint32_t lanes = uint32_t(w * 32) << 16;
-            const float scale = g.scale ? g.scale[at.x] : 1.0f;
-            float v[RP];
-            // Inner values of this lane's token, from this CTA's part of k.
-            if (chunks) {
-                if (ok) ok = ptx::mbar_wait_bounded(&inner_full, 0);
-                __syncwarp();
-                ptx::tc_fence_after();
-                if constexpr (RP == 16) {
-                    ptx::tmem_load16(v, tmem + lanes);
-                    ptx::tmem_wait_load16(v);
+            if (group < S::kHalves) {
+                const float scale = g.scale ? g.scale[at.x] : 1.0f;
+                constexpr int W = RP / S::kHalves;  // inner values to a thread
+                const int c0 = group * W;
+                float v[W];
+                // Inner values of this lane's token, from this CTA's part of k.
+                if (chunks) {
+                    if (ok) ok = ptx::mbar_wait_bounded(&inner_full, 0);
+                    __syncwarp();
+                    ptx::tc_fence_after();
+                    if constexpr (W == 16) {
+                        ptx::tmem_load16(v, tmem + lanes + c0);
+                        ptx::tmem_wait_load16(v);
+                    } else {
+    #pragma unroll
+                        for (int c = 0; c < W; c += 32) {
+                            float part[32];
+                            ptx::tmem_load32(part, tmem + lanes + c0 + c);
+                            ptx::tmem_wait_load32(part);
+    #pragma unroll
+                            for (int k = 0; k < 32; ++k) v[c + k] = part[k];
+                        }
+                    }
+                    ptx::tc_fence_before();
                 } else {
-#pragma unroll
-                    for (int c = 0; c < RP; c += 32) {
-                        float part[32];
-                        ptx::tmem_load32(part, tmem + lanes + c);
-                        ptx::tmem_wait_load32(part);
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) v[c + k] = part[k];
+    #pragma unroll
+                    for (int c = 0; c < W; ++c) v[c] = 0.0f;
+                }
+                if (g.split > 1) {
+                    float *inner = reinterpret_cast<float *>(region);
+    #pragma unroll
+                    for (int c = 0; c < W; c += 4)
+                        *reinterpret_cast<float4 *>(inner + row * S::kPitch + c0 + c) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
+                    __syncwarp();
+                    ptx::cluster_sync();
+                    // Join the parts of 128 / split tokens, in rank order, in their place here: nobody else reads it.
+                    const int share = 128 / g.split;
+                    for (int k = th; k < share * (RP / 4); k += 128 * S::kHalves) {
+                        const int r = rank * share + k / (RP / 4), c = k % (RP / 4) * 4;
+                        float *p = inner + r * S::kPitch + c;
+                        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        if (r < count) {
+                            float4 f[8];  // all on their way before the first is used
+    #pragma unroll
+                            for (int peer = 0; peer < 8; ++peer)
+                                if (peer < g.split) f[peer] = ptx::load_cluster4(ptx::peer_addr(p, uint32_t(peer)));
+    #pragma unroll
+                            for (int peer = 0; peer < 8; ++peer)
+                                if (peer < g.split) sum = make_float4(sum.x + f[peer].x, sum.y + f[peer].y, sum.z + f[peer].z, sum.w + f[peer].w);
+                        }
+                        *reinterpret_cast<float4 *>(p) = sum;
+                    }
+                    __syncwarp();
+                    ptx::cluster_sync();
+                    const uint32_t from = ptx::peer_addr(inner + row * S::kPitch + c0, uint32_t(row / share));
+    #pragma unroll
+                    for (int c = 0; c < W; c += 4) {
+                        const float4 f = ptx::load_cluster4(from + 4 * c);
+                        v[c] = f.x;
+                        v[c + 1] = f.y;
+                        v[c + 2] = f.z;
+                        v[c + 3] = f.w;
+                    }
+                    __syncwarp();
+                    ptx::cluster_sync();  // every CTA has what it needs of the others: the region is free
+                }
+                // The terms of the inner values, 8 to a 16-byte chunk of a row in the 128-byte swizzle: hi + lo (+ a
+                // third) stand for 16 (24) significant bits, in products with b that are exact in 32 bits.  An
+                // infinity is all in the first.
+    #pragma unroll
+                for (int c = 0; c < W; c += 8) {
+                    float left[8];
+    #pragma unroll
+                    for (int k = 0; k < 8; ++k) left[k] = c0 + c + k < g.rank ? v[c + k] * scale : 0.0f;
+    #pragma unroll
+                    for (int term = 0; term < TERMS; ++term) {
+                        uint32_t word[4];
+    #pragma unroll
+                        for (int k = 0; k < 8; k += 2) {
+                            const __nv_bfloat162 two = __floats2bfloat162_rn(left[k], left[k + 1]);
+                            const float2 f = __bfloat1622float2(two);
+                            left[k] = fabsf(f.x) == INFINITY ? 0.0f : left[k] - f.x;
+                            left[k + 1] = fabsf(f.y) == INFINITY ? 0.0f : left[k + 1] - f.y;
+                            word[k / 2] = *reinterpret_cast<const uint32_t *>(&two);
+                        }
+                        const int col = term * RP + c0 + c;
+                        *reinterpret_cast<uint4 *>(region + col / 64 * kTileX + row * 128 + ((col % 64 * 2) ^ ((row & 7) << 4))) =
+                            make_uint4(word[0], word[1], word[2], word[3]);
                     }
                 }
-                ptx::tc_fence_before();
-            } else {
-#pragma unroll
-                for (int c = 0; c < RP; ++c) v[c] = 0.0f;
-            }
-            if (g.split > 1) {
-                float *inner = reinterpret_cast<float *>(region);
-#pragma unroll
-                for (int c = 0; c < RP; c += 4)
-                    *reinterpret_cast<float4 *>(inner + row * S::kPitch + c) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
+                ptx::fence_proxy_async_smem();
                 __syncwarp();
-                ptx::cluster_sync();
-                // Join the parts of 128 / split tokens, in rank order, in their place here: nobody else reads it.
-                const int share = 128 / g.split;
-                for (int k = th; k < share * (RP / 4); k += 128) {
-                    const int r = rank * share + k / (RP / 4), c = k % (RP / 4) * 4;
-                    float *p = inner + r * S::kPitch + c;
-                    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    if (r < count) {
-                        float4 f[8];  // all on their way before the first is used
-#pragma unroll
-                        for (int peer = 0; peer < 8; ++peer)
-                            if (peer < g.split) f[peer] = ptx::load_cluster4(ptx::peer_addr(p, uint32_t(peer)));
-#pragma unroll
-                        for (int peer = 0; peer < 8; ++peer)
-                            if (peer < g.split) sum = make_float4(sum.x + f[peer].x, sum.y + f[peer].y, sum.z + f[peer].z, sum.w + f[peer].w);
-                    }
-                    *reinterpret_cast<float4 *>(p) = sum;
-                }
-                __syncwarp();
-                ptx::cluster_sync();
-                const uint32_t from = ptx::peer_addr(inner + row * S::kPitch, uint32_t(row / share));
-#pragma unroll
-                for (int c = 0; c < RP; c += 4) {
-                    const float4 f = ptx::load_cluster4(from + 4 * c);
-                    v[c] = f.x;
-                    v[c + 1] = f.y;
-                    v[c + 2] = f.z;
-                    v[c + 3] = f.w;
-                }
-                __syncwarp();
-                ptx::cluster_sync();  // every CTA has what it needs of the others: the region is free
+                if (lane == 0) ptx::mbar_arrive(&inner_ready);
+            } else if (g.split > 1) {
+                for (int k = 0; k < 3; ++k) ptx::cluster_sync();
             }
-            // The terms of the inner values, 8 to a 16-byte chunk of a row in the 128-byte swizzle: hi + lo (+ a
-            // third) stand for 16 (24) significant bits, in products with b that are exact in 32 bits.  An
-            // infinity is all in the first.
-#pragma unroll
-            for (int c = 0; c < RP; c += 8) {
-                float left[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) left[k] = c + k < g.rank ? v[c + k] * scale : 0.0f;
-#pragma unroll
-                for (int term = 0; term < TERMS; ++term) {
-                    uint32_t word[4];
-#pragma unroll
-                    for (int k = 0; k < 8; k += 2) {
-                        const __nv_bfloat162 two = __floats2bfloat162_rn(left[k], left[k + 1]);
-                        const float2 f = __bfloat1622float2(two);
-                        left[k] = fabsf(f.x) == INFINITY ? 0.0f : left[k] - f.x;
-                        left[k + 1] = fabsf(f.y) == INFINITY ? 0.0f : left[k + 1] - f.y;
-                        word[k / 2] = *reinterpret_cast<const uint32_t *>(&two);
-                    }
-                    const int col = term * RP + c;
-                    *reinterpret_cast<uint4 *>(region + col / 64 * kTileX + row * 128 + ((col % 64 * 2) ^ ((row & 7) << 4))) =
-                        make_uint4(word[0], word[1], word[2], word[3]);
-                }
-            }
-            ptx::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&inner_ready);
             // base + sums: a quarter of the columns at a time goes through shared memory, so that lanes take
             // neighbouring columns of a row.
-            uint4 *staging = reinterpret_cast<uint4 *>(region + S::kRegion) + w * 256;
-            constexpr int V = 16 / int(sizeof(T)), LANES = 32 / V, ROWS = 32 / LANES, LOADS = 32 / ROWS, AHEAD = 16 / LOADS;
-            uint4 old[AHEAD][LOADS];
-            auto place = [&](int l, int i, int q, int *r, int64_t *j) {  // of load l of quarter q of tile i
-                *r = w * 32 + l * ROWS + lane / LANES;
-                *j = (first_tile + i) * kColumns + q * 32 + lane % LANES * V;
-                return *r < count && *j < g.n;
-            };
-            auto fetch = [&](uint4 (&o)[LOADS], int i, int q) {
+            uint4 *staging = reinterpret_cast<uint4 *>(region + S::kRegion) + (warp - 2) * 256;
+            const int n = int(g.n), j_first = int(first_tile) * kColumns;
+            // What a lane takes of a quarter: LOADS chunks of V columns, or (EDGE) a column of every row.
+            constexpr int V = EDGE ? 1 : 16 / int(sizeof(T)), LANES = 32 / V, ROWS = 32 / LANES, LOADS = 32 / ROWS;
+            constexpr int AHEAD = LOADS == 4 ? 2 : 1;  // quarters of base on their way
+            const bool some = w * 32 < count;
+            const int j_lane = lane % LANES * V, left = count - w * 32;  // rows of this warp
+            Pack<T, V> old[AHEAD][LOADS];
+            constexpr bool HELD = LOADS == 4;         // the rows' tokens in registers
+            int32_t token[HELD ? LOADS : 1];
+            if constexpr (HELD)
 #pragma unroll
                 for (int l = 0; l < LOADS; ++l) {
-                    int r;
-                    int64_t j;
-                    o[l] = make_uint4(0u, 0u, 0u, 0u);
-                    if (i < tiles && place(l, i, q, &r, &j) && g.base) {
-                        const T *p = static_cast<const T *>(g.base) + rows[r] * g.ld_base + j;
-                        if (TR_LOAD_OK(sb, p, 16)) o[l] = *reinterpret_cast<const uint4 *>(p);
+                    const int r = l * ROWS + lane / LANES;
+                    token[l] = r < left ? rows[w * 32 + r] : 0;
+                }
+            auto token_of = [&](int l) { return HELD ? token[HELD ? l : 0] : rows[w * 32 + l * ROWS + lane / LANES]; };
+            auto fetch = [&](Pack<T, V> (&o)[LOADS], int i, int q) {
+                const int j = j_first + i * kColumns + q * 32 + j_lane;
+                const bool here = i < tiles && j < n && g.base;
+#pragma unroll
+                for (int l = 0; l < LOADS; ++l) {
+                    o[l].clear();
+                    if (here && l * ROWS + lane / LANES < left) {
+                        const T *p = static_cast<const T *>(g.base) + token_of(l) * g.ld_base + j;
+                        if (TR_LOAD_OK(sb, p, int(sizeof(Pack<T, V>)))) o[l] = *reinterpret_cast<const Pack<T, V> *>(p);
                     }
                 }
             };
-            if constexpr (!EDGE)
+            if (some)
 #pragma unroll
-                for (int q = 0; q < AHEAD; ++q) fetch(old[q], 0, q);
-            for (int i = 0; i < tiles; ++i) {
-                const int b = i & 1;
-                if (ok) ok = ptx::mbar_wait_bounded(sums_full + b, (i >> 1) & 1);
+                for (int q = 0; q < AHEAD; ++q) fetch(old[q], group, q);
+            for (int i = group; i < tiles; i += kGroups) {
+                if (ok) ok = ptx::mbar_wait_bounded(sums_full + group, (i / kGroups) & 1);
                 __syncwarp();
                 ptx::tc_fence_after();
+                const uint32_t from = tmem + lanes + group * kColumns;
+                if (some) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    float sums[32];
-                    ptx::tmem_load32(sums, tmem + lanes + b * kColumns + q * 32);
-                    ptx::tmem_wait_load32(sums);
-                    if (q == 3) {  // the tensor cores may go on
-                        ptx::tc_fence_before();
+                    for (int q = 0; q < 4; ++q) {
+                        float sums[32];
+                        ptx::tmem_load32(sums, from + q * 32);
+                        ptx::tmem_wait_load32(sums);
+#pragma unroll
+                        for (int c = 0; c < 8; ++c)
+                            staging[lane * 8 + (c ^ (lane & 7))] = make_uint4(__float_as_uint(sums[4 * c]), __float_as_uint(sums[4 * c + 1]),
+                                                                              __float_as_uint(sums[4 * c + 2]), __float_as_uint(sums[4 * c + 3]));
                         __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive_relaxed(sums_empty + b);
-                    }
-#pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        staging[lane * 8 + (c ^ (lane & 7))] = make_uint4(__float_as_uint(sums[4 * c]), __float_as_uint(sums[4 * c + 1]),
-                                                                          __float_as_uint(sums[4 * c + 2]), __float_as_uint(sums[4 * c + 3]));
-                    __syncwarp();
-                    if constexpr (!EDGE) {
+                        const int j = j_first + i * kColumns + q * 32 + j_lane;
 #pragma unroll
                         for (int l = 0; l < LOADS; ++l) {
-                            int r;
-                            int64_t j;
-                            if (!place(l, i, q, &r, &j)) continue;
-                            const Pack<T, V> was = *reinterpret_cast<const Pack<T, V> *>(&old[q % AHEAD][l]);
+                            const int r = l * ROWS + lane / LANES;
                             float f[V];
+                            if constexpr (EDGE) {
+                                f[0] = reinterpret_cast<const float *>(staging)[(r * 8 + ((lane >> 2) ^ (r & 7))) * 4 + (lane & 3)];
+                            } else {
 #pragma unroll
-                            for (int c = 0; c < V / 4; ++c) {
-                                const uint4 s = staging[(r & 31) * 8 + ((lane % LANES * (V / 4) + c) ^ (r & 7))];
-                                f[4 * c] = __uint_as_float(s.x);
-                                f[4 * c + 1] = __uint_as_float(s.y);
-                                f[4 * c + 2] = __uint_as_float(s.z);
-                                f[4 * c + 3] = __uint_as_float(s.w);
+                                for (int c = 0; c < V / 4; ++c) {
+                                    const uint4 s = staging[r * 8 + ((lane % LANES * (V / 4) + c) ^ (r & 7))];
+                                    f[4 * c] = __uint_as_float(s.x);
+                                    f[4 * c + 1] = __uint_as_float(s.y);
+                                    f[4 * c + 2] = __uint_as_float(s.z);
+                                    f[4 * c + 3] = __uint_as_float(s.w);
+                                }
                             }
 #pragma unroll
-                            for (int k = 0; k < V; ++k) f[k] += was.get(k);
+                            for (int k = 0; k < V; ++k) f[k] += old[q % AHEAD][l].get(k);
                             Pack<T, V> o;
                             o.round(f);
-                            T *p = static_cast<T *>(g.out) + rows[r] * g.ld_out + j;
-                            if (TR_STORE_OK(so, p, 16)) *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<const uint4 *>(&o);
+                            if (r < left && j < n) {
+                                T *p = static_cast<T *>(g.out) + token_of(l) * g.ld_out + j;
+                                if (TR_STORE_OK(so, p, int(sizeof(o)))) *reinterpret_cast<Pack<T, V> *>(p) = o;
+                            }
                         }
-                        fetch(old[q % AHEAD], i + (q + AHEAD) / 4, (q + AHEAD) % 4);
-                    } else {
-                        const float *f = reinterpret_cast<const float *>(staging);
-                        const int64_t j = (first_tile + i) * kColumns + q * 32 + lane;
-#pragma unroll 8
-                        for (int r = 0; r < 32; ++r) {
-                            if (w * 32 + r >= count || j >= g.n) continue;
-                            float s = f[(r * 8 + ((lane >> 2) ^ (r & 7))) * 4 + (lane & 3)];
-                            const T *p = static_cast<const T *>(g.base) + rows[w * 32 + r] * g.ld_base + j;
-                            T *o = static_cast<T *>(g.out) + rows[w * 32 + r] * g.ld_out + j;
-                            if (g.base && TR_LOAD_OK(sb, p, int(sizeof(T)))) s += to_f32(*p);
-                            if (TR_STORE_OK(so, o, int(sizeof(T)))) put_value(o, s);
-                        }
+                        fetch(old[q % AHEAD], q + AHEAD < 4 ? i : i + kGroups, (q + AHEAD) % 4);
+                        __syncwarp();
                     }
-                    __syncwarp();
                 }
+                ptx::tc_fence_before();  // the tensor cores may go on
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive_relaxed(sums_empty + group);
             }
         }
     }
@@ -525,7 +530,7 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
     __syncthreads();
     if (warp == 1) {
         ptx::tc_fence_after();
-        ptx::tmem_free(tmem, 2 * kColumns);
+        ptx::tmem_free(tmem, 512);
     }
 }
 
@@ -549,7 +554,7 @@ cudaError_t launch_one(const CUtensorMap (&maps)[4], Adapt g, int64_t tiles, cud
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(S::kSmem));
     if (e != cudaSuccess) return e;
     // CTAs to a tile until the tiles fill what is resident at one time, each keeping two chunks of k or more.
-    const int64_t resident = int64_t(sm_count()) * S::kPerSm;
+    const int64_t resident = sm_count();
     g.split = 1;
     while (g.split < 8 && tiles * g.split * 2 <= resident && g.chunks >= g.split * 4) g.split *= 2;
     cudaLaunchConfig_t cfg = {};
