@@ -127,22 +127,31 @@ struct Adapt {
 };
 
 constexpr int kGroups = 3;              // of four warps that take sums out of tensor memory, each with its own
-constexpr int kThreads = 64 + 128 * kGroups;
+constexpr int kThreads = 128 + 128 * kGroups;
 constexpr int kTileX = 128 * 128;       // bytes of 128 rows x 64 values
 constexpr int kColumns = 128;           // of the output, worked on together
-constexpr int kStaging = 4 * kGroups * 32 * 128;  // 32 rows of 32 sums to each warp
+// Word c (a multiple of 4) of a row of inner values in shared memory: chunks of 16 bytes in an order that 8
+// rows' accesses to the same chunk do not share a bank.
+template <int RP>
+__device__ __forceinline__ int inner_at(int row, int c) {
+    return row * RP + ((c >> 2) ^ (RP == 16 ? row >> 1 & 3 : row & 7)) * 4;
+}
 
 // RP: the rank, filled up with zeros; TERMS: bf16 values to an inner value.
 template <int RP, int TERMS>
 struct Shape {
     static constexpr int kStageBytes = kTileX + RP * 128;            // of x and a, or a tile of b
     static constexpr int kHalves = RP > 32 ? 2 : 1;                  // groups of warps that share the inner values
-    static constexpr int kPitch = RP + 4;                            // words to a row of inner values
-    static constexpr int kInner = 128 * kPitch * 4, kTerms = (RP * TERMS + 63) / 64 * kTileX;
-    static constexpr int kRegion = (kInner > kTerms ? kInner + 1023 : kTerms) / 1024 * 1024;
-    static constexpr int kFit = (222 * 1024 - kRegion - kStaging) / kStageBytes;
-    static constexpr int kStages = kFit < 8 ? kFit : 8;
-    static constexpr size_t kSmem = 1024 + size_t(kStages) * kStageBytes + kRegion + kStaging;
+    static constexpr int kInner = 128 * RP * 4, kTerms = (RP * TERMS + 63) / 64 * kTileX;
+    static constexpr int kRegion = kInner > kTerms ? kInner : kTerms;
+    // Of 224 KB: two slots of 16 KB for base to each group (they also hold what a warp exchanges where base does not
+    // come through them), or one, and the rest for stages.
+    static constexpr int kRoom = 224 * 1024 - kRegion;
+    static constexpr int kPer = kRoom - 2 * kGroups * kTileX >= 2 * kStageBytes ? 2 : 1;
+    static constexpr int kSlots = kGroups * kPer;
+    static constexpr int kFit = (kRoom - kSlots * kTileX) / kStageBytes;
+    static constexpr int kStages = kFit < 6 ? kFit : 6;
+    static constexpr size_t kSmem = 1024 + size_t(kStages) * kStageBytes + kRegion + kSlots * kTileX;
     // One CTA to an SM: a second would wait for tensor memory that the first's cluster may need to go on.
     static_assert(kStages >= 2 && 2 * kSmem > 228 * 1024, "one CTA to an SM");
 };
@@ -179,22 +188,27 @@ __device__ __forceinline__ void copy_rows(const Adapt &g, const int32_t *rows, i
 //
 //   warp 0     TMA: keeps the ring full, first with x and a, then with b
 //   warp 1     matrix instructions
-//   warps 2-   groups of four that take the tiles of columns in turn, lane = token: inner values (the first),
-//              then base + sums, with base of the group's next tile in registers
+//   warp 2     TMA: keeps the slots full with pieces of base, 128 rows x 128 bytes in the 128-byte swizzle
+//   warps 4-   groups of four that take the tiles of columns in turn, lane = token: inner values (the first groups),
+//              then base + sums in a piece's place, and from there rows of 128 bytes to out
 //
 // EDGE: rows of base and out that are off 16-byte boundaries or end off them.
 template <int RP, typename T, bool EDGE>
 __global__ void __launch_bounds__(kThreads, 1)
 k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_rows,
-           const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const __grid_constant__ Adapt g) {
+           const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+           const __grid_constant__ CUtensorMap map_base, const __grid_constant__ CUtensorMap map_base_rows,
+           const __grid_constant__ Adapt g) {
     constexpr int TERMS = sizeof(T) == 2 ? 2 : 3;
     using S = Shape<RP, TERMS>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t full[S::kStages], empty[S::kStages], inner_full, inner_ready, sums_full[kGroups], sums_empty[kGroups], drained;
+    __shared__ uint64_t base_full[S::kSlots], base_empty[S::kSlots];
     __shared__ uint32_t tmem_base;
     __shared__ int32_t rows[128];
     uint8_t *stages = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *region = stages + S::kStages * S::kStageBytes;  // inner values in 32 bits, then their terms
+    uint8_t *slots = region + S::kRegion;
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     if (t == 0) {
         for (int i = 0; i < S::kStages; ++i) {
@@ -206,6 +220,10 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
         for (int i = 0; i < kGroups; ++i) {
             ptx::mbar_init(sums_full + i, 1);
             ptx::mbar_init(sums_empty + i, 4);
+        }
+        for (int i = 0; i < S::kSlots; ++i) {
+            ptx::mbar_init(base_full + i, 1);
+            ptx::mbar_init(base_empty + i, 4);
         }
         ptx::mbar_init(&drained, 1);
         ptx::fence_barrier_init();
@@ -239,11 +257,24 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
     } else {
         const int first = int(int64_t(g.chunks) * rank / g.split), chunks = int(int64_t(g.chunks) * (rank + 1) / g.split) - first;
         const int tiles = int(last_tile - first_tile);
+        // Tokens that lie side by side are one box, others four rows to a load (the last one's row fills up).
+        const bool together = rows[count - 1] - rows[0] == count - 1;
+        const int fours = (count + 3) / 4;
+        auto load_rows = [&](uint8_t *dst, const CUtensorMap *box, const CUtensorMap *four, uint64_t *bar, int32_t c) {
+            if (together) {
+                ptx::tma_load_2d(dst, box, bar, c, rows[0]);
+                return;
+            }
+            for (int q = 0; q < fours; ++q) {
+                const int last = count - 1, r = 4 * q;
+                ptx::tma_gather4(dst + q * 512, four, bar, c, rows[r], rows[r + 1 < last ? r + 1 : last],
+                                 rows[r + 2 < last ? r + 2 : last], rows[r + 3 < last ? r + 3 : last]);
+            }
+        };
+        const uint32_t rows_bytes = together ? kTileX : fours * 512;
+        constexpr int kPiece = 128 / int(sizeof(T)), kPieces = kColumns / kPiece;  // columns of a piece of base; pieces of a tile
         if (warp == 0) {
             int filled = 0;
-            // Tokens that lie side by side are one box, others four rows to a load (the last one's row fills up).
-            const bool together = rows[count - 1] - rows[0] == count - 1;
-            const int fours = (count + 3) / 4;
             auto next = [&](auto load, uint32_t bytes) {  // lane 0
                 const int s = filled % S::kStages;
                 if (filled >= S::kStages && !ptx::mbar_wait_bounded(empty + s, ((filled / S::kStages) - 1) & 1)) ok = false;
@@ -263,16 +294,8 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
                     next([&](uint8_t *dst, uint64_t *bar) {
                         const int32_t k0 = (first + c) * 64;
                         ptx::tma_load_3d(dst + kTileX, &map_a, bar, k0, 0, at.x);
-                        if (together) {
-                            ptx::tma_load_2d(dst, &map_x, bar, k0, rows[0]);
-                        } else {
-                            for (int q = 0; q < fours; ++q) {
-                                const int last = count - 1, r = 4 * q;
-                                ptx::tma_gather4(dst + q * 512, &map_rows, bar, k0, rows[r], rows[r + 1 < last ? r + 1 : last],
-                                                 rows[r + 2 < last ? r + 2 : last], rows[r + 3 < last ? r + 3 : last]);
-                            }
-                        }
-                    }, RP * 128 + (together ? kTileX : fours * 512));
+                        load_rows(dst, &map_x, &map_rows, bar, k0);
+                    }, RP * 128 + rows_bytes);
                 for (; i < tiles && i < S::kStages && ok; ++i) load_b(i);
             }
             __syncwarp();
@@ -338,9 +361,41 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
                 if (leader) ptx::mma_commit(&drained);
                 ptx::mbar_wait_bounded(&drained, 0);
             }
+        } else if (warp < 4) {
+            // What goes into slots that nobody has to empty first, then, past the meetings that the groups come to,
+            // the rest.
+            const int pieces = EDGE || warp != 2 || lane != 0 ? 0 : tiles * kPieces;
+            int p = 0;
+            auto load = [&](bool wait) {
+                for (; p < pieces && ok; ++p) {
+                    const int i = p / kPieces, mine = i / kGroups * kPieces + p % kPieces;  // of the group's pieces
+                    const int slot = i % kGroups * S::kPer + mine % S::kPer;
+                    if (mine >= S::kPer) {
+                        if (!wait) return;
+                        ok = ptx::mbar_wait_bounded(base_empty + slot, (mine / S::kPer - 1) & 1);
+                        if (!ok) return;
+                    }
+                    if (!g.base) {
+                        ptx::mbar_arrive(base_full + slot);
+                        continue;
+                    }
+                    ptx::mbar_arrive_expect_tx(base_full + slot, rows_bytes);
+                    load_rows(slots + slot * kTileX, &map_base, &map_base_rows, base_full + slot, int32_t(first_tile) * kColumns + p * kPiece);
+                }
+            };
+            load(false);
+            __syncwarp();
+            if (g.split > 1)
+                for (int k = 0; k < 3; ++k) ptx::cluster_sync();
+            load(true);
+            if (!ok)  // no load may land after the block has gone
+                for (int i = 0; i < S::kSlots; ++i) {
+                    ptx::mbar_wait_bounded(base_full + i, 0, 10000000);
+                    ptx::mbar_wait_bounded(base_full + i, 1, 10000000);
+                }
         } else {
             const int w = warp & 3;  // the quarter of the lanes this warp may read
-            const int row = w * 32 + lane, th = t - 64, group = (warp - 2) / 4;
+            const int row = w * 32 + lane, th = t - 128, group = (warp - 4) / 4;
             const uint32_t lanes = uint32_t(w * 32) << 16;
             if (group < S::kHalves) {
                 const float scale = g.scale ? g.scale[at.x] : 1.0f;
@@ -374,14 +429,14 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
                     float *inner = reinterpret_cast<float *>(region);
     #pragma unroll
                     for (int c = 0; c < W; c += 4)
-                        *reinterpret_cast<float4 *>(inner + row * S::kPitch + c0 + c) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
+                        *reinterpret_cast<float4 *>(inner + inner_at<RP>(row, c0 + c)) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
                     __syncwarp();
                     ptx::cluster_sync();
                     // Join the parts of 128 / split tokens, in rank order, in their place here: nobody else reads it.
                     const int share = 128 / g.split;
                     for (int k = th; k < share * (RP / 4); k += 128 * S::kHalves) {
                         const int r = rank * share + k / (RP / 4), c = k % (RP / 4) * 4;
-                        float *p = inner + r * S::kPitch + c;
+                        float *p = inner + inner_at<RP>(r, c);
                         float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                         if (r < count) {
                             float4 f[8];  // all on their way before the first is used
@@ -396,10 +451,10 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
                     }
                     __syncwarp();
                     ptx::cluster_sync();
-                    const uint32_t from = ptx::peer_addr(inner + row * S::kPitch + c0, uint32_t(row / share));
+                    const uint32_t from = ptx::peer_addr(inner, uint32_t(row / share));
     #pragma unroll
                     for (int c = 0; c < W; c += 4) {
-                        const float4 f = ptx::load_cluster4(from + 4 * c);
+                        const float4 f = ptx::load_cluster4(from + 4 * inner_at<RP>(row, c0 + c));
                         v[c] = f.x;
                         v[c + 1] = f.y;
                         v[c + 2] = f.z;
@@ -438,48 +493,72 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
             } else if (g.split > 1) {
                 for (int k = 0; k < 3; ++k) ptx::cluster_sync();
             }
-            // base + sums: a quarter of the columns at a time goes through shared memory, so that lanes take
-            // neighbouring columns of a row.
-            uint4 *staging = reinterpret_cast<uint4 *>(region + S::kRegion) + (warp - 2) * 256;
-            const int n = int(g.n), j_first = int(first_tile) * kColumns;
-            // What a lane takes of a quarter: LOADS chunks of V columns, or (EDGE) a column of every row.
-            constexpr int V = EDGE ? 1 : 16 / int(sizeof(T)), LANES = 32 / V, ROWS = 32 / LANES, LOADS = 32 / ROWS;
-            constexpr int AHEAD = LOADS == 4 ? 2 : 1;  // quarters of base on their way
-            const bool some = w * 32 < count;
-            const int j_lane = lane % LANES * V, left = count - w * 32;  // rows of this warp
-            Pack<T, V> old[AHEAD][LOADS];
-            constexpr bool HELD = LOADS == 4;         // the rows' tokens in registers
-            int32_t token[HELD ? LOADS : 1];
-            if constexpr (HELD)
-#pragma unroll
-                for (int l = 0; l < LOADS; ++l) {
-                    const int r = l * ROWS + lane / LANES;
-                    token[l] = r < left ? rows[w * 32 + r] : 0;
-                }
-            auto token_of = [&](int l) { return HELD ? token[HELD ? l : 0] : rows[w * 32 + l * ROWS + lane / LANES]; };
-            auto fetch = [&](Pack<T, V> (&o)[LOADS], int i, int q) {
-                const int j = j_first + i * kColumns + q * 32 + j_lane;
-                const bool here = i < tiles && j < n && g.base;
-#pragma unroll
-                for (int l = 0; l < LOADS; ++l) {
-                    o[l].clear();
-                    if (here && l * ROWS + lane / LANES < left) {
-                        const T *p = static_cast<const T *>(g.base) + token_of(l) * g.ld_base + j;
-                        if (TR_LOAD_OK(sb, p, int(sizeof(Pack<T, V>)))) o[l] = *reinterpret_cast<const Pack<T, V> *>(p);
-                    }
-                }
-            };
-            if (some)
-#pragma unroll
-                for (int q = 0; q < AHEAD; ++q) fetch(old[q], group, q);
+            const int n = int(g.n), j_first = int(first_tile) * kColumns, left = count - w * 32;  // rows of this warp
             for (int i = group; i < tiles; i += kGroups) {
                 if (ok) ok = ptx::mbar_wait_bounded(sums_full + group, (i / kGroups) & 1);
                 __syncwarp();
                 ptx::tc_fence_after();
                 const uint32_t from = tmem + lanes + group * kColumns;
-                if (some) {
+                if constexpr (!EDGE) {
+                    constexpr int V = 16 / int(sizeof(T));
 #pragma unroll
+                    for (int p = 0; p < kPieces; ++p) {
+                        const int mine = i / kGroups * kPieces + p, slot = group * S::kPer + mine % S::kPer;
+                        if (ok) ok = ptx::mbar_wait_bounded(base_full + slot, (mine / S::kPer) & 1);
+                        __syncwarp();
+                        if (left > 0) {
+                            uint8_t *piece = slots + slot * kTileX;
+#pragma unroll
+                            for (int c = 0; c < kPiece; c += 32) {
+                                float sums[32];
+                                ptx::tmem_load32(sums, from + p * kPiece + c);
+                                ptx::tmem_wait_load32(sums);
+#pragma unroll
+                                for (int k = 0; k < 32; k += V) {
+                                    Pack<T, V> *at = reinterpret_cast<Pack<T, V> *>(piece + row * 128 + (((c + k) * int(sizeof(T))) ^ ((row & 7) << 4)));
+                                    float f[V];
+                                    if (g.base) {
+                                        const Pack<T, V> was = *at;
+#pragma unroll
+                                        for (int q = 0; q < V; ++q) f[q] = sums[k + q] + was.get(q);
+                                    } else {
+#pragma unroll
+                                        for (int q = 0; q < V; ++q) f[q] = sums[k + q];
+                                    }
+                                    Pack<T, V> o;
+                                    o.round(f);
+                                    *at = o;
+                                }
+                            }
+                            __syncwarp();
+                            const int j = j_first + i * kColumns + p * kPiece + lane % 8 * V;
+#pragma unroll
+                            for (int l = 0; l < 8; ++l) {
+                                const int r = l * 4 + lane / 8;
+                                if (r < left && j < n) {
+                                    T *o = static_cast<T *>(g.out) + rows[w * 32 + r] * g.ld_out + j;
+                                    const uint4 v = *reinterpret_cast<const uint4 *>(piece + (w * 32 + r) * 128 + ((lane % 8 * 16) ^ ((r & 7) << 4)));
+                                    if (TR_STORE_OK(so, o, 16)) *reinterpret_cast<uint4 *>(o) = v;
+                                }
+                            }
+                            ptx::fence_proxy_async_smem();
+                        }
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(base_empty + slot);
+                    }
+                } else if (left > 0) {
+                    // A quarter of the columns at a time goes through shared memory, so that lanes take neighbouring
+                    // columns; base's values of the quarter are on their way meanwhile.
+                    uint4 *staging = reinterpret_cast<uint4 *>(slots) + (warp - 4) * 256;
+#pragma unroll 1
                     for (int q = 0; q < 4; ++q) {
+                        const int j = j_first + i * kColumns + q * 32 + lane;
+                        T old[32];
+#pragma unroll
+                        for (int r = 0; r < 32; ++r) {
+                            const T *p = static_cast<const T *>(g.base) + (r < left ? rows[w * 32 + r] : 0) * g.ld_base + j;
+                            old[r] = g.base && r < left && j < n && TR_LOAD_OK(sb, p, int(sizeof(T))) ? *p : T(0.0f);
+                        }
                         float sums[32];
                         ptx::tmem_load32(sums, from + q * 32);
                         ptx::tmem_wait_load32(sums);
@@ -488,33 +567,14 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
                             staging[lane * 8 + (c ^ (lane & 7))] = make_uint4(__float_as_uint(sums[4 * c]), __float_as_uint(sums[4 * c + 1]),
                                                                               __float_as_uint(sums[4 * c + 2]), __float_as_uint(sums[4 * c + 3]));
                         __syncwarp();
-                        const int j = j_first + i * kColumns + q * 32 + j_lane;
 #pragma unroll
-                        for (int l = 0; l < LOADS; ++l) {
-                            const int r = l * ROWS + lane / LANES;
-                            float f[V];
-                            if constexpr (EDGE) {
-                                f[0] = reinterpret_cast<const float *>(staging)[(r * 8 + ((lane >> 2) ^ (r & 7))) * 4 + (lane & 3)];
-                            } else {
-#pragma unroll
-                                for (int c = 0; c < V / 4; ++c) {
-                                    const uint4 s = staging[r * 8 + ((lane % LANES * (V / 4) + c) ^ (r & 7))];
-                                    f[4 * c] = __uint_as_float(s.x);
-                                    f[4 * c + 1] = __uint_as_float(s.y);
-                                    f[4 * c + 2] = __uint_as_float(s.z);
-                                    f[4 * c + 3] = __uint_as_float(s.w);
-                                }
-                            }
-#pragma unroll
-                            for (int k = 0; k < V; ++k) f[k] += old[q % AHEAD][l].get(k);
-                            Pack<T, V> o;
-                            o.round(f);
+                        for (int r = 0; r < 32; ++r) {
+                            const float f = reinterpret_cast<const float *>(staging)[(r * 8 + ((lane >> 2) ^ (r & 7))) * 4 + (lane & 3)];
                             if (r < left && j < n) {
-                                T *p = static_cast<T *>(g.out) + token_of(l) * g.ld_out + j;
-                                if (TR_STORE_OK(so, p, int(sizeof(o)))) *reinterpret_cast<Pack<T, V> *>(p) = o;
+                                T *o = static_cast<T *>(g.out) + rows[w * 32 + r] * g.ld_out + j;
+                                if (TR_STORE_OK(so, o, int(sizeof(T)))) put_value(o, f + to_f32(old[r]));
                             }
                         }
-                        fetch(old[q % AHEAD], q + AHEAD < 4 ? i : i + kGroups, (q + AHEAD) % 4);
                         __syncwarp();
                     }
                 }
@@ -534,20 +594,21 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
     }
 }
 
-// bf16 planes of rows x cols, or a matrix (planes 0): boxes of 64 columns x box_rows.
-bool encode(CUtensorMap *map, const void *base, int64_t planes, int64_t rows, int64_t cols, int64_t ld, int64_t stride, int box_rows) {
+// Planes of rows x cols values of 2 or 4 bytes, or a matrix (planes 0): boxes of 128 bytes x box_rows.
+bool encode(CUtensorMap *map, const void *base, int es, int64_t planes, int64_t rows, int64_t cols, int64_t ld, int64_t stride,
+            int box_rows) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t dims[3] = {cuuint64_t(cols), cuuint64_t(rows), cuuint64_t(planes)};
-    const cuuint64_t strides[2] = {cuuint64_t(ld) * 2, cuuint64_t(planes > 1 ? stride : rows * ld) * 2};
-    const cuuint32_t box[3] = {64, cuuint32_t(box_rows), 1}, estr[3] = {1, 1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, planes ? 3 : 2, const_cast<void *>(base), dims, strides, box, estr,
+    const cuuint64_t strides[2] = {cuuint64_t(ld * es), cuuint64_t((planes > 1 ? stride : rows * ld) * es)};
+    const cuuint32_t box[3] = {cuuint32_t(128 / es), cuuint32_t(box_rows), 1}, estr[3] = {1, 1, 1};
+    return fn(map, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, planes ? 3 : 2, const_cast<void *>(base), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int RP, typename T, bool EDGE>
-cudaError_t launch_one(const CUtensorMap (&maps)[4], Adapt g, int64_t tiles, cudaStream_t stream) {
+cudaError_t launch_one(const CUtensorMap (&maps)[6], Adapt g, int64_t tiles, cudaStream_t stream) {
     using S = Shape<RP, sizeof(T) == 2 ? 2 : 3>;
     auto kern = k_adapters<RP, T, EDGE>;
     // Always the same value: setting it again is harmless.
@@ -571,13 +632,13 @@ cudaError_t launch_one(const CUtensorMap (&maps)[4], Adapt g, int64_t tiles, cud
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, kern, maps[0], maps[1], maps[2], maps[3], g);
+    e = cudaLaunchKernelEx(&cfg, kern, maps[0], maps[1], maps[2], maps[3], maps[4], maps[5], g);
     if (e != cudaSuccess) (void)cudaGetLastError();
     return e;
 }
 
 template <int RP>
-cudaError_t launch_rank(const CUtensorMap (&maps)[4], const Adapt &g, bool f32, bool edge, int64_t tiles, cudaStream_t stream) {
+cudaError_t launch_rank(const CUtensorMap (&maps)[6], const Adapt &g, bool f32, bool edge, int64_t tiles, cudaStream_t stream) {
     if (f32) return edge ? launch_one<RP, float, true>(maps, g, tiles, stream) : launch_one<RP, float, false>(maps, g, tiles, stream);
     return edge ? launch_one<RP, __nv_bfloat16, true>(maps, g, tiles, stream) : launch_one<RP, __nv_bfloat16, false>(maps, g, tiles, stream);
 }
@@ -611,10 +672,12 @@ cudaError_t launch_adapters(const tr_adapters_args &p, const char **why) {
     const Adapt g{p.scale, static_cast<const int32_t *>(p.plan), p.base, p.out, p.tokens, p.adapters, p.n, p.ld_base, p.ld_out,
                   int32_t(p.rank), none ? 0 : int32_t((p.k + 63) / 64), 1};
     const int rp = p.rank <= 16 ? 16 : p.rank <= 32 ? 32 : p.rank <= 64 ? 64 : 128;
-    CUtensorMap maps[4] = {};
-    if (!none && (!encode(maps, p.x, 0, p.tokens, p.k, p.ld_x, 0, 128) || !encode(maps + 1, p.x, 0, p.tokens, p.k, p.ld_x, 0, 1) ||
-                  !encode(maps + 2, p.a, p.adapters, p.rank, p.k, p.ld_a, p.stride_a, rp) ||
-                  !encode(maps + 3, p.b, p.adapters, p.n, p.rank, p.ld_b, p.stride_b, kColumns))) {
+    CUtensorMap maps[6] = {};
+    if (!none && (!encode(maps, p.x, 2, 0, p.tokens, p.k, p.ld_x, 0, 128) || !encode(maps + 1, p.x, 2, 0, p.tokens, p.k, p.ld_x, 0, 1) ||
+                  !encode(maps + 2, p.a, 2, p.adapters, p.rank, p.k, p.ld_a, p.stride_a, rp) ||
+                  !encode(maps + 3, p.b, 2, p.adapters, p.n, p.rank, p.ld_b, p.stride_b, kColumns) ||
+                  (p.base && !edge && (!encode(maps + 4, p.base, es, 0, p.tokens, p.n, p.ld_base, 0, 128) ||
+                                       !encode(maps + 5, p.base, es, 0, p.tokens, p.n, p.ld_base, 0, 1))))) {
         *why = "adapters: cuTensorMapEncodeTiled rejected the operands (a pitch of 2^40 bytes or more)";
         return cudaErrorInvalidValue;
     }
