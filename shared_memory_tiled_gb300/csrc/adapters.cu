@@ -145,13 +145,13 @@ struct Shape {
     static constexpr int kInner = 128 * RP * 4, kTerms = (RP * TERMS + 63) / 64 * kTileX;
     static constexpr int kRegion = kInner > kTerms ? kInner : kTerms;
     // Of 224 KB: two slots of 16 KB for base to each group (they also hold what a warp exchanges where base does not
-    // come through them), or one, and the rest for stages.
+    // come through them), or one, and the rest for stages.  Before the inner values are there the slots are stages too.
     static constexpr int kRoom = 224 * 1024 - kRegion;
     static constexpr int kPer = kRoom - 2 * kGroups * kTileX >= 2 * kStageBytes ? 2 : 1;
     static constexpr int kSlots = kGroups * kPer;
-    static constexpr int kFit = (kRoom - kSlots * kTileX) / kStageBytes;
-    static constexpr int kStages = kFit < 6 ? kFit : 6;
-    static constexpr size_t kSmem = 1024 + size_t(kStages) * kStageBytes + kRegion + kSlots * kTileX;
+    static constexpr int kStages = (kRoom - kSlots * kTileX) / kStageBytes < 6 ? (kRoom - kSlots * kTileX) / kStageBytes : 6;
+    static constexpr int kStagesX = kRoom / kStageBytes < 12 ? kRoom / kStageBytes : 12;
+    static constexpr size_t kSmem = 1024 + kRegion + size_t(kRoom);
     // One CTA to an SM: a second would wait for tensor memory that the first's cluster may need to go on.
     static_assert(kStages >= 2 && 2 * kSmem > 228 * 1024, "one CTA to an SM");
 };
@@ -165,17 +165,33 @@ __device__ __forceinline__ void copy_rows(const Adapt &g, const int32_t *rows, i
     for (int r = warp; r < count; r += kThreads / 32) {
         const T *p = static_cast<const T *>(g.base) + rows[r] * g.ld_base;
         T *o = static_cast<T *>(g.out) + rows[r] * g.ld_out;
+        constexpr int U = 8;  // loads on their way
         if (whole) {
-            for (int64_t j = j0 + lane * V; j < j1; j += 32 * V) {
-                uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                if (g.base && TR_LOAD_OK(sb, p + j, 16)) v = *reinterpret_cast<const uint4 *>(p + j);
-                if (TR_STORE_OK(so, o + j, 16)) *reinterpret_cast<uint4 *>(o + j) = v;
+            for (int64_t j = j0 + lane * V; j < j1; j += U * 32 * V) {
+                uint4 v[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int64_t c = j + u * 32 * V;
+                    v[u] = make_uint4(0u, 0u, 0u, 0u);
+                    if (g.base && c < j1 && TR_LOAD_OK(sb, p + c, 16)) v[u] = *reinterpret_cast<const uint4 *>(p + c);
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int64_t c = j + u * 32 * V;
+                    if (c < j1 && TR_STORE_OK(so, o + c, 16)) *reinterpret_cast<uint4 *>(o + c) = v[u];
+                }
             }
         } else {
-            for (int64_t j = j0 + lane; j < j1; j += 32) {
-                T v = T(0.0f);
-                if (g.base && TR_LOAD_OK(sb, p + j, int(sizeof(T)))) v = p[j];
-                if (TR_STORE_OK(so, o + j, int(sizeof(T)))) o[j] = v;
+            for (int64_t j = j0 + lane; j < j1; j += U * 32) {
+                T v[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int64_t c = j + u * 32;
+                    v[u] = g.base && c < j1 && TR_LOAD_OK(sb, p + c, int(sizeof(T))) ? p[c] : T(0.0f);
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (j + u * 32 < j1 && TR_STORE_OK(so, o + j + u * 32, int(sizeof(T)))) o[j + u * 32] = v[u];
             }
         }
     }
@@ -202,19 +218,24 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
     constexpr int TERMS = sizeof(T) == 2 ? 2 : 3;
     using S = Shape<RP, TERMS>;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t full[S::kStages], empty[S::kStages], inner_full, inner_ready, sums_full[kGroups], sums_empty[kGroups], drained;
+    __shared__ uint64_t full_x[S::kStagesX], empty_x[S::kStagesX], full[S::kStages], empty[S::kStages], joined[3], inner_full, inner_ready, sums_full[kGroups], sums_empty[kGroups], drained;
     __shared__ uint64_t base_full[S::kSlots], base_empty[S::kSlots];
     __shared__ uint32_t tmem_base;
     __shared__ int32_t rows[128];
     uint8_t *stages = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t *region = stages + S::kStages * S::kStageBytes;  // inner values in 32 bits, then their terms
-    uint8_t *slots = region + S::kRegion;
+    uint8_t *slots = stages + S::kStages * S::kStageBytes;
+    uint8_t *region = stages + S::kRoom;  // inner values in 32 bits, then their terms
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     if (t == 0) {
         for (int i = 0; i < S::kStages; ++i) {
             ptx::mbar_init(full + i, 1);
             ptx::mbar_init(empty + i, 1);
         }
+        for (int i = 0; i < S::kStagesX; ++i) {
+            ptx::mbar_init(full_x + i, 1);
+            ptx::mbar_init(empty_x + i, 1);
+        }
+        for (int i = 0; i < 3; ++i) ptx::mbar_init(joined + i, 4 * S::kHalves * g.split);
         ptx::mbar_init(&inner_full, 1);
         ptx::mbar_init(&inner_ready, 4 * S::kHalves);
         for (int i = 0; i < kGroups; ++i) {
@@ -233,6 +254,7 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
     if (warp == 1) ptx::tmem_alloc(&tmem_base, 512);
     ptx::tc_fence_before();
     __syncthreads();
+    if (g.split > 1) ptx::cluster_sync();  // the others' barriers are ready
     ptx::tc_fence_after();
     const uint32_t tmem = tmem_base;
     pdl_prologue();  // after the tensor memory is taken, as in the product
@@ -274,76 +296,63 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
         const uint32_t rows_bytes = together ? kTileX : fours * 512;
         constexpr int kPiece = 128 / int(sizeof(T)), kPieces = kColumns / kPiece;  // columns of a piece of base; pieces of a tile
         if (warp == 0) {
-            int filled = 0;
-            auto next = [&](auto load, uint32_t bytes) {  // lane 0
-                const int s = filled % S::kStages;
-                if (filled >= S::kStages && !ptx::mbar_wait_bounded(empty + s, ((filled / S::kStages) - 1) & 1)) ok = false;
-                if (!ok) return;
-                ptx::mbar_arrive_expect_tx(full + s, bytes);
-                load(stages + s * S::kStageBytes, full + s);
-                ++filled;
-            };
-            auto load_b = [&](int i) {
-                next([&](uint8_t *dst, uint64_t *bar) {
-                    for (int c = 0; c < RP; c += 64) ptx::tma_load_3d(dst + c / 64 * kTileX, &map_b, bar, c, int32_t((first_tile + i) * kColumns), at.x);
-                }, (RP + 63) / 64 * kTileX);
-            };
-            int i = 0;
             if (lane == 0) {
-                for (int c = 0; c < chunks && ok; ++c)
-                    next([&](uint8_t *dst, uint64_t *bar) {
-                        const int32_t k0 = (first + c) * 64;
-                        ptx::tma_load_3d(dst + kTileX, &map_a, bar, k0, 0, at.x);
-                        load_rows(dst, &map_x, &map_rows, bar, k0);
-                    }, RP * 128 + rows_bytes);
-                for (; i < tiles && i < S::kStages && ok; ++i) load_b(i);
-            }
-            __syncwarp();
-            if (g.split > 1)
-                for (int k = 0; k < 3; ++k) ptx::cluster_sync();
-            if (lane == 0) {
-                for (; i < tiles && ok; ++i) load_b(i);
-                // Nothing may arrive after the block has gone.
+                int c = 0, i = 0;
+                for (; c < chunks; ++c) {
+                    const int s = c % S::kStagesX;
+                    if (c >= S::kStagesX) ok = ptx::mbar_wait_bounded(empty_x + s, (c / S::kStagesX - 1) & 1);
+                    if (!ok) break;
+                    uint8_t *dst = stages + s * S::kStageBytes;
+                    const int32_t k0 = (first + c) * 64;
+                    ptx::mbar_arrive_expect_tx(full_x + s, RP * 128 + rows_bytes);
+                    ptx::tma_load_3d(dst + kTileX, &map_a, full_x + s, k0, 0, at.x);
+                    load_rows(dst, &map_x, &map_rows, full_x + s, k0);
+                }
+                // Nothing may arrive after the block has gone, nor into memory that is used for something else.
+                if (!leave_ring<S::kStagesX>(
+                        c, [&](int s, uint32_t parity) { return ptx::mbar_wait_bounded(empty_x + s, parity); },
+                        [&](int s, uint32_t parity) { ptx::mbar_wait_bounded(full_x + s, parity); }))
+                    ok = false;
+                for (; i < tiles && ok; ++i) {
+                    const int s = i % S::kStages;
+                    if (i >= S::kStages) ok = ptx::mbar_wait_bounded(empty + s, (i / S::kStages - 1) & 1);
+                    if (!ok) break;
+                    ptx::mbar_arrive_expect_tx(full + s, (RP + 63) / 64 * kTileX);
+                    for (int k = 0; k < RP; k += 64)
+                        ptx::tma_load_3d(stages + s * S::kStageBytes + k / 64 * kTileX, &map_b, full + s, k, int32_t((first_tile + i) * kColumns), at.x);
+                }
                 if (!leave_ring<S::kStages>(
-                        filled, [&](int s, uint32_t parity) { return ptx::mbar_wait_bounded(empty + s, parity); },
+                        i, [&](int s, uint32_t parity) { return ptx::mbar_wait_bounded(empty + s, parity); },
                         [&](int s, uint32_t parity) { ptx::mbar_wait_bounded(full + s, parity); }))
                     ok = false;
             }
         } else if (warp == 1) {
             const bool leader = ptx::elect_one();
-            int used = 0;
-            auto operands = [&]() {  // the next stage's
-                const int s = used % S::kStages;
-                ok = ok && ptx::mbar_wait_bounded(full + s, (used / S::kStages) & 1);
-                ok = __all_sync(0xffffffffu, ok);
-                return s;
-            };
             const uint32_t idesc_a = ptx::bf16_idesc(128, RP), idesc_b = ptx::bf16_idesc(128, kColumns);
             for (int c = 0; c < chunks && ok; ++c) {
-                const int s = operands();
+                const int s = c % S::kStagesX;
+                ok = ptx::mbar_wait_bounded(full_x + s, (c / S::kStagesX) & 1);
+                ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                ++used;
                 ptx::tc_fence_after();
                 const uint32_t p = ptx::smem_addr(stages + s * S::kStageBytes);
                 const uint64_t dx = ptx::operand_desc(p), da = ptx::operand_desc(p + kTileX);
                 if (leader) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) ptx::mma_bf16(tmem, dx + 2 * k, da + 2 * k, idesc_a, c > 0 || k > 0);
-                    ptx::mma_commit(empty + s);
+                    ptx::mma_commit(empty_x + s);
                     if (c + 1 == chunks) ptx::mma_commit(&inner_full);
                 }
             }
             __syncwarp();
-            if (g.split > 1)
-                for (int k = 0; k < 3; ++k) ptx::cluster_sync();
             ok = ok && ptx::mbar_wait_bounded(&inner_ready, 0);
             const uint32_t v = ptx::smem_addr(region);
             for (int i = 0; i < tiles && ok; ++i) {
-                const int s = operands(), b = i % kGroups;
-                ok = ok && (i < kGroups || ptx::mbar_wait_bounded(sums_empty + b, (i / kGroups - 1) & 1));
+                const int s = i % S::kStages, b = i % kGroups;
+                ok = ok && ptx::mbar_wait_bounded(full + s, (i / S::kStages) & 1) &&
+                     (i < kGroups || ptx::mbar_wait_bounded(sums_empty + b, (i / kGroups - 1) & 1));
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                ++used;
                 ptx::tc_fence_after();
                 const uint32_t p = ptx::smem_addr(stages + s * S::kStageBytes);
                 if (leader) {
@@ -362,32 +371,20 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
                 ptx::mbar_wait_bounded(&drained, 0);
             }
         } else if (warp < 4) {
-            // What goes into slots that nobody has to empty first, then, past the meetings that the groups come to,
-            // the rest.
             const int pieces = EDGE || warp != 2 || lane != 0 ? 0 : tiles * kPieces;
-            int p = 0;
-            auto load = [&](bool wait) {
-                for (; p < pieces && ok; ++p) {
-                    const int i = p / kPieces, mine = i / kGroups * kPieces + p % kPieces;  // of the group's pieces
-                    const int slot = i % kGroups * S::kPer + mine % S::kPer;
-                    if (mine >= S::kPer) {
-                        if (!wait) return;
-                        ok = ptx::mbar_wait_bounded(base_empty + slot, (mine / S::kPer - 1) & 1);
-                        if (!ok) return;
-                    }
-                    if (!g.base) {
-                        ptx::mbar_arrive(base_full + slot);
-                        continue;
-                    }
-                    ptx::mbar_arrive_expect_tx(base_full + slot, rows_bytes);
-                    load_rows(slots + slot * kTileX, &map_base, &map_base_rows, base_full + slot, int32_t(first_tile) * kColumns + p * kPiece);
+            if (pieces && chunks) ok = ptx::mbar_wait_bounded(&inner_full, 0);  // the slots were stages
+            for (int p = 0; p < pieces && ok; ++p) {
+                const int i = p / kPieces, mine = i / kGroups * kPieces + p % kPieces;  // of the group's pieces
+                const int slot = i % kGroups * S::kPer + mine % S::kPer;
+                if (mine >= S::kPer) ok = ptx::mbar_wait_bounded(base_empty + slot, (mine / S::kPer - 1) & 1);
+                if (!ok) break;
+                if (!g.base) {
+                    ptx::mbar_arrive(base_full + slot);
+                    continue;
                 }
-            };
-            load(false);
-            __syncwarp();
-            if (g.split > 1)
-                for (int k = 0; k < 3; ++k) ptx::cluster_sync();
-            load(true);
+                ptx::mbar_arrive_expect_tx(base_full + slot, rows_bytes);
+                load_rows(slots + slot * kTileX, &map_base, &map_base_rows, base_full + slot, int32_t(first_tile) * kColumns + p * kPiece);
+            }
             if (!ok)  // no load may land after the block has gone
                 for (int i = 0; i < S::kSlots; ++i) {
                     ptx::mbar_wait_bounded(base_full + i, 0, 10000000);
@@ -427,41 +424,60 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
                 }
                 if (g.split > 1) {
                     float *inner = reinterpret_cast<float *>(region);
-    #pragma unroll
+#pragma unroll
                     for (int c = 0; c < W; c += 4)
                         *reinterpret_cast<float4 *>(inner + inner_at<RP>(row, c0 + c)) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
-                    __syncwarp();
-                    ptx::cluster_sync();
-                    // Join the parts of 128 / split tokens, in rank order, in their place here: nobody else reads it.
-                    const int share = 128 / g.split;
-                    for (int k = th; k < share * (RP / 4); k += 128 * S::kHalves) {
-                        const int r = rank * share + k / (RP / 4), c = k % (RP / 4) * 4;
-                        float *p = inner + inner_at<RP>(r, c);
-                        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                        if (r < count) {
+                    // A warp tells every CTA that it has come to a point, and waits until all warps have.
+                    auto meet = [&](int k) {
+                        __syncwarp();
+                        if (lane < g.split) ptx::mbar_arrive_release_at(ptx::peer_addr(joined + k, uint32_t(lane)));
+                        if (ok) ok = ptx::mbar_wait_cluster(joined + k, 0);
+                        __syncwarp();
+                    };
+                    meet(0);
+                    if (g.split == 2) {
+                        // Both parts of the row, in rank order.
+                        const uint32_t one = ptx::peer_addr(inner, 0), two = ptx::peer_addr(inner, 1);
+#pragma unroll
+                        for (int c = 0; c < W; c += 4) {
+                            const int word = 4 * inner_at<RP>(row, c0 + c);
+                            const float4 a = ptx::load_cluster4(one + word), b = ptx::load_cluster4(two + word);
+                            v[c] = a.x + b.x;
+                            v[c + 1] = a.y + b.y;
+                            v[c + 2] = a.z + b.z;
+                            v[c + 3] = a.w + b.w;
+                        }
+                    } else {
+                        // Join the parts of 128 / split tokens, in rank order, in their place here: nobody else reads it.
+                        const int share = 128 / g.split;
+                        for (int k = th; k < share * (RP / 4); k += 128 * S::kHalves) {
+                            const int r = rank * share + k / (RP / 4), c = k % (RP / 4) * 4;
+                            if (r >= count) continue;
+                            float *p = inner + inner_at<RP>(r, c);
+                            float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                             float4 f[8];  // all on their way before the first is used
-    #pragma unroll
+#pragma unroll
                             for (int peer = 0; peer < 8; ++peer)
                                 if (peer < g.split) f[peer] = ptx::load_cluster4(ptx::peer_addr(p, uint32_t(peer)));
-    #pragma unroll
+#pragma unroll
                             for (int peer = 0; peer < 8; ++peer)
                                 if (peer < g.split) sum = make_float4(sum.x + f[peer].x, sum.y + f[peer].y, sum.z + f[peer].z, sum.w + f[peer].w);
+                            *reinterpret_cast<float4 *>(p) = sum;
                         }
-                        *reinterpret_cast<float4 *>(p) = sum;
+                        meet(1);
+                        if (row < count) {
+                            const uint32_t from = ptx::peer_addr(inner, uint32_t(row / share));
+#pragma unroll
+                            for (int c = 0; c < W; c += 4) {
+                                const float4 f = ptx::load_cluster4(from + 4 * inner_at<RP>(row, c0 + c));
+                                v[c] = f.x;
+                                v[c + 1] = f.y;
+                                v[c + 2] = f.z;
+                                v[c + 3] = f.w;
+                            }
+                        }
                     }
-                    __syncwarp();
-                    ptx::cluster_sync();
-                    const uint32_t from = ptx::peer_addr(inner, uint32_t(row / share));
-    #pragma unroll
-                    for (int c = 0; c < W; c += 4) {
-                        const float4 f = ptx::load_cluster4(from + 4 * inner_at<RP>(row, c0 + c));
-                        v[c] = f.x;
-                        v[c + 1] = f.y;
-                        v[c + 2] = f.z;
-                        v[c + 3] = f.w;
-                    }
-                    __syncwarp();
-                    ptx::cluster_sync();  // every CTA has what it needs of the others: the region is free
+                    meet(2);  // every CTA has what it needs of the others: the region is free
                 }
                 // The terms of the inner values, 8 to a 16-byte chunk of a row in the 128-byte swizzle: hi + lo (+ a
                 // third) stand for 16 (24) significant bits, in products with b that are exact in 32 bits.  An
@@ -490,10 +506,11 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
                 ptx::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(&inner_ready);
-            } else if (g.split > 1) {
-                for (int k = 0; k < 3; ++k) ptx::cluster_sync();
             }
             const int n = int(g.n), j_first = int(first_tile) * kColumns, left = count - w * 32;  // rows of this warp
+            int32_t token[8];  // of the rows that this lane stores
+#pragma unroll
+            for (int l = 0; l < 8; ++l) token[l] = l * 4 + lane / 8 < left ? rows[w * 32 + l * 4 + lane / 8] : 0;
             for (int i = group; i < tiles; i += kGroups) {
                 if (ok) ok = ptx::mbar_wait_bounded(sums_full + group, (i / kGroups) & 1);
                 __syncwarp();
@@ -507,7 +524,11 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
                         if (ok) ok = ptx::mbar_wait_bounded(base_full + slot, (mine / S::kPer) & 1);
                         __syncwarp();
                         if (left > 0) {
-                            uint8_t *piece = slots + slot * kTileX;
+                            // Every step's accesses are under way before the first is used.
+                            const uint32_t piece = ptx::smem_addr(slots + slot * kTileX), own = piece + row * 128;
+                            uint4 was[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) was[k] = g.base ? ptx::load_shared_16(own + ((k ^ (row & 7)) << 4)) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
                             for (int c = 0; c < kPiece; c += 32) {
                                 float sums[32];
@@ -515,19 +536,14 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
                                 ptx::tmem_wait_load32(sums);
 #pragma unroll
                                 for (int k = 0; k < 32; k += V) {
-                                    Pack<T, V> *at = reinterpret_cast<Pack<T, V> *>(piece + row * 128 + (((c + k) * int(sizeof(T))) ^ ((row & 7) << 4)));
+                                    const int at = (c + k) / V;
+                                    const Pack<T, V> old = *reinterpret_cast<const Pack<T, V> *>(&was[at]);
                                     float f[V];
-                                    if (g.base) {
-                                        const Pack<T, V> was = *at;
 #pragma unroll
-                                        for (int q = 0; q < V; ++q) f[q] = sums[k + q] + was.get(q);
-                                    } else {
-#pragma unroll
-                                        for (int q = 0; q < V; ++q) f[q] = sums[k + q];
-                                    }
+                                    for (int q = 0; q < V; ++q) f[q] = sums[k + q] + old.get(q);
                                     Pack<T, V> o;
                                     o.round(f);
-                                    *at = o;
+                                    ptx::store_shared_16(own + ((at ^ (row & 7)) << 4), *reinterpret_cast<const uint4 *>(&o));
                                 }
                             }
                             __syncwarp();
@@ -535,12 +551,14 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
 #pragma unroll
                             for (int l = 0; l < 8; ++l) {
                                 const int r = l * 4 + lane / 8;
-                                if (r < left && j < n) {
-                                    T *o = static_cast<T *>(g.out) + rows[w * 32 + r] * g.ld_out + j;
-                                    const uint4 v = *reinterpret_cast<const uint4 *>(piece + (w * 32 + r) * 128 + ((lane % 8 * 16) ^ ((r & 7) << 4)));
-                                    if (TR_STORE_OK(so, o, 16)) *reinterpret_cast<uint4 *>(o) = v;
-                                }
+                                was[l] = ptx::load_shared_16(piece + (w * 32 + r) * 128 + ((lane ^ r) % 8 << 4));
                             }
+#pragma unroll
+                            for (int l = 0; l < 8; ++l)
+                                if (l * 4 + lane / 8 < left && j < n) {
+                                    T *o = static_cast<T *>(g.out) + token[l] * g.ld_out + j;
+                                    if (TR_STORE_OK(so, o, 16)) *reinterpret_cast<uint4 *>(o) = was[l];
+                                }
                             ptx::fence_proxy_async_smem();
                         }
                         __syncwarp();
@@ -588,6 +606,7 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
     __syncwarp();
     ptx::tc_fence_before();
     __syncthreads();
+    if (g.split > 1) ptx::cluster_sync();  // nobody leaves while another may read its shared memory, whatever ran out before
     if (warp == 1) {
         ptx::tc_fence_after();
         ptx::tmem_free(tmem, 512);
@@ -669,8 +688,8 @@ cudaError_t launch_adapters(const tr_adapters_args &p, const char **why) {
     const int es = f32 ? 4 : 2;
     const bool edge = (p.n * es) % 16 != 0 || !side_aligned16(p.out, p.ld_out, 0, 1, es) || (p.base && !side_aligned16(p.base, p.ld_base, 0, 1, es));
     const bool none = p.adapters == 0 || p.k == 0;  // nothing to add: base alone
-    const Adapt g{p.scale, static_cast<const int32_t *>(p.plan), p.base, p.out, p.tokens, p.adapters, p.n, p.ld_base, p.ld_out,
-                  int32_t(p.rank), none ? 0 : int32_t((p.k + 63) / 64), 1};
+    const Adapt g{p.scale, static_cast<const int32_t *>(p.plan), p.base, p.out, p.tokens, p.adapters,
+                  p.n, p.ld_base, p.ld_out, int32_t(p.rank), none ? 0 : int32_t((p.k + 63) / 64), 1};
     const int rp = p.rank <= 16 ? 16 : p.rank <= 32 ? 32 : p.rank <= 64 ? 64 : 128;
     CUtensorMap maps[6] = {};
     if (!none && (!encode(maps, p.x, 2, 0, p.tokens, p.k, p.ld_x, 0, 128) || !encode(maps + 1, p.x, 2, 0, p.tokens, p.k, p.ld_x, 0, 1) ||

@@ -175,6 +175,29 @@ __device__ __forceinline__ void mbar_arrive_at(uint32_t addr) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 
+// Arrival on a barrier of the cluster's window that orders the warp's earlier accesses (behind __syncwarp), and the
+// bounded wait that goes with it.
+__device__ __forceinline__ void mbar_arrive_release_at(uint32_t addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity, uint64_t limit_ns = 1000000000ull,
+                                                  uint32_t max_probes = 1u << 28) {
+    const uint64_t t0 = global_timer_ns();
+    for (uint32_t n = 0; n < max_probes; ++n) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(smem_addr(bar)), "r"(parity)
+            : "memory");
+        if (done) return true;
+        if ((n & 255u) == 255u && global_timer_ns() - t0 > limit_ns) return false;
+    }
+    return false;
+}
+
 // Registers of each thread of this warpgroup: a block's warpgroups share what it was
 // launched with, so their sum stays at or below that.
 template <int N>
