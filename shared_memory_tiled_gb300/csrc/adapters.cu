@@ -1,5 +1,7 @@
 // Low-rank adapters of many requests at once: out[i] = base[i] + B_g (scale_g A_g x_i) for
 // each token i with its own adapter g.
+#include <type_traits>
+
 #include "adapter_plan.cuh"
 #include "launch.cuh"
 #include "operand_ring.cuh"
@@ -613,6 +615,265 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
     }
 }
 
+// --- a few tokens ---------------------------------------------------------------------------
+//
+// Next tokens of many requests: most adapters have a token or two, and what counts is how soon the adapters' bytes are
+// here.  A cluster to a tile as above, but no tensor memory, tensor maps or rings to set up: each warp reads its
+// part of the adapter straight into the fragments of warp-wide matrix instructions, 16 tokens by 8 ranks (columns).
+// The order of a contraction is free, so a lane's 16 contiguous bytes serve as the fragments of two
+// instructions.  The columns of four instructions are spread so that a lane ends up with 8 neighbouring ones.
+
+struct Few {
+    const __nv_bfloat16 *x, *a, *b;
+    const float *scale;
+    const int32_t *plan;
+    const void *base;
+    void *out;
+    int64_t tokens, adapters, ld_x, ld_a, stride_a, ld_b, stride_b, ld_base, ld_out;
+    int32_t rank, k, n, split;
+};
+
+constexpr int64_t kFewTokens = 64;  // up to here these kernels
+constexpr int kFewThreads = 256, kFewWarps = kFewThreads / 32;
+
+// D[16][8] += A[16][16] B[8][16]^T, a fragment's words being pairs along the contraction.
+__device__ __forceinline__ void mma_16x8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// N (4 or 8) values of a row from column c on, zeros from `cols` on and where there is no row.  WHOLE: all of them
+// are below `cols` or none is; a load without a branch, so that many can be under way.
+template <int N, bool WHOLE>
+__device__ __forceinline__ uint4 values(const __nv_bfloat16 *row, int c, int cols, bool have, const dbg::Side &s) {
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if constexpr (WHOLE) {
+        if (have && c < cols && TR_LOAD_OK(s, row + c, 2 * N)) {
+            if constexpr (N == 8) {
+                v = *reinterpret_cast<const uint4 *>(row + c);
+            } else {
+                const uint2 two = *reinterpret_cast<const uint2 *>(row + c);
+                v.x = two.x;
+                v.y = two.y;
+            }
+        }
+        return v;
+    }
+    if (!have) return v;
+    uint32_t w[4] = {};
+#pragma unroll
+    for (int q = 0; q < N; ++q)
+        if (c + q < cols && TR_LOAD_OK(s, row + c + q, 2)) w[q / 2] |= uint32_t(__bfloat16_as_ushort(row[c + q])) << (q % 2 * 16);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+constexpr int few_shares(int rp) { return rp <= 32 ? 1 : rp / 32; }
+
+// EDGE: as above.
+template <int RP, typename T, bool EDGE>
+__global__ void __launch_bounds__(kFewThreads, 2) k_adapters_few(const Few g) {
+    pdl_prologue();
+    constexpr int TERMS = sizeof(T) == 2 ? 2 : 3;
+    constexpr int RC = RP == 16 ? 4 : 8, STEPS = RP / (4 * RC);  // values of a row of b to a lane and step
+    constexpr int PITCH = RP + 8;                                // of the terms, in values
+    constexpr int AHEAD = RP <= 64 ? 2 : 1;                      // units of 32 columns whose b and base are read before the inner values are there
+    constexpr int SHARES = few_shares(RP), RW = RP / SHARES;     // warps share the ranks first, RW to each, then k
+    extern __shared__ float part[];                              // [warps / SHARES][16][RP]
+    __shared__ float sums[16][RP + 4];
+    __shared__ alignas(16) __nv_bfloat16 terms[TERMS][16][PITCH];
+    __shared__ int32_t rows[128];
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5, gid = lane >> 2, tid = lane & 3;
+    const int64_t tile = blockIdx.x / unsigned(g.split);
+    const int rank = int(blockIdx.x % unsigned(g.split));
+    const int4 head = *reinterpret_cast<const int4 *>(g.plan), at = *reinterpret_cast<const int4 *>(g.plan + plan_tiles_at() + 4 * tile);
+    if (head.y != g.tokens || head.z != g.adapters || tile >= head.x) return;  // the whole cluster
+    const int count = at.z;
+    if (t < count) rows[t] = g.plan[plan_order_at(g.tokens, g.adapters) + at.y + t];
+    __syncthreads();
+    [[maybe_unused]] const dbg::Side sx = dbg::side(g.x, 1, g.tokens, g.k, g.ld_x, 0, 2);
+    [[maybe_unused]] const dbg::Side sa = dbg::side(g.a, g.adapters, g.rank, g.k, g.ld_a, g.stride_a, 2);
+    [[maybe_unused]] const dbg::Side sv = dbg::side(g.b, g.adapters, g.n, g.rank, g.ld_b, g.stride_b, 2);
+    [[maybe_unused]] const dbg::Side sb = dbg::side(g.base, 1, g.tokens, g.n, g.ld_base, 0, sizeof(T));
+    [[maybe_unused]] const dbg::Side so = dbg::side(g.out, 1, g.tokens, g.n, g.ld_out, 0, sizeof(T));
+    const int units = (g.n + 31) / 32, first = int(int64_t(units) * rank / g.split), last = int(int64_t(units) * (rank + 1) / g.split);
+    const bool bare = at.x >= g.adapters || g.k == 0;
+    if (bare && g.base == g.out) return;
+    const int runs = (g.k + 31) / 32;  // of 32 values of k
+    const int run0 = int(int64_t(runs) * rank / g.split), run1 = int(int64_t(runs) * (rank + 1) / g.split);
+    const __nv_bfloat16 *a = g.a + at.x * g.stride_a, *b = g.b + at.x * g.stride_b;
+    const float scale = bare ? 0.0f : g.scale ? g.scale[at.x] : 1.0f;
+    // What b's loads will find in L2 when the inner values are there.
+    if (!bare) {
+        constexpr int ROWS = 64 / RP ? 64 / RP : 1;  // of b to 128 bytes, about
+        for (int col = first * 32 + t * ROWS; col < last * 32 && col < g.n; col += kFewThreads * ROWS)
+            for (int r = 0; r < g.rank; r += 64) ptx::prefetch_l2(b + col * g.ld_b + r);
+    }
+
+    for (int m0 = 0; m0 < count; m0 += 16) {
+        // The two tokens of this lane's rows of a fragment.
+        const bool has[2] = {m0 + gid < count, m0 + gid + 8 < count};
+        const int64_t token[2] = {has[0] ? rows[m0 + gid] : 0, has[1] ? rows[m0 + gid + 8] : 0};
+        if (!bare) {
+            float acc[RW / 8][4] = {};
+            const __nv_bfloat16 *x0 = g.x + token[0] * g.ld_x, *x1 = g.x + token[1] * g.ld_x;
+            const int r0 = warp % SHARES * RW, depth = warp / SHARES;
+            auto add = [&](int run, auto whole) {
+                constexpr bool W = decltype(whole)::value;
+                const int c = run * 32 + tid * 8;
+                const uint4 u = values<8, W>(x0, c, g.k, has[0], sx), v = values<8, W>(x1, c, g.k, has[1], sx);
+                uint4 w[RW / 8];
+#pragma unroll
+                for (int j = 0; j < RW / 8; ++j) {
+                    const int r = r0 + j * 8 + gid;
+                    w[j] = values<8, W>(a + r * g.ld_a, c, g.k, r < g.rank, sa);
+                }
+#pragma unroll
+                for (int j = 0; j < RW / 8; ++j) {
+                    mma_16x8(acc[j], u.x, v.x, u.y, v.y, w[j].x, w[j].y);
+                    mma_16x8(acc[j], u.z, v.z, u.w, v.w, w[j].z, w[j].w);
+                }
+            };
+            const bool ragged = g.k % 8 != 0 && run1 == runs;  // the last run is of pieces
+            constexpr int EACH = kFewWarps / SHARES;           // warps along k
+            int run = run0 + depth;
+            const int end = ragged ? run1 - 1 : run1;
+            for (; run + 3 * EACH < end; run += 4 * EACH) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) add(run + q * EACH, std::true_type());
+            }
+            for (; run < end; run += EACH) add(run, std::true_type());
+            if (run < run1) add(run, std::false_type());
+#pragma unroll
+            for (int j = 0; j < RW / 8; ++j) {
+                float *p = part + (depth * 16 + gid) * RP + r0 + j * 8 + tid * 2;
+                *reinterpret_cast<float2 *>(p) = make_float2(acc[j][0], acc[j][1]);
+                *reinterpret_cast<float2 *>(p + 8 * RP) = make_float2(acc[j][2], acc[j][3]);
+            }
+        }
+        // Unit u: b's rows of its 32 columns and the lane's 8 columns of base.
+        struct Unit {
+            uint4 b[STEPS][4];
+            Pack<T, 16 / int(sizeof(T))> base[2][sizeof(T) / 2];
+        };
+        constexpr int V = 16 / int(sizeof(T));
+        const bool pieces = g.rank % RC != 0;
+        auto read = [&](Unit &m, int u) {
+            const bool here = u < last;
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int col = u * 32 + 8 * (gid >> 1) + 2 * j + (gid & 1);
+                    const bool have = here && !bare && col < g.n;
+                    m.b[s][j] = pieces ? values<RC, false>(b + col * g.ld_b, s * 4 * RC + tid * RC, g.rank, have, sv)
+                                       : values<RC, true>(b + col * g.ld_b, s * 4 * RC + tid * RC, g.rank, have, sv);
+                }
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int h = 0; h < int(sizeof(T)) / 2; ++h) {
+                    m.base[r][h].clear();
+                    const int col = u * 32 + 8 * tid + h * V;
+                    const T *p = static_cast<const T *>(g.base) + token[r] * g.ld_base + col;
+                    if (!g.base || !here || !has[r]) continue;
+                    if constexpr (EDGE) {
+#pragma unroll
+                        for (int q = 0; q < V; ++q)
+                            if (col + q < g.n && TR_LOAD_OK(sb, p + q, int(sizeof(T)))) m.base[r][h].set(q, p[q]);
+                    } else {
+                        if (col < g.n && TR_LOAD_OK(sb, p, 16)) m.base[r][h] = *reinterpret_cast<const Pack<T, V> *>(p);
+                    }
+                }
+        };
+        Unit unit[AHEAD];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) read(unit[i], first + warp + i * kFewWarps);
+        if (!bare) {
+            // The warps' parts, then the CTAs', both in order.
+            __syncthreads();
+            for (int i = t; i < 16 * RP; i += kFewThreads) {
+                float v = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kFewWarps / SHARES; ++w) v += part[w * 16 * RP + i];
+                sums[i / RP][i % RP] = v;
+            }
+            if (g.split > 1) ptx::cluster_sync();
+            else __syncthreads();
+            for (int i = t; i < 16 * RP; i += kFewThreads) {
+                const int m = i / RP, r = i % RP;
+                float v = 0.0f, f[8];
+#pragma unroll
+                for (int peer = 0; peer < 8; ++peer)
+                    if (peer < g.split) f[peer] = ptx::load_cluster(ptx::peer_addr(&sums[m][r], uint32_t(peer)));
+#pragma unroll
+                for (int peer = 0; peer < 8; ++peer)
+                    if (peer < g.split) v += f[peer];
+                v = r < g.rank ? v * scale : 0.0f;
+#pragma unroll
+                for (int term = 0; term < TERMS; ++term) {  // as above
+                    const __nv_bfloat16 h = __float2bfloat16_rn(v);
+                    v = fabsf(__bfloat162float(h)) == INFINITY ? 0.0f : v - __bfloat162float(h);
+                    terms[term][m][r] = h;
+                }
+            }
+            __syncthreads();
+            if (g.split > 1) ptx::cluster_arrive();
+        }
+        auto finish = [&](const Unit &m, int u) {
+            float d[4][4] = {};
+            if (!bare)
+#pragma unroll
+                for (int term = 0; term < TERMS; ++term)
+#pragma unroll
+                    for (int s = 0; s < STEPS; ++s) {
+                        const __nv_bfloat16 *p = &terms[term][gid][s * 4 * RC + tid * RC], *q = p + 8 * PITCH;
+                        if constexpr (RC == 4) {
+                            const uint2 v0 = *reinterpret_cast<const uint2 *>(p), v1 = *reinterpret_cast<const uint2 *>(q);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) mma_16x8(d[j], v0.x, v1.x, v0.y, v1.y, m.b[s][j].x, m.b[s][j].y);
+                        } else {
+                            const uint4 v0 = *reinterpret_cast<const uint4 *>(p), v1 = *reinterpret_cast<const uint4 *>(q);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                mma_16x8(d[j], v0.x, v1.x, v0.y, v1.y, m.b[s][j].x, m.b[s][j].y);
+                                mma_16x8(d[j], v0.z, v1.z, v0.w, v1.w, m.b[s][j].z, m.b[s][j].w);
+                            }
+                        }
+                    }
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int h = 0; h < int(sizeof(T)) / 2; ++h) {
+                    const int col = u * 32 + 8 * tid + h * V;
+                    if (!has[r] || col >= g.n) continue;
+                    float f[V];
+#pragma unroll
+                    for (int q = 0; q < V; ++q) f[q] = d[(h * V + q) / 2][2 * r + q % 2] + m.base[r][h].get(q);
+                    Pack<T, V> o;
+                    o.round(f);
+                    T *p = static_cast<T *>(g.out) + token[r] * g.ld_out + col;
+                    if constexpr (EDGE) {
+#pragma unroll
+                        for (int q = 0; q < V; ++q)
+                            if (col + q < g.n && TR_STORE_OK(so, p + q, int(sizeof(T)))) p[q] = pack_elem(o, q);
+                    } else {
+                        if (TR_STORE_OK(so, p, 16)) *reinterpret_cast<Pack<T, V> *>(p) = o;
+                    }
+                }
+        };
+        for (int u = first + warp; u < last; u += AHEAD * kFewWarps)
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                if (u + i * kFewWarps >= last) continue;
+                finish(unit[i], u + i * kFewWarps);
+                read(unit[i], u + (i + AHEAD) * kFewWarps);
+            }
+        __syncwarp();
+        if (!bare && g.split > 1) ptx::cluster_wait();  // nobody writes its sums anew, or leaves, before all have read them
+    }
+}
+
 // Planes of rows x cols values of 2 or 4 bytes, or a matrix (planes 0): boxes of 128 bytes x box_rows.
 bool encode(CUtensorMap *map, const void *base, int es, int64_t planes, int64_t rows, int64_t cols, int64_t ld, int64_t stride,
             int box_rows) {
@@ -626,6 +887,47 @@ bool encode(CUtensorMap *map, const void *base, int es, int64_t planes, int64_t 
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A launch in clusters that may start while the kernel before it drains.
+template <typename... K, typename... A>
+cudaError_t launch_clusters(void (*kern)(K...), int64_t grid, int threads, size_t smem, int cluster, cudaStream_t stream, A &&...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(grid));
+    cfg.blockDim = dim3(unsigned(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = unsigned(cluster);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, std::forward<A>(args)...);
+    if (e != cudaSuccess) (void)cudaGetLastError();
+    return e;
+}
+
+template <int RP, typename T, bool EDGE>
+cudaError_t launch_few(Few g, int64_t tiles, cudaStream_t stream) {
+    auto kern = k_adapters_few<RP, T, EDGE>;
+    constexpr size_t smem = size_t(kFewWarps / few_shares(RP)) * 16 * RP * 4;
+    // Eight CTAs to a tile, fewer where as many tiles as there can be would not be resident at one time, or a warp
+    // would have less than a run of k and a unit of columns.
+    const int64_t resident = 2 * int64_t(sm_count());
+    g.split = 8;
+    while (g.split > 1 && (tiles * g.split > resident || ((g.k + 31) / 32 < g.split * kFewWarps && (g.n + 31) / 32 < g.split * kFewWarps)))
+        g.split /= 2;
+    return launch_clusters(kern, tiles * g.split, kFewThreads, smem, g.split, stream, g);
+}
+
+template <int RP>
+cudaError_t launch_few_rank(const Few &g, bool f32, bool edge, int64_t tiles, cudaStream_t stream) {
+    if (f32) return edge ? launch_few<RP, float, true>(g, tiles, stream) : launch_few<RP, float, false>(g, tiles, stream);
+    return edge ? launch_few<RP, __nv_bfloat16, true>(g, tiles, stream) : launch_few<RP, __nv_bfloat16, false>(g, tiles, stream);
+}
+
 template <int RP, typename T, bool EDGE>
 cudaError_t launch_one(const CUtensorMap (&maps)[6], Adapt g, int64_t tiles, cudaStream_t stream) {
     using S = Shape<RP, sizeof(T) == 2 ? 2 : 3>;
@@ -633,27 +935,12 @@ cudaError_t launch_one(const CUtensorMap (&maps)[6], Adapt g, int64_t tiles, cud
     // Always the same value: setting it again is harmless.
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(S::kSmem));
     if (e != cudaSuccess) return e;
-    // CTAs to a tile until the tiles fill what is resident at one time, each keeping two chunks of k or more.
-    const int64_t resident = sm_count();
+    // CTAs to a tile until the fewest tiles that these tokens can make fill what is resident at one time (how many there
+    // are is known on the device alone), each keeping two chunks of k or more.
+    const int64_t resident = sm_count(), least = (g.tokens + kPlanTile - 1) / kPlanTile;
     g.split = 1;
-    while (g.split < 8 && tiles * g.split * 2 <= resident && g.chunks >= g.split * 4) g.split *= 2;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(tiles * g.split));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = S::kSmem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = unsigned(g.split);
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, kern, maps[0], maps[1], maps[2], maps[3], maps[4], maps[5], g);
-    if (e != cudaSuccess) (void)cudaGetLastError();
-    return e;
+    while (g.split < 8 && least * g.split * 2 <= resident && g.chunks >= g.split * 4) g.split *= 2;
+    return launch_clusters(kern, tiles * g.split, kThreads, S::kSmem, g.split, stream, maps[0], maps[1], maps[2], maps[3], maps[4], maps[5], g);
 }
 
 template <int RP>
@@ -691,6 +978,17 @@ cudaError_t launch_adapters(const tr_adapters_args &p, const char **why) {
     const Adapt g{p.scale, static_cast<const int32_t *>(p.plan), p.base, p.out, p.tokens, p.adapters,
                   p.n, p.ld_base, p.ld_out, int32_t(p.rank), none ? 0 : int32_t((p.k + 63) / 64), 1};
     const int rp = p.rank <= 16 ? 16 : p.rank <= 32 ? 32 : p.rank <= 64 ? 64 : 128;
+    const int64_t tiles = plan_tiles(p.tokens, p.adapters);
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(p.stream);
+    if (p.tokens <= kFewTokens) {
+        const Few few{static_cast<const __nv_bfloat16 *>(p.x), static_cast<const __nv_bfloat16 *>(p.a), static_cast<const __nv_bfloat16 *>(p.b),
+                      p.scale, g.plan, p.base, p.out, p.tokens, p.adapters, p.ld_x, p.ld_a, p.stride_a, p.ld_b, p.stride_b, p.ld_base, p.ld_out,
+                      int32_t(p.rank), int32_t(none ? 0 : p.k), int32_t(p.n), 1};
+        if (rp == 16) return launch_few_rank<16>(few, f32, edge, tiles, stream);
+        if (rp == 32) return launch_few_rank<32>(few, f32, edge, tiles, stream);
+        if (rp == 64) return launch_few_rank<64>(few, f32, edge, tiles, stream);
+        return launch_few_rank<128>(few, f32, edge, tiles, stream);
+    }
     CUtensorMap maps[6] = {};
     if (!none && (!encode(maps, p.x, 2, 0, p.tokens, p.k, p.ld_x, 0, 128) || !encode(maps + 1, p.x, 2, 0, p.tokens, p.k, p.ld_x, 0, 1) ||
                   !encode(maps + 2, p.a, 2, p.adapters, p.rank, p.k, p.ld_a, p.stride_a, rp) ||
@@ -700,8 +998,6 @@ cudaError_t launch_adapters(const tr_adapters_args &p, const char **why) {
         *why = "adapters: cuTensorMapEncodeTiled rejected the operands (a pitch of 2^40 bytes or more)";
         return cudaErrorInvalidValue;
     }
-    const int64_t tiles = plan_tiles(p.tokens, p.adapters);
-    cudaStream_t stream = reinterpret_cast<cudaStream_t>(p.stream);
     if (rp == 16) return launch_rank<16>(maps, g, f32, edge, tiles, stream);
     if (rp == 32) return launch_rank<32>(maps, g, f32, edge, tiles, stream);
     if (rp == 64) return launch_rank<64>(maps, g, f32, edge, tiles, stream);

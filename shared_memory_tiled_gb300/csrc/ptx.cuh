@@ -161,6 +161,11 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
         : "memory");
 }
 
+// The 128 bytes around p into L2.
+__device__ __forceinline__ void prefetch_l2(const void *p) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory");
+}
+
 // 16 bytes of shared memory, kept in program order.
 __device__ __forceinline__ uint4 load_shared_16(uint32_t addr) {
     uint4 v;
