@@ -6,13 +6,10 @@
 
 namespace tr {
 
-constexpr int kPlanTile = 128;              // tokens of one adapter that are worked on together
-constexpr int64_t kPlanHead = 4;            // tiles, tokens, adapters, 0
+constexpr int kPlanTile = 128;              // tokens of one adapter that are worked on together, at the most
+constexpr int kPlanFew = 16;                // tokens of a small tile, at the most
+constexpr int64_t kPlanHead = 4;            // large tiles, tokens, adapters, small tiles
 constexpr int64_t kMostAdapters = 32767;    // a warp's counts of them fit shared memory
-
-struct PlanTile {
-    int32_t group, first, count, zero;      // adapter (adapters: none), place in the order, tokens
-};
 
 // Tiles of `tokens` tokens at the most: every adapter, and those without one, may end
 // inside a tile.
@@ -21,7 +18,14 @@ __host__ __device__ inline int64_t plan_tiles(int64_t tokens, int64_t adapters) 
     return (tokens - groups) / kPlanTile + groups;
 }
 
-// Places, in words, of the tiles and of the order of the tokens.
+// Of those with more than kPlanFew tokens.
+__host__ __device__ inline int64_t plan_large_tiles(int64_t tokens, int64_t adapters) {
+    const int64_t most = tokens / (kPlanFew + 1), tiles = plan_tiles(tokens, adapters);
+    return most < tiles ? most : tiles;
+}
+
+// Places, in words, of the tiles -- {adapter (adapters: none), place in the order, tokens, 0} each, the large ones from
+// the front, the small ones from the back -- and of the order of the tokens.
 __host__ __device__ inline int64_t plan_tiles_at() { return kPlanHead; }
 __host__ __device__ inline int64_t plan_order_at(int64_t tokens, int64_t adapters) {
     return kPlanHead + 4 * plan_tiles(tokens, adapters);

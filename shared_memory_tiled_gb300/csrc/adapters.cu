@@ -31,12 +31,12 @@ __global__ void __launch_bounds__(kPlanThreads) k_adapter_plan(const int32_t *in
                                                                int adapters, int warps) {
     pdl_prologue();
     extern __shared__ int32_t counts[];  // [warps][adapters + 1]
-    __shared__ int2 joined[32], carry;
+    __shared__ int3 joined[32], carry;  // tokens, large tiles, small tiles
     const int groups = adapters + 1, t = threadIdx.x, lane = t & 31, warp = t >> 5;
     [[maybe_unused]] const dbg::Side si = dbg::side(index, 1, 1, tokens, tokens, 0, 4);
     [[maybe_unused]] const dbg::Side sp = dbg::side(plan, 1, 1, plan_bytes(tokens, adapters) / 4, plan_bytes(tokens, adapters) / 4, 0, 4);
     for (int i = t; i < warps * groups; i += kPlanThreads) counts[i] = 0;
-    if (t == 0) carry = make_int2(0, 0);
+    if (t == 0) carry = make_int3(0, 0, 0);
     __syncthreads();
     const int64_t run = ((int64_t(tokens) + warps - 1) / warps + 31) / 32 * 32;
     const int64_t first = warp * run, last = first + run < tokens ? first + run : tokens;
@@ -62,43 +62,42 @@ __global__ void __launch_bounds__(kPlanThreads) k_adapter_plan(const int32_t *in
     };
     walk([](int64_t, int, int) {});
     __syncthreads();
-    // Tokens before each adapter (x) and tiles before it (y), 1024 adapters at a time.
+    // Tokens before each adapter, large tiles before it and small ones, 1024 adapters at a time.
+    auto up = [&](int3 v) {  // sums over the lanes up to this one
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, v.x, o), y = __shfl_up_sync(0xffffffffu, v.y, o), z = __shfl_up_sync(0xffffffffu, v.z, o);
+            if (lane >= o) v = make_int3(v.x + x, v.y + y, v.z + z);
+        }
+        return v;
+    };
+    const int64_t most = plan_tiles(tokens, adapters);
     for (int g0 = 0; g0 < groups; g0 += kPlanThreads) {
         const int g = g0 + t;
         int n = 0;
         if (g < groups)
             for (int w = 0; w < warps; ++w) n += counts[w * groups + g];
-        const int2 own = make_int2(n, (n + kPlanTile - 1) / kPlanTile);
-        int2 s = own;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int x = __shfl_up_sync(0xffffffffu, s.x, o), y = __shfl_up_sync(0xffffffffu, s.y, o);
-            if (lane >= o) s = make_int2(s.x + x, s.y + y);
-        }
+        const int rest = n % kPlanTile;
+        const int3 own = make_int3(n, n / kPlanTile + (rest > kPlanFew), rest > 0 && rest <= kPlanFew);
+        const int3 s = up(own);
         if (lane == 31) joined[warp] = s;
         __syncthreads();
         if (warp == 0) {
-            int2 j = joined[lane];
-            const int2 was = j;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int x = __shfl_up_sync(0xffffffffu, j.x, o), y = __shfl_up_sync(0xffffffffu, j.y, o);
-                if (lane >= o) j = make_int2(j.x + x, j.y + y);
-            }
-            joined[lane] = make_int2(carry.x + j.x - was.x, carry.y + j.y - was.y);
+            const int3 was = joined[lane], j = up(was);
+            joined[lane] = make_int3(carry.x + j.x - was.x, carry.y + j.y - was.y, carry.z + j.z - was.z);
             __syncwarp();
-            if (lane == 31) carry = make_int2(carry.x + j.x, carry.y + j.y);
+            if (lane == 31) carry = make_int3(carry.x + j.x, carry.y + j.y, carry.z + j.z);
         }
         __syncthreads();
         if (g < groups) {
             int at = joined[warp].x + s.x - own.x;
-            const int tile = joined[warp].y + s.y - own.y;
-            for (int k = 0; k < own.y; ++k) {
-                const int left = n - k * kPlanTile;
-                int32_t *p = plan + plan_tiles_at() + 4 * int64_t(tile + k);
-                if (TR_STORE_OK(sp, p, 16))
-                    *reinterpret_cast<int4 *>(p) = make_int4(g, at + k * kPlanTile, left < kPlanTile ? left : kPlanTile, 0);
-            }
+            const int64_t large = joined[warp].y + s.y - own.y, small = joined[warp].z + s.z - own.z;
+            auto tile = [&](int64_t place, int from, int count) {
+                int32_t *p = plan + plan_tiles_at() + 4 * place;
+                if (TR_STORE_OK(sp, p, 16)) *reinterpret_cast<int4 *>(p) = make_int4(g, from, count, 0);
+            };
+            for (int k = 0; k < own.y; ++k) tile(large + k, at + k * kPlanTile, n - k * kPlanTile < kPlanTile ? n - k * kPlanTile : kPlanTile);
+            if (own.z) tile(most - 1 - small, at + n - rest, rest);
             for (int w = 0; w < warps; ++w) {
                 const int c = counts[w * groups + g];
                 counts[w * groups + g] = at;
@@ -112,10 +111,22 @@ __global__ void __launch_bounds__(kPlanThreads) k_adapter_plan(const int32_t *in
         int32_t *p = order + mine[g] + before;
         if (TR_STORE_OK(sp, p, 4)) *p = int32_t(i);
     });
-    if (t == 0 && TR_STORE_OK(sp, plan, 16)) *reinterpret_cast<int4 *>(plan) = make_int4(carry.y, tokens, adapters, 0);
+    if (t == 0 && TR_STORE_OK(sp, plan, 16)) *reinterpret_cast<int4 *>(plan) = make_int4(carry.y, tokens, adapters, carry.z);
 }
 
 // --- the adapters ---------------------------------------------------------------------------
+
+// Tile k of a plan, of the large ones, the small ones or all; false where there is none.
+enum Which { kAll, kLarge, kSmall };
+__device__ __forceinline__ bool plan_tile(const int32_t *plan, int64_t tokens, int64_t adapters, int which, int64_t k, int4 *tile) {
+    const int4 head = *reinterpret_cast<const int4 *>(plan);
+    if (head.y != tokens || head.z != adapters) return false;  // not these tokens' plan
+    const int64_t large = which == kSmall ? 0 : head.x, small = which == kLarge ? 0 : head.w;
+    if (k >= large + small) return false;
+    const int64_t place = k < large ? k : plan_tiles(tokens, adapters) - 1 - (k - large);
+    *tile = *reinterpret_cast<const int4 *>(plan + plan_tiles_at() + 4 * place);
+    return true;
+}
 
 struct Adapt {
     const float *scale;
@@ -126,6 +137,8 @@ struct Adapt {
     int64_t ld_base, ld_out;
     int32_t rank, chunks;  // chunks of 64 of the contraction over k
     int32_t split;         // CTAs that share a tile
+    int32_t which;         // tiles (Which)
+    int32_t beside;        // the small ones are another kernel's, just before this one
 };
 
 constexpr int kGroups = 3;              // of four warps that take sums out of tensor memory, each with its own
@@ -259,13 +272,15 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
     if (g.split > 1) ptx::cluster_sync();  // the others' barriers are ready
     ptx::tc_fence_after();
     const uint32_t tmem = tmem_base;
-    pdl_prologue();  // after the tensor memory is taken, as in the product
+    // After the tensor memory is taken, as in the product.  The kernel beside this one lets it start when it has waited
+    // for what was before it, and writes other rows: that one is waited for at the end.
+    ptx::launch_dependents();
+    if (!g.beside) ptx::wait_dependencies();
 
     const int64_t tile = blockIdx.x / unsigned(g.split);
     const int rank = int(blockIdx.x % unsigned(g.split));
-    const bool mine = g.plan[1] == g.tokens && g.plan[2] == g.adapters && tile < g.plan[0];
     int4 at = make_int4(0, 0, 0, 0);
-    if (mine) at = *reinterpret_cast<const int4 *>(g.plan + plan_tiles_at() + 4 * tile);
+    const bool mine = plan_tile(g.plan, g.tokens, g.adapters, g.which, tile, &at);
     const int count = at.z;
     const int64_t columns = (g.n + kColumns - 1) / kColumns;  // tiles of them
     const int64_t first_tile = columns * rank / g.split, last_tile = columns * (rank + 1) / g.split;
@@ -613,12 +628,13 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
         ptx::tc_fence_after();
         ptx::tmem_free(tmem, 512);
     }
+    if (g.beside) ptx::wait_dependencies();
 }
 
 // --- a few tokens ---------------------------------------------------------------------------
 //
 // Next tokens of many requests: most adapters have a token or two, and what counts is how soon the adapters' bytes are
-// here.  A cluster to a tile as above, but no tensor memory, tensor maps or rings to set up: each warp reads its
+// here.  Tiles of up to 16 tokens, others 16 at a time.  A cluster to a tile as above, but no tensor memory, tensor maps or rings to set up: each warp reads its
 // part of the adapter straight into the fragments of warp-wide matrix instructions, 16 tokens by 8 ranks (columns).
 // The order of a contraction is free, so a lane's 16 contiguous bytes serve as the fragments of two
 // instructions.  The columns of four instructions are spread so that a lane ends up with 8 neighbouring ones.
@@ -630,10 +646,11 @@ struct Few {
     const void *base;
     void *out;
     int64_t tokens, adapters, ld_x, ld_a, stride_a, ld_b, stride_b, ld_base, ld_out;
-    int32_t rank, k, n, split;
+    int32_t rank, k, n, split, which;
 };
 
-constexpr int64_t kFewTokens = 64;  // up to here these kernels
+// Up to kFewTokens tokens this kernel works alone, up to kBothTokens on the small tiles.
+constexpr int64_t kFewTokens = 32, kBothTokens = 2048;
 constexpr int kFewThreads = 256, kFewWarps = kFewThreads / 32;
 
 // D[16][8] += A[16][16] B[8][16]^T, a fragment's words being pairs along the contraction.
@@ -673,7 +690,8 @@ constexpr int few_shares(int rp) { return rp <= 32 ? 1 : rp / 32; }
 // EDGE: as above.
 template <int RP, typename T, bool EDGE>
 __global__ void __launch_bounds__(kFewThreads, 2) k_adapters_few(const Few g) {
-    pdl_prologue();
+    ptx::wait_dependencies();
+    ptx::launch_dependents();  // in this order: see k_adapters
     constexpr int TERMS = sizeof(T) == 2 ? 2 : 3;
     constexpr int RC = RP == 16 ? 4 : 8, STEPS = RP / (4 * RC);  // values of a row of b to a lane and step
     constexpr int PITCH = RP + 8;                                // of the terms, in values
@@ -686,8 +704,8 @@ __global__ void __launch_bounds__(kFewThreads, 2) k_adapters_few(const Few g) {
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5, gid = lane >> 2, tid = lane & 3;
     const int64_t tile = blockIdx.x / unsigned(g.split);
     const int rank = int(blockIdx.x % unsigned(g.split));
-    const int4 head = *reinterpret_cast<const int4 *>(g.plan), at = *reinterpret_cast<const int4 *>(g.plan + plan_tiles_at() + 4 * tile);
-    if (head.y != g.tokens || head.z != g.adapters || tile >= head.x) return;  // the whole cluster
+    int4 at;
+    if (!plan_tile(g.plan, g.tokens, g.adapters, g.which, tile, &at)) return;  // the whole cluster
     const int count = at.z;
     if (t < count) rows[t] = g.plan[plan_order_at(g.tokens, g.adapters) + at.y + t];
     __syncthreads();
@@ -975,20 +993,27 @@ cudaError_t launch_adapters(const tr_adapters_args &p, const char **why) {
     const int es = f32 ? 4 : 2;
     const bool edge = (p.n * es) % 16 != 0 || !side_aligned16(p.out, p.ld_out, 0, 1, es) || (p.base && !side_aligned16(p.base, p.ld_base, 0, 1, es));
     const bool none = p.adapters == 0 || p.k == 0;  // nothing to add: base alone
-    const Adapt g{p.scale, static_cast<const int32_t *>(p.plan), p.base, p.out, p.tokens, p.adapters,
-                  p.n, p.ld_base, p.ld_out, int32_t(p.rank), none ? 0 : int32_t((p.k + 63) / 64), 1};
+    Adapt g{p.scale, static_cast<const int32_t *>(p.plan), p.base, p.out, p.tokens, p.adapters,
+                  p.n, p.ld_base, p.ld_out, int32_t(p.rank), none ? 0 : int32_t((p.k + 63) / 64), 1, kAll, 0};
     const int rp = p.rank <= 16 ? 16 : p.rank <= 32 ? 32 : p.rank <= 64 ? 64 : 128;
     const int64_t tiles = plan_tiles(p.tokens, p.adapters);
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(p.stream);
-    if (p.tokens <= kFewTokens) {
+    const bool alone = p.tokens <= kFewTokens;
+    if (p.tokens <= kBothTokens) {
         const Few few{static_cast<const __nv_bfloat16 *>(p.x), static_cast<const __nv_bfloat16 *>(p.a), static_cast<const __nv_bfloat16 *>(p.b),
                       p.scale, g.plan, p.base, p.out, p.tokens, p.adapters, p.ld_x, p.ld_a, p.stride_a, p.ld_b, p.stride_b, p.ld_base, p.ld_out,
-                      int32_t(p.rank), int32_t(none ? 0 : p.k), int32_t(p.n), 1};
-        if (rp == 16) return launch_few_rank<16>(few, f32, edge, tiles, stream);
-        if (rp == 32) return launch_few_rank<32>(few, f32, edge, tiles, stream);
-        if (rp == 64) return launch_few_rank<64>(few, f32, edge, tiles, stream);
-        return launch_few_rank<128>(few, f32, edge, tiles, stream);
+                      int32_t(p.rank), int32_t(none ? 0 : p.k), int32_t(p.n), 1, alone ? kAll : kSmall};
+        // Each adapter, and those without one, has one small tile at the most.
+        const int64_t small = alone || tiles < p.adapters + 1 ? tiles : p.adapters + 1;
+        const cudaError_t e = rp == 16   ? launch_few_rank<16>(few, f32, edge, small, stream)
+                              : rp == 32 ? launch_few_rank<32>(few, f32, edge, small, stream)
+                              : rp == 64 ? launch_few_rank<64>(few, f32, edge, small, stream)
+                                         : launch_few_rank<128>(few, f32, edge, small, stream);
+        if (e != cudaSuccess || alone) return e;
+        g.which = kLarge;
+        g.beside = 1;
     }
+    const int64_t large = g.beside ? plan_large_tiles(p.tokens, p.adapters) : tiles;
     CUtensorMap maps[6] = {};
     if (!none && (!encode(maps, p.x, 2, 0, p.tokens, p.k, p.ld_x, 0, 128) || !encode(maps + 1, p.x, 2, 0, p.tokens, p.k, p.ld_x, 0, 1) ||
                   !encode(maps + 2, p.a, 2, p.adapters, p.rank, p.k, p.ld_a, p.stride_a, rp) ||
@@ -998,10 +1023,10 @@ cudaError_t launch_adapters(const tr_adapters_args &p, const char **why) {
         *why = "adapters: cuTensorMapEncodeTiled rejected the operands (a pitch of 2^40 bytes or more)";
         return cudaErrorInvalidValue;
     }
-    if (rp == 16) return launch_rank<16>(maps, g, f32, edge, tiles, stream);
-    if (rp == 32) return launch_rank<32>(maps, g, f32, edge, tiles, stream);
-    if (rp == 64) return launch_rank<64>(maps, g, f32, edge, tiles, stream);
-    return launch_rank<128>(maps, g, f32, edge, tiles, stream);
+    if (rp == 16) return launch_rank<16>(maps, g, f32, edge, large, stream);
+    if (rp == 32) return launch_rank<32>(maps, g, f32, edge, large, stream);
+    if (rp == 64) return launch_rank<64>(maps, g, f32, edge, large, stream);
+    return launch_rank<128>(maps, g, f32, edge, large, stream);
 }
 
 }  // namespace tr

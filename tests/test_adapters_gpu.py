@@ -38,15 +38,19 @@ def test_plan_is_a_stable_sort(tokens, count):
         index[rng.integers(0, tokens, 20)] = [-2 ** 31, 2 ** 31 - 1] * 10
     w = words(B.adapter_plan(torch.from_numpy(index).cuda(), count))
     group = np.where((index < 0) | (index >= count), count, index)
-    tiles, order = w[0], w[-tokens:]
+    large, small, order = w[0], w[3], w[-tokens:]
     assert w[1] == tokens and w[2] == count
     assert np.array_equal(order, np.argsort(group, kind="stable"))
-    want, at = [], 0
+    want, at = [[], []], 0
     for g in range(count + 1):
         n = int((group == g).sum())
-        want += [(g, at + k, min(128, n - k), 0) for k in range(0, n, 128)]
+        for k in range(0, n, 128):
+            want[min(128, n - k) <= 16].append((g, at + k, min(128, n - k), 0))
         at += n
-    assert tiles == len(want) and np.array_equal(w[4:4 + 4 * tiles].reshape(-1, 4), np.array(want))
+    table = w[4:-tokens].reshape(-1, 4)
+    assert large == len(want[0]) and small == len(want[1]) and large + small <= len(table)
+    assert np.array_equal(table[:large], np.array(want[0]).reshape(-1, 4))
+    assert np.array_equal(table[::-1][:small], np.array(want[1]).reshape(-1, 4))
 
 
 def held(values, pitch, shape_off=0):
@@ -84,10 +88,11 @@ def check(p, w, out, got, base="base"):
 
 
 # tokens, adapters, k, n, rank: single tokens, tiles that end anywhere, a contraction and columns of
-# one value, of less than a tile and of more than one CTA's part, ranks from 1 to 128
+# one value, of less than a tile and of more than one CTA's part, ranks from 1 to 128, both sides of each kernel's limit
 CASES = [(1, 1, 8, 8, 8), (1, 3, 1, 1, 1), (2, 1, 64, 128, 16), (5, 4, 100, 77, 5), (17, 3, 1111, 129, 12), (64, 48, 520, 300, 16),
          (128, 1, 512, 256, 32), (129, 2, 513, 257, 64), (300, 5, 1000, 1000, 128), (200, 2, 4096, 96, 100), (77, 9, 64, 2049, 33),
-         (1000, 3, 264, 520, 8), (260, 1, 8192, 24, 127), (400, 30, 136, 4096, 24)]
+         (1000, 3, 264, 520, 8), (260, 1, 8192, 24, 127), (400, 30, 136, 4096, 24), (32, 1, 300, 200, 16), (33, 1, 300, 200, 16), (2048, 90, 72, 136, 16),
+         (2049, 90, 72, 136, 16), (2300, 2, 1032, 264, 64), (20000, 3, 40, 72, 32)]
 
 
 @pytest.mark.parametrize("out", ["bf16", "f32"])
