@@ -544,6 +544,39 @@ def _run(name, args, device):
         check(status)
 
 
+def _packer(layout):
+    """Packs an argument struct of the C entry points in one step: a ctypes structure of as many fields
+    takes four times as long to fill.  ``q`` an address or a size, ``i`` an int32, ``f`` a float."""
+    import struct
+    return struct.Struct("@" + layout).pack
+
+
+_PACK_RMSNORM = _packer("10q4i10qfiq")
+_PACK_RMSNORM_BACKWARD = _packer("9q2i7q")
+_PACK_PLAN = _packer("6q")
+_PACK_ADAPTERS = _packer("8q2i13q")
+_packed: dict = {}  # {entry point: (library, the function taking packed bytes)}
+
+
+def _run_packed(name, pack, device, *values):
+    """``_run`` with the arguments' values in the struct's order, the stream left out."""
+    index = device.index
+    lib = _lib or load()
+    held = _packed.get(name)
+    if held is None or held[0] is not lib:  # a test may put another build of the library in place
+        f = lib[name]
+        f.argtypes, f.restype = [ctypes.c_char_p], ctypes.c_int
+        _packed[name] = held = (lib, f)
+    packed = pack(*values, _torch._C._cuda_getCurrentRawStream(index))
+    if _torch.cuda.current_device() == index:
+        status = held[1](packed)
+    else:
+        with _torch.cuda.device(device):  # the library sets kernels up per current device
+            status = held[1](packed)
+    if status:
+        check(status)
+
+
 def _on(stream, x, call):
     """Makes the call, and so allocates what it returns and works in, on that
     cudaStream_t instead of torch's current stream."""
@@ -721,7 +754,7 @@ def _stream_of(x, residual, residual_out, rows, cols, dev):
     if residual is None:
         if residual_out is not None:
             raise ValueError("residual_out needs a residual: without one the stream is x")
-        return None, 0, x, None, 0
+        return 0, 0, x, 0, 0
     r, c, ld = _matrix(residual, "residual", dev)
     if r != rows or c != cols or residual.dtype != x.dtype:
         raise ValueError("residual must match x in shape and dtype")
@@ -751,9 +784,9 @@ def rmsnorm(x, gamma, residual=None, *, eps=1e-6, out=None, residual_out=None, s
     rstd = torch.empty(rows, dtype=torch.float32, device=dev)
     if not cols:  # the library launches nothing; the mean of no squares is 0 / 0
         rstd.fill_(float("nan"))
-    _run("tr_rmsnorm", RmsnormArgs(
-        x.data_ptr(), res, gamma.data_ptr(), at_h, out.data_ptr(), rstd.data_ptr(), None, None, None, None,
-        xk, wk, 0, 0, rows, cols, ld, ld_r, ld_h, ld_y, 0, 0, 0, 0, eps, 0), dev)
+    _run_packed("tr_rmsnorm", _PACK_RMSNORM, dev,
+                x.data_ptr(), res, gamma.data_ptr(), at_h, out.data_ptr(), rstd.data_ptr(), 0, 0, 0, 0,
+                xk, wk, 0, 0, rows, cols, ld, ld_r, ld_h, ld_y, 0, 0, 0, 0, eps, 0)
     return out, h, rstd
 
 
@@ -777,7 +810,7 @@ def rmsnorm_fp8(x, gamma, residual=None, *, eps=1e-6, dtype=None, transposed=Fal
         dtype = torch.float8_e4m3fn
     xk, wk, qk = _kind(x.dtype, _WIDE, "x"), _kind(gamma.dtype, _WIDE, "gamma"), _kind(dtype, _NARROW, "dtype")
     res, ld_r, h, at_h, ld_h = _stream_of(x, residual, residual_out, rows, cols, dev)
-    y, ld_y = None, 0
+    y, ld_y = 0, 0
     if out is not None:
         out, ld_y = _like(out, x, rows, cols, dev)
         y = out.data_ptr()
@@ -788,16 +821,16 @@ def rmsnorm_fp8(x, gamma, residual=None, *, eps=1e-6, dtype=None, transposed=Fal
     if not cols:
         rstd.fill_(float("nan"))
     if not transposed:
-        _run("tr_rmsnorm", RmsnormArgs(
-            x.data_ptr(), res, gamma.data_ptr(), at_h, y, rstd.data_ptr(), q.data_ptr(), scale.data_ptr(), None, None,
-            xk, wk, qk, 0, rows, cols, ld, ld_r, ld_h, ld_y, ld_q, rows, 0, 0, eps, 0), dev)
+        _run_packed("tr_rmsnorm", _PACK_RMSNORM, dev,
+                    x.data_ptr(), res, gamma.data_ptr(), at_h, y, rstd.data_ptr(), q.data_ptr(), scale.data_ptr(), 0, 0,
+                    xk, wk, qk, 0, rows, cols, ld, ld_r, ld_h, ld_y, ld_q, rows, 0, 0, eps, 0)
         return q, scale, h, rstd
     ld_t = (rows + 15) // 16 * 16
     qt = strided((cols, rows), (ld_t, 1), dtype=dtype, device=dev)
     scale_t = empty(((rows + 127) // 128, cols), dtype=f32, device=dev)
-    _run("tr_rmsnorm", RmsnormArgs(
-        x.data_ptr(), res, gamma.data_ptr(), at_h, y, rstd.data_ptr(), q.data_ptr(), scale.data_ptr(), qt.data_ptr(),
-        scale_t.data_ptr(), xk, wk, qk, 0, rows, cols, ld, ld_r, ld_h, ld_y, ld_q, rows, ld_t, cols, eps, 0), dev)
+    _run_packed("tr_rmsnorm", _PACK_RMSNORM, dev,
+                x.data_ptr(), res, gamma.data_ptr(), at_h, y, rstd.data_ptr(), q.data_ptr(), scale.data_ptr(), qt.data_ptr(),
+                scale_t.data_ptr(), xk, wk, qk, 0, rows, cols, ld, ld_r, ld_h, ld_y, ld_q, rows, ld_t, cols, eps, 0)
     return q, scale, qt, scale_t, h, rstd
 
 
@@ -821,7 +854,7 @@ def rmsnorm_backward(dy, h, gamma, rstd, *, dresidual=None, out=None, stream=Non
     _vector(rstd, "rstd", rows, dev)
     _kind(rstd.dtype, _F32, "rstd")
     xk, wk = _kind(h.dtype, _WIDE, "h"), _kind(gamma.dtype, _WIDE, "gamma")
-    res, ld_r = None, 0
+    res, ld_r = 0, 0
     if dresidual is not None:
         r, c, ld_r = _matrix(dresidual, "dresidual", dev)
         if r != rows or c != cols or dresidual.dtype != h.dtype:
@@ -831,9 +864,9 @@ def rmsnorm_backward(dy, h, gamma, rstd, *, dresidual=None, out=None, stream=Non
     dgamma = torch.empty(cols, dtype=torch.float32, device=dev)
     size = (_lib or load()).tr_rmsnorm_backward_workspace(rows, cols)
     workspace = torch.empty(size, dtype=torch.uint8, device=dev)
-    _run("tr_rmsnorm_backward", RmsnormBackwardArgs(
-        dy.data_ptr(), h.data_ptr(), gamma.data_ptr(), rstd.data_ptr(), res, out.data_ptr(), dgamma.data_ptr(),
-        workspace.data_ptr(), size, xk, wk, rows, cols, ld_dy, ld, ld_r, ld_dx), dev)
+    _run_packed("tr_rmsnorm_backward", _PACK_RMSNORM_BACKWARD, dev,
+                dy.data_ptr(), h.data_ptr(), gamma.data_ptr(), rstd.data_ptr(), res, out.data_ptr(), dgamma.data_ptr(),
+                workspace.data_ptr(), size, xk, wk, rows, cols, ld_dy, ld, ld_r, ld_dx)
     return out, dgamma
 
 
@@ -865,7 +898,7 @@ def adapter_plan(index, adapters, *, stream=None):
     if size < 0:
         raise ValueError(f"{adapters} adapters: expected 0 to 32767")
     words = torch.empty(size, dtype=torch.uint8, device=dev)
-    _run("tr_adapter_plan", AdapterPlanArgs(index.data_ptr(), words.data_ptr(), size, tokens, adapters), dev)
+    _run_packed("tr_adapter_plan", _PACK_PLAN, dev, index.data_ptr(), words.data_ptr(), size, tokens, adapters)
     return AdapterPlan(words, tokens, adapters)
 
 
@@ -913,12 +946,12 @@ def adapters(x, a, b, plan, *, scale=None, base=None, out=None, out_dtype=None, 
         raise ValueError(f"a plan of {plan.tokens} tokens and {plan.adapters} adapters, expected {tokens} and {count}")
     if tokens <= 1:
         ld_x = (k + 7) // 8 * 8
-    at_scale = None
+    at_scale = 0
     if scale is not None:
         _vector(scale, "scale", count, dev)
         _kind(scale.dtype, _F32, "scale")
         at_scale = scale.data_ptr()
-    at_base, ld_base = None, 0
+    at_base, ld_base = 0, 0
     if base is not None:
         bt, bn, ld_base = _matrix(base, "base", dev)
         if bt != tokens or bn != n:
@@ -936,8 +969,8 @@ def adapters(x, a, b, plan, *, scale=None, base=None, out=None, out_dtype=None, 
             raise ValueError(f"out has shape {(ot, on)}, expected {(tokens, n)}")
     if base is not None and base.dtype != out.dtype:
         raise TypeError("base and out must have the same dtype")
-    _run("tr_adapters", AdaptersArgs(
-        x.data_ptr(), a.data_ptr(), b.data_ptr(), at_scale, words.data_ptr(), at_base, out.data_ptr(),
-        words.numel(), _kind(out.dtype, _WIDE, "out"), 0, tokens, count, k, n, rank, ld_x, ld_a, stride_a, ld_b,
-        stride_b, ld_base, ld_out), dev)
+    _run_packed("tr_adapters", _PACK_ADAPTERS, dev,
+                x.data_ptr(), a.data_ptr(), b.data_ptr(), at_scale, words.data_ptr(), at_base, out.data_ptr(),
+                words.numel(), _kind(out.dtype, _WIDE, "out"), 0, tokens, count, k, n, rank, ld_x, ld_a, stride_a, ld_b,
+                stride_b, ld_base, ld_out)
     return out

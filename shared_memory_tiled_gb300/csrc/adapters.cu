@@ -950,8 +950,7 @@ template <int RP, typename T, bool EDGE>
 cudaError_t launch_one(const CUtensorMap (&maps)[6], Adapt g, int64_t tiles, cudaStream_t stream) {
     using S = Shape<RP, sizeof(T) == 2 ? 2 : 3>;
     auto kern = k_adapters<RP, T, EDGE>;
-    // Always the same value: setting it again is harmless.
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(S::kSmem));
+    const cudaError_t e = allow_shared<k_adapters<RP, T, EDGE>>(S::kSmem);
     if (e != cudaSuccess) return e;
     // CTAs to a tile until the fewest tiles that these tokens can make fill what is resident at one time (how many there
     // are is known on the device alone), each keeping two chunks of k or more.
@@ -981,8 +980,7 @@ cudaError_t launch_adapter_plan(const tr_adapter_plan_args &p) {
     const int64_t room = 200 * 1024 / (4 * groups);
     if (warps > room) warps = room;
     if (warps > kPlanThreads / 32) warps = kPlanThreads / 32;
-    // Always the most that any call needs: threads with other sizes set it too.
-    const cudaError_t e = cudaFuncSetAttribute(k_adapter_plan, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+    const cudaError_t e = allow_shared<k_adapter_plan>(200 * 1024);  // the most that any call needs
     if (e != cudaSuccess) return e;
     return launch_pdl(k_adapter_plan, dim3(1), dim3(kPlanThreads), size_t(warps * groups * 4), reinterpret_cast<cudaStream_t>(p.stream),
                       p.index, static_cast<int32_t *>(p.plan), int(p.tokens), int(p.adapters), int(warps));

@@ -17,9 +17,25 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <utility>
 
 namespace tr {
+
+// Allows the kernel K this much shared memory, once per device.  (Internal linkage: the static of an inline
+// function would be exported.)
+template <auto K>
+static cudaError_t allow_shared(size_t bytes) {
+    static std::atomic<bool> allowed[64];  // zero-initialised
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (allowed[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    e = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));  // doing it twice is harmless
+    if (e == cudaSuccess) allowed[dev].store(true, std::memory_order_release);
+    return e;
+}
 
 // First statement of every kernel launched through launch_pdl.
 __device__ __forceinline__ void pdl_prologue() {

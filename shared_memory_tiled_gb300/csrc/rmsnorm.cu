@@ -477,14 +477,11 @@ cudaError_t launch_ring(const Rms &a, bool vec, cudaStream_t stream) {
     if (fit < 2) return cudaErrorNotSupported;
     const int stages = int(fit < kMaxStages ? fit : kMaxStages);
     const int64_t resident = int64_t(sm_count()) * per_sm;
-    auto run = [&](auto kern) {
-        // Always the most that any call needs: threads with rows of other lengths set it too.
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(ring_room(1)));
-        if (e != cudaSuccess) return e;
-        return launch_pdl(kern, dim3(unsigned(a.rows < resident ? a.rows : resident)), dim3(unsigned(threads)), size_t(stages) * stage_bytes,
-                          stream, a, stages, row_bytes);
-    };
-    return vec ? run(k_rmsnorm_ring<T, true>) : run(k_rmsnorm_ring<T, false>);
+    // Always the most that any call needs.
+    const cudaError_t e = vec ? allow_shared<k_rmsnorm_ring<T, true>>(ring_room(1)) : allow_shared<k_rmsnorm_ring<T, false>>(ring_room(1));
+    if (e != cudaSuccess) return e;
+    return launch_pdl(vec ? k_rmsnorm_ring<T, true> : k_rmsnorm_ring<T, false>, dim3(unsigned(a.rows < resident ? a.rows : resident)),
+                      dim3(unsigned(threads)), size_t(stages) * stage_bytes, stream, a, stages, row_bytes);
 }
 
 template <typename T>

@@ -379,15 +379,14 @@ cudaError_t launch_ring(RmsBwd a, bool vec, cudaStream_t stream) {
     a.parts = int64_t(sm_count()) * per_sm;
     if (a.parts > most_parts(a.rows, a.cols)) a.parts = most_parts(a.rows, a.cols);
     const size_t smem = size_t(stages) * stage_bytes + weights;
-    auto run = [&](auto kern) {
-        // Always the most that any call needs: threads with rows of other lengths set it too.
-        const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(ring_room(1)));
-        if (err != cudaSuccess) return err;
+    auto run = [&](auto allowed, auto kern) {
+        if (allowed != cudaSuccess) return allowed;
         return launch_pdl(kern, dim3(unsigned(a.parts)), dim3(unsigned(threads)), smem, stream, a, int(stages), row_bytes);
     };
-    cudaError_t err;
-    if (keep) err = vec ? run(k_rms_backward<T, true, true>) : run(k_rms_backward<T, true, false>);
-    else err = vec ? run(k_rms_backward<T, false, true>) : run(k_rms_backward<T, false, false>);
+#define TR_RING(KEEP, VEC)  /* always the most shared memory that any call needs */ \
+    run(allow_shared<k_rms_backward<T, KEEP, VEC>>(ring_room(1)), k_rms_backward<T, KEEP, VEC>)
+    const cudaError_t err = keep ? (vec ? TR_RING(true, true) : TR_RING(true, false)) : (vec ? TR_RING(false, true) : TR_RING(false, false));
+#undef TR_RING
     return err == cudaSuccess ? launch_join(a, stream) : err;
 }
 

@@ -2,6 +2,8 @@
 before any CUDA call (no GPU needed; the addresses are never dereferenced)."""
 from __future__ import annotations
 
+import ctypes
+
 import pytest
 
 from shared_memory_tiled_gb300 import binding as B
@@ -123,3 +125,15 @@ def test_adapters_refusals():
                 dict(out=AT[5] + 2, ld_out=300)):
         assert adapters(**bad) == S.ERR_OVERLAP, bad
     assert adapters(tokens=0, x=0, out=0, plan=0) == S.OK and adapters(n=0, b=0, out=0) == S.OK
+
+
+@pytest.mark.parametrize("pack,struct", [(B._PACK_RMSNORM, B.RmsnormArgs), (B._PACK_RMSNORM_BACKWARD, B.RmsnormBackwardArgs),
+                                         (B._PACK_PLAN, B.AdapterPlanArgs), (B._PACK_ADAPTERS, B.AdaptersArgs)])
+def test_packed_arguments_are_the_structs(pack, struct):
+    values = [i + 1.5 if kind is ctypes.c_float else 1 << (20 + i) if ctypes.sizeof(kind) == 8 else i + 1
+              for i, (_, kind) in enumerate(struct._fields_)]
+    packed = pack(*values)
+    assert len(packed) == ctypes.sizeof(struct)
+    held = struct.from_buffer_copy(packed)
+    for (name, _), v in zip(struct._fields_, values):
+        assert getattr(held, name) == v, name
