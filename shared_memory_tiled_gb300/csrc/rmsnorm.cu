@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) k_rmsnorm_held(const Rm
     }
 }
 
-// Many rows: a resident block walks rows; bulk copies keep a ring of its next rows of x and residual in flight,
+// Many rows: a block walks every n-th row; bulk copies keep a ring of its next rows of x and residual in flight,
 // so no register holds loaded data and any alignment reads whole granules.  A thread owns the same 16
 // columns of every row, their weights in registers.  VEC: columns in 16-byte chunks, every row on a
 // 16-byte boundary; else a warp owns blocks of 128 columns and a lane every 32nd of them.
@@ -476,11 +476,17 @@ cudaError_t launch_ring(const Rms &a, bool vec, cudaStream_t stream) {
     const uint32_t fit = ring_room(per_sm) / stage_bytes;
     if (fit < 2) return cudaErrorNotSupported;
     const int stages = int(fit < kMaxStages ? fit : kMaxStages);
-    const int64_t resident = int64_t(sm_count()) * per_sm;
+    // Five rows to a block, or 160 KB of them, whatever is resident: more blocks than that balance, and a block's end
+    // overlaps another's start.  16384 x 8192 bf16 takes 181.6 us with resident blocks that walk all rows, 162.4, 157.5,
+    // 155.8 and 172.0 with 4, 8, 16 and 32 times as many (2 rows each); 12289 x 7919 fp32 261.5, 243.0, 236.3, 232.4 and
+    // 244.0.  Blocks of neighbouring rows are slower than blocks of every n-th one (fp32 238.9, 16 times).
+    const int64_t resident = int64_t(sm_count()) * per_sm, each = 160 * 1024 / stage_bytes > 5 ? 160 * 1024 / stage_bytes : 5;
+    int64_t grid = (a.rows + each - 1) / each;
+    if (grid < resident) grid = a.rows < resident ? a.rows : resident;
     // Always the most that any call needs.
     const cudaError_t e = vec ? allow_shared<k_rmsnorm_ring<T, true>>(ring_room(1)) : allow_shared<k_rmsnorm_ring<T, false>>(ring_room(1));
     if (e != cudaSuccess) return e;
-    return launch_pdl(vec ? k_rmsnorm_ring<T, true> : k_rmsnorm_ring<T, false>, dim3(unsigned(a.rows < resident ? a.rows : resident)),
+    return launch_pdl(vec ? k_rmsnorm_ring<T, true> : k_rmsnorm_ring<T, false>, dim3(unsigned(grid)),
                       dim3(unsigned(threads)), size_t(stages) * stage_bytes, stream, a, stages, row_bytes);
 }
 
