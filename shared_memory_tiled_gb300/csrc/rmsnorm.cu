@@ -3,6 +3,8 @@
 // 8 bits with a scale for each block of 128, by rows and transposed.
 //
 // Bound by memory: x and residual are read once, h, y, q and qt written once.
+#include <type_traits>
+
 #include "fp8.cuh"
 #include "launch.cuh"
 #include "ptx.cuh"
@@ -51,38 +53,84 @@ __device__ __forceinline__ RmsSides sides_of(const Rms &a) {
 
 __device__ __forceinline__ uint32_t bits_of(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
-// Quantizes a chunk of V values of row `row` from column lo (a multiple of V) on, whose block of 128 the
-// 128 / V neighbouring lanes hold; those past the row's end are zero and not stored.
-template <int V>
-__device__ __forceinline__ void quantize_chunk(const Rms &a, int64_t row, int64_t lo, const float (&y)[V], const RmsSides &s) {
-    uint32_t m = kFloorBits;
+// The larger of a and |b|; a NaN wins.
+__device__ __forceinline__ float max_abs(float a, float b) {
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(fabsf(b)));
+    return m;
+}
+constexpr float kFloor = 0x1p-100f;  // kFloorBits
+
+// y = h * rstd * w for N values, two to an instruction.
+template <int N>
+__device__ __forceinline__ void normed(float (&y)[N], const float (&h)[N], float rstd, const float (&w)[N]) {
 #pragma unroll
-    for (int q = 0; q < V; ++q) m = max(m, bits_of(y[q]));
-    if constexpr (V == 4) {
-        m = __reduce_max_sync(0xffffffffu, m);
-    } else {
-#pragma unroll
-        for (int o = 64 / V; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int q = 0; q < N; q += 2) {
+        const float2 v = __fmul2_rn(__fmul2_rn(make_float2(h[q], h[q + 1]), make_float2(rstd, rstd)), make_float2(w[q], w[q + 1]));
+        y[q] = v.x;
+        y[q + 1] = v.y;
     }
-    if (lo >= a.cols) return;
-    const float amax = __uint_as_float(m), inv = a.top / amax;
-    if (lo % 128 == 0) {
-        float *p = a.scale + (lo >> 7) * a.ld_scale + row;
-        if (TR_STORE_OK(s.scale, p, 4)) *p = amax / a.top;
-    }
-    uint8_t *out = a.q + row * a.ld_q;
-    const __nv_fp8_interpretation_t kind = a.e5m2 ? __NV_E5M2 : __NV_E4M3;
-    uint32_t w[V / 4];
+}
+
+// V values times r as V bytes in words.
+template <bool E5M2, int V>
+__device__ __forceinline__ void to_words(uint32_t (&w)[V / 4], const float (&y)[V], float r) {
+    constexpr __nv_fp8_interpretation_t K = E5M2 ? __NV_E5M2 : __NV_E4M3;
 #pragma unroll
     for (int k = 0; k < V / 4; ++k) {
-        const uint32_t b0 = __nv_cvt_float2_to_fp8x2(make_float2(y[4 * k] * inv, y[4 * k + 1] * inv), __NV_SATFINITE, kind);
-        const uint32_t b1 = __nv_cvt_float2_to_fp8x2(make_float2(y[4 * k + 2] * inv, y[4 * k + 3] * inv), __NV_SATFINITE, kind);
-        w[k] = b0 | b1 << 16;
+        const float2 a = __fmul2_rn(make_float2(y[4 * k], y[4 * k + 1]), make_float2(r, r));
+        const float2 b = __fmul2_rn(make_float2(y[4 * k + 2], y[4 * k + 3]), make_float2(r, r));
+        w[k] = uint32_t(__nv_cvt_float2_to_fp8x2(a, __NV_SATFINITE, K)) | uint32_t(__nv_cvt_float2_to_fp8x2(b, __NV_SATFINITE, K)) << 16;
     }
-    if constexpr (V == 8) {
-        store8(out, lo, a.cols, make_uint2(w[0], w[1]), s.q);
-    } else {
-        if (TR_STORE_OK(s.q, out + lo, 4)) *reinterpret_cast<uint32_t *>(out + lo) = w[0];
+}
+
+// Quantizes N chunks of V values of row `row`, the chunk n from column lo[n] (a multiple of V) on, each one's block of
+// 128 held by the 128 / V neighbouring lanes; those past the row's end are zero and not stored.  A warp has N * V / 4
+// blocks: as many lanes find one's T / a and as many its a / T, with one division's instructions for all of them
+// (a division in each lane for each chunk: 163 us against 150 for 16384 x 8192 bf16, rows alone).
+template <int V, int N>
+__device__ __forceinline__ void quantize_chunks(const Rms &a, int64_t row, const int (&lo)[N], const float (&y)[N][V], const RmsSides &s) {
+    constexpr int LANES = 128 / V, BLOCKS = 32 / LANES;  // blocks of a warp to a chunk
+    const int lane = threadIdx.x & 31;
+    float m[N], mine = kFloor;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        m[n] = kFloor;
+#pragma unroll
+        for (int q = 0; q < V; ++q) m[n] = max_abs(m[n], y[n][q]);
+#pragma unroll
+        for (int o = LANES / 2; o; o >>= 1) m[n] = max_abs(m[n], __shfl_xor_sync(0xffffffffu, m[n], o));
+        // Block b of chunk n goes to lane n * BLOCKS + b, and to the one 16 further.
+        const float f = BLOCKS == 1 ? m[n] : __shfl_sync(0xffffffffu, m[n], (lane & (BLOCKS - 1)) * LANES);
+        if ((lane & 15) / BLOCKS == n) mine = f;
+    }
+    const bool inverse = lane < 16;
+    const float ratio = (inverse ? a.top : mine) / (inverse ? mine : a.top);
+    // a / T: lane 16 + n * BLOCKS + b stores block b of chunk n.
+    {
+        const int n = (lane & 15) / BLOCKS, b = lane & (BLOCKS - 1);
+        int col = 0;
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            if (k == n) col = lo[k] - lane * V + b * 128;  // the warp's first column of that chunk, and the block's
+        if (!inverse && n < N && col < a.cols) {
+            float *p = a.scale + int64_t(col >> 7) * a.ld_scale + row;
+            if (TR_STORE_OK(s.scale, p, 4)) *p = ratio;
+        }
+    }
+    uint8_t *out = a.q + row * a.ld_q;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const float inv = __shfl_sync(0xffffffffu, ratio, n * BLOCKS + lane / LANES);
+        uint32_t w[V / 4];
+        if (a.e5m2) to_words<true, V>(w, y[n], inv);
+        else to_words<false, V>(w, y[n], inv);
+        if (lo[n] >= a.cols) continue;
+        if constexpr (V == 8) {
+            if (TR_STORE_OK(s.q, out + lo[n], 8)) *reinterpret_cast<uint2 *>(out + lo[n]) = make_uint2(w[0], w[1]);
+        } else {
+            if (TR_STORE_OK(s.q, out + lo[n], 4)) *reinterpret_cast<uint32_t *>(out + lo[n]) = w[0];
+        }
     }
 }
 
@@ -138,19 +186,22 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) k_rmsnorm_held(const Rm
         group_sum<TPR, 1>(sum, slots[turn]);
         const float rstd = 1.0f / sqrtf(fmaf(sum[0], a.inv_cols, a.eps));
         if (t == 0 && a.rstd && TR_STORE_OK(s.rstd, a.rstd + row, 4)) a.rstd[row] = rstd;
+        float y[NCH][V];
+        int lo[NCH];
 #pragma unroll
         for (int i = 0; i < NCH; ++i) {
-            const int lo = (t + i * TPR) * V;
+            lo[i] = (t + i * TPR) * V;
             float v[V];
 #pragma unroll
-            for (int q = 0; q < V; ++q) v[q] = h[i].get(q) * rstd * w[i][q];
-            if (a.y && lo < cols) {
+            for (int q = 0; q < V; ++q) v[q] = h[i].get(q);
+            normed<V>(y[i], v, rstd, w[i]);
+            if (a.y && lo[i] < cols) {
                 Pack<T, V> o;
-                o.round(v);
-                store_chunk<T, V, false>(static_cast<T *>(a.y) + row * a.ld_y, lo, cols, o, s.y);
+                o.round(y[i]);
+                store_chunk<T, V, false>(static_cast<T *>(a.y) + row * a.ld_y, lo[i], cols, o, s.y);
             }
-            if (a.q) quantize_chunk<V>(a, row, lo, v, s);
         }
+        if (a.q) quantize_chunks<V, NCH>(a, row, lo, y, s);
     }
 }
 
@@ -227,7 +278,8 @@ __global__ void __launch_bounds__(1024, 1) k_rmsnorm_ring(const Rms a, int stage
             }
         }
         T *ho = static_cast<T *>(a.h) + row * a.ld_h;
-        float h[N][V], sum = 0.0f;
+        float h[N][V];
+        float2 sums = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             if constexpr (VEC) {
@@ -261,9 +313,9 @@ __global__ void __launch_bounds__(1024, 1) k_rmsnorm_ring(const Rms a, int stage
                 }
             }
 #pragma unroll
-            for (int q = 0; q < V; ++q) sum = fmaf(h[i][q], h[i][q], sum);
+            for (int q = 0; q < V; q += 2) sums = __ffma2_rn(make_float2(h[i][q], h[i][q + 1]), make_float2(h[i][q], h[i][q + 1]), sums);
         }
-        sum = block_sum(sum, slots[turn]);
+        const float sum = block_sum(sums.x + sums.y, slots[turn]);
         if (t == 0 && ok) {  // past its meeting the block has read this row
             const int64_t next = row + int64_t(stages) * gridDim.x;
             if (next < a.rows) issue(next, stage);
@@ -271,36 +323,46 @@ __global__ void __launch_bounds__(1024, 1) k_rmsnorm_ring(const Rms a, int stage
         const float rstd = 1.0f / sqrtf(fmaf(sum, a.inv_cols, a.eps));
         if (t == 0 && a.rstd && TR_STORE_OK(s.rstd, a.rstd + row, 4)) a.rstd[row] = rstd;
         T *yo = static_cast<T *>(a.y) + row * a.ld_y;
+        float y[N][V];
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
+        for (int i = 0; i < N; ++i) normed<V>(y[i], h[i], rstd, w[i]);
+        if constexpr (VEC) {
+            int lo[N];
 #pragma unroll
-            for (int q = 0; q < V; ++q) h[i][q] = h[i][q] * rstd * w[i][q];
-            if constexpr (VEC) {
-                const int lo = column(i, 0);
-                if (a.y && lo < cols) {
+            for (int i = 0; i < N; ++i) {
+                lo[i] = column(i, 0);
+                if (a.y && lo[i] < cols) {
                     Pack<T, V> o;
-                    o.round(h[i]);
-                    store_chunk<T, V, false>(yo, lo, cols, o, s.y);
+                    o.round(y[i]);
+                    store_chunk<T, V, false>(yo, lo[i], cols, o, s.y);
                 }
-                if (a.q) quantize_chunk<V>(a, row, lo, h[i], s);
-            } else {
-                uint32_t m = kFloorBits;
+            }
+            if (a.q) quantize_chunks<V, N>(a, row, lo, y, s);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                float m = kFloor;
 #pragma unroll
                 for (int q = 0; q < V; ++q) {
                     const int j = column(i, q);
-                    if (a.y && j < cols && TR_STORE_OK(s.y, yo + j, int(sizeof(T)))) put_value(yo + j, h[i][q]);
-                    m = max(m, bits_of(h[i][q]));
+                    if (a.y && j < cols && TR_STORE_OK(s.y, yo + j, int(sizeof(T)))) put_value(yo + j, y[i][q]);
+                    m = max_abs(m, y[i][q]);
                 }
                 if (!a.q || column(i, 0) - lane >= cols) continue;
-                const float amax = __uint_as_float(__reduce_max_sync(0xffffffffu, m)), inv = a.top / amax;
+                // One division for both ratios: lane 0 takes the scale.
+                const float amax = __uint_as_float(__reduce_max_sync(0xffffffffu, bits_of(m)));
+                const float ratio = (lane == 0 ? amax : a.top) / (lane == 0 ? a.top : amax), inv = __shfl_sync(0xffffffffu, ratio, 1);
                 if (lane == 0) {
                     float *p = a.scale + int64_t(column(i, 0) >> 7) * a.ld_scale + row;
-                    if (TR_STORE_OK(s.scale, p, 4)) *p = amax / a.top;
+                    if (TR_STORE_OK(s.scale, p, 4)) *p = ratio;
                 }
+                uint32_t word[1];
+                if (a.e5m2) to_words<true, 4>(word, y[i], inv);
+                else to_words<false, 4>(word, y[i], inv);
 #pragma unroll
                 for (int q = 0; q < V; ++q) {
                     uint8_t *p = a.q + row * a.ld_q + column(i, q);
-                    if (column(i, q) < cols && TR_STORE_OK(s.q, p, 1)) *p = to_byte(h[i][q] * inv, a.e5m2);
+                    if (column(i, q) < cols && TR_STORE_OK(s.q, p, 1)) *p = uint8_t(word[0] >> (8 * q));
                 }
             }
         }
@@ -379,7 +441,7 @@ __global__ void __launch_bounds__(1024) k_rmsnorm_any(const Rms a) {
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) k_rmsnorm_turned(const Rms a) {
     pdl_prologue();
-    __shared__ alignas(16) uint32_t col_max[8][128];
+    __shared__ alignas(16) float col_max[8][128];
     __shared__ alignas(16) float col_inv[128];
     __shared__ uint2 turned[128 * 16];
     const T *src = static_cast<const T *>(a.residual ? a.h : a.x);
@@ -417,26 +479,34 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) k_rmsnorm_turned(
             rstd[i] = r0 + i < a.rows && TR_LOAD_OK(sd, a.rstd + r0 + i, 4) ? a.rstd[r0 + i] : 0.0f;
             w[i] = c0 + i < a.cols ? weight(a.gamma, a.w_bf16, c0 + i, sw) : 0.0f;
         }
-        auto value = [&](int i, int j) { return h[i][j / W].get(j % W) * rstd[i] * w[j]; };
-        uint32_t most[8];
+        // Columns j and j + 1 of row i.
+        auto pair = [&](int i, int j) {
+            return __fmul2_rn(__fmul2_rn(make_float2(h[i][j / W].get(j % W), h[i][j / W].get(j % W + 1)), make_float2(rstd[i], rstd[i])),
+                              make_float2(w[j], w[j + 1]));
+        };
+        float most[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            uint32_t m = kFloorBits;
+        for (int j = 0; j < 8; j += 2) {
+            most[j] = most[j + 1] = kFloor;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) m = max(m, bits_of(value(i, j)));
-            most[j] = max(m, __shfl_xor_sync(0xffffffffu, m, 16));
+            for (int i = 0; i < 8; ++i) {
+                const float2 v = pair(i, j);
+                most[j] = max_abs(most[j], v.x);
+                most[j + 1] = max_abs(most[j + 1], v.y);
+            }
+            most[j] = max_abs(most[j], __shfl_xor_sync(0xffffffffu, most[j], 16));
+            most[j + 1] = max_abs(most[j + 1], __shfl_xor_sync(0xffffffffu, most[j + 1], 16));
         }
         if (lane < 16) {
-            uint4 *p = reinterpret_cast<uint4 *>(&col_max[warp][cg * 8]);
-            p[0] = make_uint4(most[0], most[1], most[2], most[3]);
-            p[1] = make_uint4(most[4], most[5], most[6], most[7]);
+            float4 *p = reinterpret_cast<float4 *>(&col_max[warp][cg * 8]);
+            p[0] = make_float4(most[0], most[1], most[2], most[3]);
+            p[1] = make_float4(most[4], most[5], most[6], most[7]);
         }
         __syncthreads();
         if (t < 128) {
-            uint32_t m = kFloorBits;
+            float amax = kFloor;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) m = max(m, col_max[k][t]);
-            const float amax = __uint_as_float(m);
+            for (int k = 0; k < 8; ++k) amax = max_abs(amax, col_max[k][t]);
             col_inv[t] = a.top / amax;
             if (tc * 128 + t < a.cols) {
                 float *u = a.scale_t + tr * a.ld_scale_t + tc * 128 + t;
@@ -444,14 +514,26 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) k_rmsnorm_turned(
             }
         }
         __syncthreads();
+        auto turn = [&](auto e5m2) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            float col[8];
+            for (int j = 0; j < 8; j += 2) {
+                const float2 inv = *reinterpret_cast<const float2 *>(&col_inv[cg * 8 + j]);
+                float2 v[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) col[i] = value(i, j);
-            const float inv = col_inv[cg * 8 + j];
-            turned[(cg * 8 + j) * 16 + (rg ^ cg)] = a.e5m2 ? to_bytes<true>(col, inv) : to_bytes<false>(col, inv);
-        }
+                for (int i = 0; i < 8; ++i) v[i] = __fmul2_rn(pair(i, j), inv);
+                constexpr __nv_fp8_interpretation_t K = decltype(e5m2)::value ? __NV_E5M2 : __NV_E4M3;
+                uint32_t a[4], b[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    a[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i].x, v[2 * i + 1].x), __NV_SATFINITE, K);
+                    b[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i].y, v[2 * i + 1].y), __NV_SATFINITE, K);
+                }
+                turned[(cg * 8 + j) * 16 + (rg ^ cg)] = make_uint2(a[0] | a[1] << 16, a[2] | a[3] << 16);
+                turned[(cg * 8 + j + 1) * 16 + (rg ^ cg)] = make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
+            }
+        };
+        if (a.e5m2) turn(std::true_type());
+        else turn(std::false_type());
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
