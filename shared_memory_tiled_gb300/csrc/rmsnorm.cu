@@ -59,6 +59,12 @@ __device__ __forceinline__ float max_abs(float a, float b) {
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(fabsf(b)));
     return m;
 }
+// The largest magnitude of three; a NaN wins.
+__device__ __forceinline__ float max_abs(float a, float b, float c) {
+    float m;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+    return m;
+}
 constexpr float kFloor = 0x1p-100f;  // kFloorBits
 
 // y = h * rstd * w for N values, two to an instruction.
@@ -97,7 +103,7 @@ __device__ __forceinline__ void quantize_chunks(const Rms &a, int64_t row, const
     for (int n = 0; n < N; ++n) {
         m[n] = kFloor;
 #pragma unroll
-        for (int q = 0; q < V; ++q) m[n] = max_abs(m[n], y[n][q]);
+        for (int q = 0; q < V; q += 2) m[n] = max_abs(m[n], y[n][q], y[n][q + 1]);
 #pragma unroll
         for (int o = LANES / 2; o; o >>= 1) m[n] = max_abs(m[n], __shfl_xor_sync(0xffffffffu, m[n], o));
         // Block b of chunk n goes to lane n * BLOCKS + b, and to the one 16 further.
@@ -184,7 +190,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) k_rmsnorm_held(const Rm
             for (int q = 0; q < V; ++q) sum[0] = fmaf(h[i].get(q), h[i].get(q), sum[0]);
         }
         group_sum<TPR, 1>(sum, slots[turn]);
-        const float rstd = 1.0f / sqrtf(fmaf(sum[0], a.inv_cols, a.eps));
+        const float rstd = __frsqrt_rn(fmaf(sum[0], a.inv_cols, a.eps));
         if (t == 0 && a.rstd && TR_STORE_OK(s.rstd, a.rstd + row, 4)) a.rstd[row] = rstd;
         float y[NCH][V];
         int lo[NCH];
@@ -227,6 +233,7 @@ __global__ void __launch_bounds__(1024, 1) k_rmsnorm_ring(const Rms a, int stage
     }
     __syncthreads();
     pdl_prologue();
+    const int64_t first = blockIdx.x, step = gridDim.x;
     auto issue = [&](int64_t row, int stage) {  // one thread
         const Granules gx = granules<T>(a.x, a.rows, a.cols, a.ld_x, row);
         const Granules gr = add ? granules<T>(a.residual, a.rows, a.cols, a.ld_residual, row) : Granules{nullptr, 0, 0, true};
@@ -240,8 +247,7 @@ __global__ void __launch_bounds__(1024, 1) k_rmsnorm_ring(const Rms a, int stage
         if (add) ptx::bulk_load(at + row_bytes, gr.src, gr.bytes, full + stage);
     };
     if (t == 0)
-        for (int i = 0; i < stages && blockIdx.x + int64_t(i) * gridDim.x < a.rows; ++i)
-            issue(blockIdx.x + int64_t(i) * gridDim.x, i);
+        for (int i = 0; i < stages && first + i * step < a.rows; ++i) issue(first + i * step, i);
     // Column of value q of the thread's piece i.
     auto column = [&](int i, int q) {
         return VEC ? (t + i * nt) * V + q : (i * (nt >> 5) + (t >> 5)) * 128 + q * 32 + lane;
@@ -257,7 +263,7 @@ __global__ void __launch_bounds__(1024, 1) k_rmsnorm_ring(const Rms a, int stage
     bool ok = true;
     int stage = 0, turn = 0;
     uint32_t phase = 0;
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    for (int64_t row = first; row < a.rows; row += step) {
         if (ok) ok = ptx::mbar_wait_bounded(full + stage, phase);
         uint8_t *at = ring + size_t(stage) * stage_bytes;
         T *px = reinterpret_cast<T *>(at), *pr = reinterpret_cast<T *>(at + row_bytes);
@@ -317,10 +323,10 @@ __global__ void __launch_bounds__(1024, 1) k_rmsnorm_ring(const Rms a, int stage
         }
         const float sum = block_sum(sums.x + sums.y, slots[turn]);
         if (t == 0 && ok) {  // past its meeting the block has read this row
-            const int64_t next = row + int64_t(stages) * gridDim.x;
+            const int64_t next = row + stages * step;
             if (next < a.rows) issue(next, stage);
         }
-        const float rstd = 1.0f / sqrtf(fmaf(sum, a.inv_cols, a.eps));
+        const float rstd = __frsqrt_rn(fmaf(sum, a.inv_cols, a.eps));
         if (t == 0 && a.rstd && TR_STORE_OK(s.rstd, a.rstd + row, 4)) a.rstd[row] = rstd;
         T *yo = static_cast<T *>(a.y) + row * a.ld_y;
         float y[N][V];
@@ -346,7 +352,7 @@ __global__ void __launch_bounds__(1024, 1) k_rmsnorm_ring(const Rms a, int stage
                 for (int q = 0; q < V; ++q) {
                     const int j = column(i, q);
                     if (a.y && j < cols && TR_STORE_OK(s.y, yo + j, int(sizeof(T)))) put_value(yo + j, y[i][q]);
-                    m = max_abs(m, y[i][q]);
+                    if (q % 2) m = max_abs(m, y[i][q - 1], y[i][q]);
                 }
                 if (!a.q || column(i, 0) - lane >= cols) continue;
                 // One division for both ratios: lane 0 takes the scale.
@@ -405,7 +411,7 @@ __global__ void __launch_bounds__(1024) k_rmsnorm_any(const Rms a) {
             sum[0] = fmaf(v, v, sum[0]);
         }
         group_sum<1024, 1>(sum, slots[turn]);
-        const float rstd = 1.0f / sqrtf(fmaf(sum[0], a.inv_cols, a.eps));
+        const float rstd = __frsqrt_rn(fmaf(sum[0], a.inv_cols, a.eps));
         if (threadIdx.x == 0 && a.rstd && TR_STORE_OK(s.rstd, a.rstd + row, 4)) a.rstd[row] = rstd;
         const T *from = a.residual ? h : x;
         for (int64_t c0 = int64_t(warp) * 128; c0 < a.cols; c0 += int64_t(blockDim.x) * 4) {
@@ -435,15 +441,69 @@ __global__ void __launch_bounds__(1024) k_rmsnorm_any(const Rms a) {
     }
 }
 
-// The transposed 8-bit output, a 128 x 128 tile of h at a time: a thread holds the 8 x 8 values of row group rg
-// and column group cg, as the quantizer does.  The last rows of h are the likeliest to be in L2 still, so the tiles
-// are walked from the last to the first.  VEC: rows of h on 16-byte boundaries.
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) k_rmsnorm_turned(const Rms a) {
+// Four neighbouring values of a row.
+template <typename T>
+struct Quad;
+template <>
+struct Quad<__nv_bfloat16> {
+    uint32_t w[2];
+    __device__ __forceinline__ void clear() { w[0] = w[1] = 0u; }
+    __device__ __forceinline__ void set(int q, __nv_bfloat16 v) { w[q >> 1] |= uint32_t(__bfloat16_as_ushort(v)) << (q & 1 ? 16 : 0); }
+    __device__ __forceinline__ float get(int q) const { return __uint_as_float(q & 1 ? w[q >> 1] & 0xffff0000u : w[q >> 1] << 16); }
+    __device__ __forceinline__ void held(const void *p) {  // in shared memory
+        const uint2 v = *static_cast<const uint2 *>(p);
+        w[0] = v.x;
+        w[1] = v.y;
+    }
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
+        const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(p));
+        w[0] = v.x;
+        w[1] = v.y;
+    }
+};
+template <>
+struct Quad<float> {
+    float e[4];
+    __device__ __forceinline__ void clear() { e[0] = e[1] = e[2] = e[3] = 0.0f; }
+    __device__ __forceinline__ void set(int q, float v) { e[q] = v; }
+    __device__ __forceinline__ float get(int q) const { return e[q]; }
+    __device__ __forceinline__ void held(const void *p) {
+        const float4 v = *static_cast<const float4 *>(p);
+        e[0] = v.x;
+        e[1] = v.y;
+        e[2] = v.z;
+        e[3] = v.w;
+    }
+    __device__ __forceinline__ void load(const float *p) {
+        const float4 v = __ldcs(reinterpret_cast<const float4 *>(p));
+        e[0] = v.x;
+        e[1] = v.y;
+        e[2] = v.z;
+        e[3] = v.w;
+    }
+};
+
+constexpr int kTurners = 512;  // threads to a tile
+struct TurnSpace {
+    float most[16][128];
+    float inv[128], rstd[128], w[128];
+    uint2 turned[128 * 16];
+};
+
+// The transposed 8-bit output after the rows, a 128 x 128 tile of h at a time: a thread holds 8 rows (group rg, its
+// warp) of 4 columns (group cg, its lane), as u = h * rstd for both walks over it.  The bytes go through shared memory in
+// slots of 8, slot XOR column group.  AHEAD: the next tile's rows, on 16-byte boundaries, are copied to shared memory
+// meanwhile (a block meets four times a tile, and two blocks to an SM do not cover for one another: 16384 x 8192
+// bf16 takes 88 us without); else they come straight from memory, VEC in one access to four values.  The last rows
+// of h are the likeliest to be in L2 still, so the tiles are walked from the last to the first.
+//
+// With these tiles in the same launch as the rows, each waiting for its rows' rstd, so that h comes from L2, 16384 x
+// 8192 bf16 took 259 us, 234 with this kernel's first form after the rows'.
+template <typename T, bool VEC, bool AHEAD>
+__global__ void __launch_bounds__(kTurners, 2) k_rmsnorm_turned(const Rms a) {
     pdl_prologue();
-    __shared__ alignas(16) float col_max[8][128];
-    __shared__ alignas(16) float col_inv[128];
-    __shared__ uint2 turned[128 * 16];
+    __shared__ alignas(16) TurnSpace m;
+    extern __shared__ uint4 ring4[];  // AHEAD: two tiles
     const T *src = static_cast<const T *>(a.residual ? a.h : a.x);
     const int64_t ld = a.residual ? a.ld_h : a.ld_x;
     [[maybe_unused]] const dbg::Side sh = dbg::side(src, 1, a.rows, a.cols, ld, 0, sizeof(T));
@@ -451,97 +511,137 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) k_rmsnorm_turned(
     [[maybe_unused]] const dbg::Side sd = dbg::side(a.rstd, 1, 1, a.rows, a.rows, 0, 4);
     [[maybe_unused]] const dbg::Side st = dbg::side(a.qt, 1, a.cols, a.rows, a.ld_qt, 0, 1);
     [[maybe_unused]] const dbg::Side su = dbg::side(a.scale_t, 1, (a.rows + 127) / 128, a.cols, a.ld_scale_t, 0, 4);
-    const int64_t tiles_r = (a.rows + 127) / 128, tiles_c = (a.cols + 127) / 128;
-    const int t = threadIdx.x, lane = t & 31, cg = t & 15, rg = t >> 4, warp = t >> 5;
-    for (int64_t at = tiles_r * tiles_c - 1 - int64_t(blockIdx.x); at >= 0; at -= gridDim.x) {
-        const int64_t tr = at / tiles_c, tc = at - tr * tiles_c, r0 = tr * 128 + rg * 8, c0 = tc * 128 + cg * 8;
-        Pack<T, 16 / int(sizeof(T))> h[8][sizeof(T) / 2];
-        constexpr int W = 16 / int(sizeof(T));
-        float rstd[8], w[8];
+    const int t = threadIdx.x, cg = t & 31, rg = t >> 5;
+    // Tiles counted in 32 bits: a 64-bit division would be a hundred instructions to each thread.
+    const uint32_t tiles_c = uint32_t((a.cols + 127) / 128), tiles = uint32_t((a.rows + 127) / 128) * tiles_c;
+    constexpr int kChunks = 128 * int(sizeof(T)) / 16, kRow = 128 * int(sizeof(T));  // of a tile's row: granules, bytes
+    // What tile `at` needs: rstd of its rows and the weights of its columns, one to each of 256 threads, and its rows.
+    auto number = [&](uint32_t at) {
+        const int64_t row = int64_t(at / tiles_c) * 128 + t, col = int64_t(at % tiles_c) * 128 + t - 128;
+        if (t < 128) return row < a.rows && TR_LOAD_OK(sd, a.rstd + row, 4) ? a.rstd[row] : 0.0f;
+        return t < 256 && col < a.cols ? weight(a.gamma, a.w_bf16, col, sw) : 0.0f;
+    };
+    auto copy = [&](uint32_t at, int buffer) {
+        if constexpr (AHEAD) {
+            uint8_t *to = reinterpret_cast<uint8_t *>(ring4) + size_t(buffer) * 128 * kRow;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const T *p = src + (r0 + i) * ld;
-#pragma unroll
-            for (int k = 0; k < int(sizeof(T)) / 2; ++k) {
-                if (VEC && r0 + i < a.rows && c0 + (k + 1) * W <= a.cols) {
-                    h[i][k] = load_chunk<T, W, false>(p, c0 + k * W, a.cols, sh);
-                } else {
-                    h[i][k].clear();
-                    if (r0 + i < a.rows)
-#pragma unroll
-                        for (int q = 0; q < W; ++q)
-                            if (c0 + k * W + q < a.cols && TR_LOAD_OK(sh, p + c0 + k * W + q, int(sizeof(T)))) h[i][k].set(q, p[c0 + k * W + q]);
-                }
+            for (int k = 0; k < 128 * kChunks / kTurners; ++k) {
+                const int id = t + k * kTurners, r = id / kChunks, c = id % kChunks;
+                const int64_t row = int64_t(at / tiles_c) * 128 + r, col = int64_t(at % tiles_c) * 128 + c * (16 / int(sizeof(T)));
+                uint8_t *dst = to + r * kRow + c * 16;
+                const T *p = src + row * ld + col;
+                if (row < a.rows && col < a.cols && TR_LOAD_OK(sh, p, 16)) ptx::cp_async_16(dst, p);
+                else *reinterpret_cast<uint4 *>(dst) = make_uint4(0u, 0u, 0u, 0u);
             }
+            ptx::cp_async_commit();
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            rstd[i] = r0 + i < a.rows && TR_LOAD_OK(sd, a.rstd + r0 + i, 4) ? a.rstd[r0 + i] : 0.0f;
-            w[i] = c0 + i < a.cols ? weight(a.gamma, a.w_bf16, c0 + i, sw) : 0.0f;
+    };
+    uint32_t left = blockIdx.x;  // tiles are counted from the end
+    if (left >= tiles) return;
+    float next = number(tiles - 1 - left);
+    copy(tiles - 1 - left, 0);
+    for (int buffer = 0; left < tiles; left += gridDim.x, buffer ^= 1) {
+        const uint32_t at = tiles - 1 - left;
+        const int64_t tr = at / tiles_c, tc = at % tiles_c, r0 = tr * 128 + rg * 8, c0 = tc * 128 + cg * 4;
+        const bool whole = VEC && tr * 128 + 128 <= a.rows && tc * 128 + 128 <= a.cols;
+        if (t < 128) m.rstd[t] = next;
+        else if (t < 256) m.w[t - 128] = next;
+        const bool more = tiles - left > gridDim.x;
+        if (more) {
+            next = number(at - gridDim.x);
+            copy(at - gridDim.x, buffer ^ 1);
         }
-        // Columns j and j + 1 of row i.
-        auto pair = [&](int i, int j) {
-            return __fmul2_rn(__fmul2_rn(make_float2(h[i][j / W].get(j % W), h[i][j / W].get(j % W + 1)), make_float2(rstd[i], rstd[i])),
-                              make_float2(w[j], w[j + 1]));
-        };
-        float most[8];
+        Quad<T> h[8];
+        if constexpr (AHEAD) {
+            if (more) ptx::cp_async_wait<1>();
+            else ptx::cp_async_wait<0>();
+            __syncthreads();
+            const uint8_t *from = reinterpret_cast<const uint8_t *>(ring4) + size_t(buffer) * 128 * kRow;
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-            most[j] = most[j + 1] = kFloor;
+            for (int i = 0; i < 8; ++i) h[i].held(from + (rg * 8 + i) * kRow + cg * 4 * int(sizeof(T)));
+        } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float2 v = pair(i, j);
-                most[j] = max_abs(most[j], v.x);
-                most[j + 1] = max_abs(most[j + 1], v.y);
+                const T *p = src + (r0 + i) * ld + c0;
+                h[i].clear();
+                if (VEC && (whole || (r0 + i < a.rows && c0 + 4 <= a.cols))) {
+                    if (TR_LOAD_OK(sh, p, int(4 * sizeof(T)))) h[i].load(p);
+                } else if (r0 + i < a.rows) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        if (c0 + q < a.cols && TR_LOAD_OK(sh, p + q, int(sizeof(T)))) h[i].set(q, p[q]);
+                }
             }
-            most[j] = max_abs(most[j], __shfl_xor_sync(0xffffffffu, most[j], 16));
-            most[j + 1] = max_abs(most[j + 1], __shfl_xor_sync(0xffffffffu, most[j + 1], 16));
+            __syncthreads();
         }
-        if (lane < 16) {
-            float4 *p = reinterpret_cast<float4 *>(&col_max[warp][cg * 8]);
-            p[0] = make_float4(most[0], most[1], most[2], most[3]);
-            p[1] = make_float4(most[4], most[5], most[6], most[7]);
+        float2 u[8][2];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float rstd = m.rstd[rg * 8 + i];
+                u[i][j] = make_float2(h[i].get(2 * j) * rstd, h[i].get(2 * j + 1) * rstd);
+            }
+        const float4 w4 = *reinterpret_cast<const float4 *>(&m.w[cg * 4]);
+        const float2 w[2] = {make_float2(w4.x, w4.y), make_float2(w4.z, w4.w)};
+        float2 most[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            most[j] = make_float2(kFloor, kFloor);
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                const float2 v = __fmul2_rn(u[i][j], w[j]), x = __fmul2_rn(u[i + 1][j], w[j]);
+                most[j].x = max_abs(most[j].x, v.x, x.x);
+                most[j].y = max_abs(most[j].y, v.y, x.y);
+            }
         }
+        *reinterpret_cast<float4 *>(&m.most[rg][cg * 4]) = make_float4(most[0].x, most[0].y, most[1].x, most[1].y);
         __syncthreads();
         if (t < 128) {
             float amax = kFloor;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) amax = max_abs(amax, col_max[k][t]);
-            col_inv[t] = a.top / amax;
+            for (int k = 0; k < 16; k += 2) amax = max_abs(amax, m.most[k][t], m.most[k + 1][t]);
+            m.inv[t] = a.top / amax;
             if (tc * 128 + t < a.cols) {
-                float *u = a.scale_t + tr * a.ld_scale_t + tc * 128 + t;
-                if (TR_STORE_OK(su, u, 4)) *u = amax / a.top;
+                float *p = a.scale_t + tr * a.ld_scale_t + tc * 128 + t;
+                if (TR_STORE_OK(su, p, 4)) *p = amax / a.top;
             }
         }
         __syncthreads();
-        auto turn = [&](auto e5m2) {
+        auto bytes = [&](auto e5m2) {
+            constexpr __nv_fp8_interpretation_t K = decltype(e5m2)::value ? __NV_E5M2 : __NV_E4M3;
+            const float4 inv4 = *reinterpret_cast<const float4 *>(&m.inv[cg * 4]);
+            const float2 inv[2] = {make_float2(inv4.x, inv4.y), make_float2(inv4.z, inv4.w)};
 #pragma unroll
-            for (int j = 0; j < 8; j += 2) {
-                const float2 inv = *reinterpret_cast<const float2 *>(&col_inv[cg * 8 + j]);
-                float2 v[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = __fmul2_rn(pair(i, j), inv);
-                constexpr __nv_fp8_interpretation_t K = decltype(e5m2)::value ? __NV_E5M2 : __NV_E4M3;
-                uint32_t a[4], b[4];
+            for (int j = 0; j < 2; ++j) {
+                uint32_t p[4], q[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    a[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i].x, v[2 * i + 1].x), __NV_SATFINITE, K);
-                    b[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i].y, v[2 * i + 1].y), __NV_SATFINITE, K);
+                    const float2 x = __fmul2_rn(__fmul2_rn(u[2 * i][j], w[j]), inv[j]), v = __fmul2_rn(__fmul2_rn(u[2 * i + 1][j], w[j]), inv[j]);
+                    p[i] = __nv_cvt_float2_to_fp8x2(make_float2(x.x, v.x), __NV_SATFINITE, K);
+                    q[i] = __nv_cvt_float2_to_fp8x2(make_float2(x.y, v.y), __NV_SATFINITE, K);
                 }
-                turned[(cg * 8 + j) * 16 + (rg ^ cg)] = make_uint2(a[0] | a[1] << 16, a[2] | a[3] << 16);
-                turned[(cg * 8 + j + 1) * 16 + (rg ^ cg)] = make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
+                uint2 *slot = m.turned + (cg * 4 + 2 * j) * 16 + (rg ^ (cg & 15));
+                slot[0] = make_uint2(p[0] | p[1] << 16, p[2] | p[3] << 16);
+                slot[16] = make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
             }
         };
-        if (a.e5m2) turn(std::true_type());
-        else turn(std::false_type());
+        if (a.e5m2) bytes(std::true_type());
+        else bytes(std::false_type());
         __syncthreads();
+        const int r = t & 15;
+        uint8_t *p = a.qt + (tc * 128 + (t >> 4)) * a.ld_qt;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int c = i * 16 + rg;
-            const int64_t col = tc * 128 + c;
-            if (col < a.cols) store8(a.qt + col * a.ld_qt, tr * 128 + cg * 8, a.rows, turned[c * 16 + (cg ^ (c >> 3))], st);
+        for (int i = 0; i < 4; ++i, p += 32 * a.ld_qt) {
+            const int c = i * 32 + (t >> 4);
+            const uint2 v = m.turned[c * 16 + (r ^ (c >> 2 & 15))];
+            if (whole) {
+                if (TR_STORE_OK(st, p + tr * 128 + r * 8, 8)) *reinterpret_cast<uint2 *>(p + tr * 128 + r * 8) = v;
+            } else if (tc * 128 + c < a.cols) {
+                store8(p, tr * 128 + r * 8, a.rows, v, st);
+            }
         }
-        __syncthreads();  // the shared words are written anew in the next turn
+        // The next turn writes rstd and w (read before two meetings) at once, everything else past its first meeting.
     }
 }
 
@@ -573,10 +673,16 @@ cudaError_t launch_ring(const Rms &a, bool vec, cudaStream_t stream) {
 }
 
 template <typename T>
-cudaError_t launch_rows(const Rms &a, cudaStream_t stream) {
+bool rows_aligned(const Rms &a) {
     constexpr int V = 16 / int(sizeof(T)), es = int(sizeof(T));
-    const bool vec = a.cols % V == 0 && side_aligned16(a.x, a.ld_x, 0, 1, es) && (!a.y || side_aligned16(a.y, a.ld_y, 0, 1, es)) &&
-                     (!a.residual || (side_aligned16(a.residual, a.ld_residual, 0, 1, es) && side_aligned16(a.h, a.ld_h, 0, 1, es)));
+    return a.cols % V == 0 && side_aligned16(a.x, a.ld_x, 0, 1, es) && (!a.y || side_aligned16(a.y, a.ld_y, 0, 1, es)) &&
+           (!a.residual || (side_aligned16(a.residual, a.ld_residual, 0, 1, es) && side_aligned16(a.h, a.ld_h, 0, 1, es)));
+}
+
+template <typename T>
+cudaError_t launch_rows(const Rms &a, cudaStream_t stream) {
+    constexpr int V = 16 / int(sizeof(T));
+    const bool vec = rows_aligned<T>(a);
     const int64_t chunks = a.cols / V, resident = sm_count();
     if (vec && (reinterpret_cast<uintptr_t>(a.gamma) & 15u) == 0) {
         auto run = [&](auto kern, int threads, int rows_per_block, int64_t per_sm) {
@@ -600,11 +706,20 @@ template <typename T>
 cudaError_t launch_typed(const Rms &a, cudaStream_t stream) {
     const cudaError_t e = launch_rows<T>(a, stream);
     if (e != cudaSuccess || !a.qt) return e;
-    const int64_t tiles = ((a.rows + 127) / 128) * ((a.cols + 127) / 128), most = int64_t(1) << 30;
-    const dim3 grid(unsigned(tiles < most ? tiles : most));
-    const bool vec = a.residual ? side_aligned16(a.h, a.ld_h, 0, 1, sizeof(T)) : side_aligned16(a.x, a.ld_x, 0, 1, sizeof(T));
-    return vec ? launch_pdl(k_rmsnorm_turned<T, true>, grid, dim3(256), 0, stream, a)
-               : launch_pdl(k_rmsnorm_turned<T, false>, grid, dim3(256), 0, stream, a);
+    const int64_t tiles = ((a.rows + 127) / 128) * ((a.cols + 127) / 128), resident = 2 * int64_t(sm_count());
+    if (tiles > 0x7fffffffll) return cudaErrorInvalidValue;
+    const dim3 grid(unsigned(tiles < resident ? tiles : resident));
+    constexpr int V = 16 / int(sizeof(T));
+    const bool vec = a.cols % V == 0 && (a.residual ? side_aligned16(a.h, a.ld_h, 0, 1, sizeof(T)) : side_aligned16(a.x, a.ld_x, 0, 1, sizeof(T)));
+    if constexpr (sizeof(T) == 2) {
+        if (vec) {
+            constexpr size_t two = 2 * 128 * 128 * sizeof(T);
+            const cudaError_t allowed = allow_shared<k_rmsnorm_turned<T, true, true>>(two);
+            return allowed != cudaSuccess ? allowed : launch_pdl(k_rmsnorm_turned<T, true, true>, grid, dim3(kTurners), two, stream, a);
+        }
+    }
+    return vec ? launch_pdl(k_rmsnorm_turned<T, true, false>, grid, dim3(kTurners), 0, stream, a)
+               : launch_pdl(k_rmsnorm_turned<T, false, false>, grid, dim3(kTurners), 0, stream, a);
 }
 
 }  // namespace

@@ -171,7 +171,8 @@ def test_backward_many_rows():
 
 def test_8_bits_many_rows():
     import torch
-    for rows, cols, kind in [(5000, 256, "bf16"), (3001, 1000, "f32"), (1300, 8192, "bf16"), (2000, 519, "f32")]:
+    for rows, cols, kind in [(5000, 256, "bf16"), (3001, 1000, "f32"), (1300, 8192, "bf16"), (2000, 519, "f32"), (1025, 8200, "bf16"),
+                             (1100, 5000, "f32"), (1023, 4096, "bf16")]:
         g = torch.Generator(device="cuda").manual_seed(rows)
         x, res = (torch.randn(rows, cols, device="cuda", generator=g).to(torch_types(kind)) for _ in range(2))
         gamma = torch.rand(cols, device="cuda", generator=g) + 0.5
