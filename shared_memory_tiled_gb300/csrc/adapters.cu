@@ -47,17 +47,24 @@ __global__ void __launch_bounds__(kPlanThreads) k_adapter_plan(const int32_t *in
     int32_t *mine = counts + warp * groups;
     auto walk = [&](auto put) {
         if (warp >= warps) return;
-        for (int64_t i0 = first; i0 < last; i0 += 32) {
-            const int64_t i = i0 + lane;
-            const unsigned here = __ballot_sync(0xffffffffu, i < last);
-            if (i < last) {
-                const int g = group_of(i);
-                const unsigned same = __match_any_sync(here, g);
-                put(i, g, __popc(same & ((1u << lane) - 1)));
-                __syncwarp(here);
-                if (lane == 31 - __clz(same)) mine[g] += __popc(same);
+        constexpr int U = 8;  // loads on their way
+        for (int64_t i0 = first; i0 < last; i0 += 32 * U) {
+            int g[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) g[u] = i0 + u * 32 + lane < last ? group_of(i0 + u * 32 + lane) : 0;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (i0 + u * 32 >= last) break;
+                const int64_t i = i0 + u * 32 + lane;
+                const unsigned here = __ballot_sync(0xffffffffu, i < last);
+                if (i < last) {
+                    const unsigned same = __match_any_sync(here, g[u]);
+                    put(i, g[u], __popc(same & ((1u << lane) - 1)));
+                    __syncwarp(here);
+                    if (lane == 31 - __clz(same)) mine[g[u]] += __popc(same);
+                }
+                __syncwarp();
             }
-            __syncwarp();
         }
     };
     walk([](int64_t, int, int) {});
@@ -411,6 +418,17 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
             const int w = warp & 3;  // the quarter of the lanes this warp may read
             const int row = w * 32 + lane, th = t - 128, group = (warp - 4) / 4;
             const uint32_t lanes = uint32_t(w * 32) << 16;
+            const int n = int(g.n), j_first = int(first_tile) * kColumns, left = count - w * 32;  // rows of this warp
+            // EDGE: a lane's column of base in each of the warp's rows.
+            auto old_value = [&](int r, int j) {
+                const T *p = static_cast<const T *>(g.base) + rows[w * 32 + r] * g.ld_base + j;
+                return g.base && j < n && TR_LOAD_OK(sb, p, int(sizeof(T))) ? *p : T(0.0f);
+            };
+            [[maybe_unused]] T old[EDGE ? 32 : 1];
+            if constexpr (EDGE) {
+#pragma unroll
+                for (int r = 0; r < 32; ++r) old[r] = r < left && group < tiles ? old_value(r, j_first + group * kColumns + lane) : T(0.0f);
+            }
             if (group < S::kHalves) {
                 const float scale = g.scale ? g.scale[at.x] : 1.0f;
                 constexpr int W = RP / S::kHalves;  // inner values to a thread
@@ -524,7 +542,6 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(&inner_ready);
             }
-            const int n = int(g.n), j_first = int(first_tile) * kColumns, left = count - w * 32;  // rows of this warp
             int32_t token[8];  // of the rows that this lane stores
 #pragma unroll
             for (int l = 0; l < 8; ++l) token[l] = l * 4 + lane / 8 < left ? rows[w * 32 + l * 4 + lane / 8] : 0;
@@ -583,17 +600,12 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
                     }
                 } else if (left > 0) {
                     // A quarter of the columns at a time goes through shared memory, so that lanes take neighbouring
-                    // columns; base's values of the quarter are on their way meanwhile.
+                    // columns; base's values of the next quarter are on their way meanwhile.
                     uint4 *staging = reinterpret_cast<uint4 *>(slots) + (warp - 4) * 256;
 #pragma unroll 1
                     for (int q = 0; q < 4; ++q) {
                         const int j = j_first + i * kColumns + q * 32 + lane;
-                        T old[32];
-#pragma unroll
-                        for (int r = 0; r < 32; ++r) {
-                            const T *p = static_cast<const T *>(g.base) + (r < left ? rows[w * 32 + r] : 0) * g.ld_base + j;
-                            old[r] = g.base && r < left && j < n && TR_LOAD_OK(sb, p, int(sizeof(T))) ? *p : T(0.0f);
-                        }
+                        const int j_next = q < 3 ? j + 32 : i + kGroups < tiles ? j + kGroups * kColumns - 96 : n;
                         float sums[32];
                         ptx::tmem_load32(sums, from + q * 32);
                         ptx::tmem_wait_load32(sums);
@@ -604,11 +616,13 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
                         __syncwarp();
 #pragma unroll
                         for (int r = 0; r < 32; ++r) {
+                            if (r >= left) break;
                             const float f = reinterpret_cast<const float *>(staging)[(r * 8 + ((lane >> 2) ^ (r & 7))) * 4 + (lane & 3)];
-                            if (r < left && j < n) {
+                            if (j < n) {
                                 T *o = static_cast<T *>(g.out) + rows[w * 32 + r] * g.ld_out + j;
                                 if (TR_STORE_OK(so, o, int(sizeof(T)))) put_value(o, f + to_f32(old[r]));
                             }
+                            old[r] = old_value(r, j_next);
                         }
                         __syncwarp();
                     }
@@ -952,11 +966,13 @@ cudaError_t launch_one(const CUtensorMap (&maps)[6], Adapt g, int64_t tiles, cud
     auto kern = k_adapters<RP, T, EDGE>;
     const cudaError_t e = allow_shared<k_adapters<RP, T, EDGE>>(S::kSmem);
     if (e != cudaSuccess) return e;
-    // CTAs to a tile until the fewest tiles that these tokens can make fill what is resident at one time (how many there
-    // are is known on the device alone), each keeping two chunks of k or more.
+    // CTAs to a tile until the tiles fill what is resident at one time, each keeping two chunks of k or more.  How many
+    // tiles there are is known on the device alone: the fewest that these tokens can make, and every second adapter's
+    // end (2000 tokens of 8 adapters, 8192 x 8192: 25 tiles take 56 us with 8 CTAs to a tile, two waves).
     const int64_t resident = sm_count(), least = (g.tokens + kPlanTile - 1) / kPlanTile;
+    const int64_t likely = least + (tiles < g.adapters + 1 ? tiles : g.adapters + 1) / 2;
     g.split = 1;
-    while (g.split < 8 && least * g.split * 2 <= resident && g.chunks >= g.split * 4) g.split *= 2;
+    while (g.split < 8 && likely * g.split * 2 <= resident && g.chunks >= g.split * 4) g.split *= 2;
     return launch_clusters(kern, tiles * g.split, kThreads, S::kSmem, g.split, stream, maps[0], maps[1], maps[2], maps[3], maps[4], maps[5], g);
 }
 
