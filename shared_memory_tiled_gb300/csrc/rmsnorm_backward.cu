@@ -270,8 +270,9 @@ __global__ void __launch_bounds__(512) k_rms_dx(const RmsBwd a) {
         for (int64_t j = threadIdx.x; j < a.cols; j += blockDim.x) {
             if (!TR_LOAD_OK(sd, dy + j, int(sizeof(T))) || !TR_LOAD_OK(sh, h + j, int(sizeof(T)))) continue;
             const float g = to_f32(dy[j]) * weight(a.gamma, a.w_bf16, j, sw), u = to_f32(h[j]) * rstd;
-            float v = rstd * fmaf(-u, c, g);
-            if (a.dres && TR_LOAD_OK(se, dr + j, int(sizeof(T)))) v += to_f32(dr[j]);
+            float v = 0.0f;
+            if (a.dres && TR_LOAD_OK(se, dr + j, int(sizeof(T)))) v = to_f32(dr[j]);
+            v = fmaf(rstd, fmaf(-u, c, g), v);
             if (TR_STORE_OK(so, dx + j, int(sizeof(T)))) put_value(dx + j, v);
         }
     }
