@@ -528,7 +528,7 @@ typedef struct tr_adapters_args {
  * and out[i] = base[i] for a token without one.  Sums are held in 32 bits, v in
  * 16 significant bits or more, out is rounded once.  Equal calls give equal bits.  x, a
  * and b are 16-byte aligned, their row pitches and strides multiples of 8 values (else
- * TR_ERR_UNSUPPORTED); tokens, k and n are below 2^31. */
+ * TR_ERR_UNSUPPORTED); tokens is below 2^31, k and n are below 2^30. */
 tr_status tr_adapters(const tr_adapters_args *args);
 
 /* Host-only planning: the variant tr_transpose_ex would run for these

@@ -261,9 +261,9 @@ tr_status adapters(const tr_adapters_args *a) {
     if (!a) return TR_ERR_NULL;
     if (a->reserved != 0 || !wide(a->out_dtype)) return unsupported("adapters: fp32 or bf16 out");
     if (a->tokens < 0 || a->adapters < 0 || a->k < 0 || a->n < 0) return TR_ERR_BAD_DIM;
-    const int64_t top = int64_t(1) << 31, need = tr_adapter_plan_bytes(a->tokens, a->adapters);
+    const int64_t top = int64_t(1) << 30, need = tr_adapter_plan_bytes(a->tokens, a->adapters);
     if (a->rank < 1 || a->rank > 128) return unsupported("adapters: ranks are 1 to 128");
-    if (need < 0 || a->k >= top || a->n >= top) return unsupported("adapters: 2^31 tokens or values, or 2^15 adapters, or more");
+    if (need < 0 || a->k >= top || a->n >= top) return unsupported("adapters: 2^31 tokens, 2^30 values to a row or 2^15 adapters, or more");
     if (a->tokens == 0 || a->n == 0) return TR_OK;
     const int es = esize_of(a->out_dtype);
     Range in[6] = {}, out;

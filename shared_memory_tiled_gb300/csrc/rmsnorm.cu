@@ -665,6 +665,7 @@ cudaError_t launch_ring(const Rms &a, bool vec, cudaStream_t stream) {
     const int64_t resident = int64_t(sm_count()) * per_sm, each = 160 * 1024 / stage_bytes > 5 ? 160 * 1024 / stage_bytes : 5;
     int64_t grid = (a.rows + each - 1) / each;
     if (grid < resident) grid = a.rows < resident ? a.rows : resident;
+    if (grid > int64_t(1) << 30) grid = int64_t(1) << 30;
     // Always the most that any call needs.
     const cudaError_t e = vec ? allow_shared<k_rmsnorm_ring<T, true>>(ring_room(1)) : allow_shared<k_rmsnorm_ring<T, false>>(ring_room(1));
     if (e != cudaSuccess) return e;

@@ -107,7 +107,7 @@ def adapters(**kw):
 
 def test_adapters_refusals():
     assert B.tr_adapters(None) == S.ERR_NULL
-    for bad in (dict(out_dtype=2), dict(reserved=1), dict(rank=0), dict(rank=129), dict(rank=-1), dict(k=1 << 31), dict(n=1 << 31),
+    for bad in (dict(out_dtype=2), dict(reserved=1), dict(rank=0), dict(rank=129), dict(rank=-1), dict(k=1 << 30), dict(n=1 << 30),
                 dict(tokens=1 << 31), dict(adapters=1 << 15)):
         assert adapters(**bad) == S.ERR_UNSUPPORTED, bad
     for name in ("tokens", "adapters", "k", "n"):
