@@ -240,7 +240,8 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
     constexpr int TERMS = sizeof(T) == 2 ? 2 : 3;
     using S = Shape<RP, TERMS>;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t full_x[S::kStagesX], empty_x[S::kStagesX], full[S::kStages], empty[S::kStages], joined[3], inner_full, inner_ready, sums_full[kGroups], sums_empty[kGroups], drained;
+    __shared__ uint64_t full_x[S::kStagesX], empty_x[S::kStagesX], full[S::kStages], empty[S::kStages];
+    __shared__ uint64_t joined[3], inner_full, inner_ready, sums_full[kGroups], sums_empty[kGroups], drained;
     __shared__ uint64_t base_full[S::kSlots], base_empty[S::kSlots];
     __shared__ uint32_t tmem_base;
     __shared__ int32_t rows[128];
@@ -419,15 +420,17 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
             const int row = w * 32 + lane, th = t - 128, group = (warp - 4) / 4;
             const uint32_t lanes = uint32_t(w * 32) << 16;
             const int n = int(g.n), j_first = int(first_tile) * kColumns, left = count - w * 32;  // rows of this warp
-            // EDGE: a lane's column of base in each of the warp's rows.
+            // EDGE: a lane's column of base in each of the warp's rows, whose tokens the lanes hold.
+            const int32_t own_token = EDGE && lane < left ? rows[row] : 0;
+            auto token_at = [&](int r) { return int64_t(__shfl_sync(0xffffffffu, own_token, r)); };
             auto old_value = [&](int r, int j) {
-                const T *p = static_cast<const T *>(g.base) + rows[w * 32 + r] * g.ld_base + j;
-                return g.base && j < n && TR_LOAD_OK(sb, p, int(sizeof(T))) ? *p : T(0.0f);
+                const T *p = static_cast<const T *>(g.base) + token_at(r) * g.ld_base + j;
+                return g.base && r < left && j < n && TR_LOAD_OK(sb, p, int(sizeof(T))) ? *p : T(0.0f);
             };
             [[maybe_unused]] T old[EDGE ? 32 : 1];
             if constexpr (EDGE) {
 #pragma unroll
-                for (int r = 0; r < 32; ++r) old[r] = r < left && group < tiles ? old_value(r, j_first + group * kColumns + lane) : T(0.0f);
+                for (int r = 0; r < 32; ++r) old[r] = old_value(r, group < tiles ? j_first + group * kColumns + lane : n);
             }
             if (group < S::kHalves) {
                 const float scale = g.scale ? g.scale[at.x] : 1.0f;
@@ -443,18 +446,18 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
                         ptx::tmem_load16(v, tmem + lanes + c0);
                         ptx::tmem_wait_load16(v);
                     } else {
-    #pragma unroll
+#pragma unroll
                         for (int c = 0; c < W; c += 32) {
                             float part[32];
                             ptx::tmem_load32(part, tmem + lanes + c0 + c);
                             ptx::tmem_wait_load32(part);
-    #pragma unroll
+#pragma unroll
                             for (int k = 0; k < 32; ++k) v[c + k] = part[k];
                         }
                     }
                     ptx::tc_fence_before();
                 } else {
-    #pragma unroll
+#pragma unroll
                     for (int c = 0; c < W; ++c) v[c] = 0.0f;
                 }
                 if (g.split > 1) {
@@ -517,15 +520,15 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
                 // The terms of the inner values, 8 to a 16-byte chunk of a row in the 128-byte swizzle: hi + lo (+ a
                 // third) stand for 16 (24) significant bits, in products with b that are exact in 32 bits.  An
                 // infinity is all in the first.
-    #pragma unroll
+#pragma unroll
                 for (int c = 0; c < W; c += 8) {
                     float left[8];
-    #pragma unroll
+#pragma unroll
                     for (int k = 0; k < 8; ++k) left[k] = c0 + c + k < g.rank ? v[c + k] * scale : 0.0f;
-    #pragma unroll
+#pragma unroll
                     for (int term = 0; term < TERMS; ++term) {
                         uint32_t word[4];
-    #pragma unroll
+#pragma unroll
                         for (int k = 0; k < 8; k += 2) {
                             const __nv_bfloat162 two = __floats2bfloat162_rn(left[k], left[k + 1]);
                             const float2 f = __bfloat1622float2(two);
@@ -614,15 +617,17 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
                             staging[lane * 8 + (c ^ (lane & 7))] = make_uint4(__float_as_uint(sums[4 * c]), __float_as_uint(sums[4 * c + 1]),
                                                                               __float_as_uint(sums[4 * c + 2]), __float_as_uint(sums[4 * c + 3]));
                         __syncwarp();
+                        // base's values are used up before the next are asked for, and those before the stores: a wait
+                        // for a value waits for all loads before it.
+#pragma unroll
+                        for (int r = 0; r < 32; ++r)
+                            sums[r] = reinterpret_cast<const float *>(staging)[(r * 8 + ((lane >> 2) ^ (r & 7))) * 4 + (lane & 3)] + to_f32(old[r]);
+#pragma unroll
+                        for (int r = 0; r < 32; ++r) old[r] = old_value(r, j_next);
 #pragma unroll
                         for (int r = 0; r < 32; ++r) {
-                            if (r >= left) break;
-                            const float f = reinterpret_cast<const float *>(staging)[(r * 8 + ((lane >> 2) ^ (r & 7))) * 4 + (lane & 3)];
-                            if (j < n) {
-                                T *o = static_cast<T *>(g.out) + rows[w * 32 + r] * g.ld_out + j;
-                                if (TR_STORE_OK(so, o, int(sizeof(T)))) put_value(o, f + to_f32(old[r]));
-                            }
-                            old[r] = old_value(r, j_next);
+                            T *o = static_cast<T *>(g.out) + token_at(r) * g.ld_out + j;
+                            if (r < left && j < n && TR_STORE_OK(so, o, int(sizeof(T)))) put_value(o, sums[r]);
                         }
                         __syncwarp();
                     }
@@ -663,8 +668,10 @@ struct Few {
     int32_t rank, k, n, split, which;
 };
 
-// Up to kFewTokens tokens this kernel works alone, up to kBothTokens on the small tiles.
-constexpr int64_t kFewTokens = 32, kBothTokens = 2048;
+// Up to kFewTokens tokens (kFewTokensNarrow with ranks up to 16) this kernel works alone, up to kBothTokens on the small
+// tiles.  64 tokens, 8192 x 8192, alone and both: rank 16 15.4 and 16.2 us with 48 adapters, 22.3 and 20.5 with one, and a
+// launch and six tensor maps less for the host; rank 32 23.1 and 23.9, 28.5 and 21.8.
+constexpr int64_t kFewTokens = 32, kFewTokensNarrow = 64, kBothTokens = 2048;
 constexpr int kFewThreads = 256, kFewWarps = kFewThreads / 32;
 
 // D[16][8] += A[16][16] B[8][16]^T, a fragment's words being pairs along the contraction.
@@ -1012,7 +1019,7 @@ cudaError_t launch_adapters(const tr_adapters_args &p, const char **why) {
     const int rp = p.rank <= 16 ? 16 : p.rank <= 32 ? 32 : p.rank <= 64 ? 64 : 128;
     const int64_t tiles = plan_tiles(p.tokens, p.adapters);
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(p.stream);
-    const bool alone = p.tokens <= kFewTokens;
+    const bool alone = p.tokens <= (rp == 16 ? kFewTokensNarrow : kFewTokens);
     if (p.tokens <= kBothTokens) {
         const Few few{static_cast<const __nv_bfloat16 *>(p.x), static_cast<const __nv_bfloat16 *>(p.a), static_cast<const __nv_bfloat16 *>(p.b),
                       p.scale, g.plan, p.base, p.out, p.tokens, p.adapters, p.ld_x, p.ld_a, p.stride_a, p.ld_b, p.stride_b, p.ld_base, p.ld_out,
