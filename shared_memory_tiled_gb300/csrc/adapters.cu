@@ -165,7 +165,10 @@ struct Shape {
     static constexpr int kStageBytes = kTileX + RP * 128;            // of x and a, or a tile of b
     static constexpr int kHalves = RP > 32 ? 2 : 1;                  // groups of warps that share the inner values
     static constexpr int kInner = 128 * RP * 4, kTerms = (RP * TERMS + 63) / 64 * kTileX;
-    static constexpr int kRegion = kInner > kTerms ? kInner : kTerms;
+    // The terms have a place of their own where that costs few stages: the cluster need not meet again before they are
+    // written.
+    static constexpr bool kApart = RP <= 32;
+    static constexpr int kRegion = kApart ? kInner + kTerms : kInner > kTerms ? kInner : kTerms, kTermsAt = kApart ? kInner : 0;
     // Of 224 KB: two slots of 16 KB for base to each group (they also hold what a warp exchanges where base does not
     // come through them), or one, and the rest for stages.  Before the inner values are there the slots are stages too.
     static constexpr int kRoom = 224 * 1024 - kRegion;
@@ -371,7 +374,7 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
             }
             __syncwarp();
             ok = ok && ptx::mbar_wait_bounded(&inner_ready, 0);
-            const uint32_t v = ptx::smem_addr(region);
+            const uint32_t v = ptx::smem_addr(region + S::kTermsAt);
             for (int i = 0; i < tiles && ok; ++i) {
                 const int s = i % S::kStages, b = i % kGroups;
                 ok = ok && ptx::mbar_wait_bounded(full + s, (i / S::kStages) & 1) &&
@@ -420,17 +423,18 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
             const int row = w * 32 + lane, th = t - 128, group = (warp - 4) / 4;
             const uint32_t lanes = uint32_t(w * 32) << 16;
             const int n = int(g.n), j_first = int(first_tile) * kColumns, left = count - w * 32;  // rows of this warp
-            // EDGE: a lane's column of base in each of the warp's rows, whose tokens the lanes hold.
-            const int32_t own_token = EDGE && lane < left ? rows[row] : 0;
-            auto token_at = [&](int r) { return int64_t(__shfl_sync(0xffffffffu, own_token, r)); };
+            // EDGE: a lane's column of base in each of the warp's rows, whose places the lanes hold.  Where there is no
+            // such row or column, the first row's last column: loads without a branch or a predicate to set up.
+            const int64_t own_token = EDGE && left > 0 ? rows[w * 32 + (lane < left ? lane : 0)] : 0;
+            const int64_t own_base = own_token * g.ld_base, own_out = own_token * g.ld_out;
             auto old_value = [&](int r, int j) {
-                const T *p = static_cast<const T *>(g.base) + token_at(r) * g.ld_base + j;
-                return g.base && r < left && j < n && TR_LOAD_OK(sb, p, int(sizeof(T))) ? *p : T(0.0f);
+                const T *p = static_cast<const T *>(g.base) + __shfl_sync(0xffffffffu, own_base, r) + (j < n ? j : n - 1);
+                return g.base && left > 0 && TR_LOAD_OK(sb, p, int(sizeof(T))) ? *p : T(0.0f);
             };
             [[maybe_unused]] T old[EDGE ? 32 : 1];
             if constexpr (EDGE) {
 #pragma unroll
-                for (int r = 0; r < 32; ++r) old[r] = old_value(r, group < tiles ? j_first + group * kColumns + lane : n);
+                for (int r = 0; r < 32; ++r) old[r] = old_value(r, j_first + group * kColumns + lane);
             }
             if (group < S::kHalves) {
                 const float scale = g.scale ? g.scale[at.x] : 1.0f;
@@ -515,7 +519,7 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
                             }
                         }
                     }
-                    meet(2);  // every CTA has what it needs of the others: the region is free
+                    if constexpr (!S::kApart) meet(2);  // every CTA has what it needs of the others: the region is free
                 }
                 // The terms of the inner values, 8 to a 16-byte chunk of a row in the 128-byte swizzle: hi + lo (+ a
                 // third) stand for 16 (24) significant bits, in products with b that are exact in 32 bits.  An
@@ -537,7 +541,7 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
                             word[k / 2] = *reinterpret_cast<const uint32_t *>(&two);
                         }
                         const int col = term * RP + c0 + c;
-                        *reinterpret_cast<uint4 *>(region + col / 64 * kTileX + row * 128 + ((col % 64 * 2) ^ ((row & 7) << 4))) =
+                        *reinterpret_cast<uint4 *>(region + S::kTermsAt + col / 64 * kTileX + row * 128 + ((col % 64 * 2) ^ ((row & 7) << 4))) =
                             make_uint4(word[0], word[1], word[2], word[3]);
                     }
                 }
@@ -623,11 +627,14 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
                         for (int r = 0; r < 32; ++r)
                             sums[r] = reinterpret_cast<const float *>(staging)[(r * 8 + ((lane >> 2) ^ (r & 7))) * 4 + (lane & 3)] + to_f32(old[r]);
 #pragma unroll
-                        for (int r = 0; r < 32; ++r) old[r] = old_value(r, j_next);
+                        for (int r = 0; r < 32; r += 8) {
 #pragma unroll
-                        for (int r = 0; r < 32; ++r) {
-                            T *o = static_cast<T *>(g.out) + token_at(r) * g.ld_out + j;
-                            if (r < left && j < n && TR_STORE_OK(so, o, int(sizeof(T)))) put_value(o, sums[r]);
+                            for (int k = r; k < r + 8; ++k) old[k] = old_value(k, j_next);
+#pragma unroll
+                            for (int k = r; k < r + 8; ++k) {
+                                T *o = static_cast<T *>(g.out) + __shfl_sync(0xffffffffu, own_out, k) + j;
+                                if (k < left && j < n && TR_STORE_OK(so, o, int(sizeof(T)))) put_value(o, sums[k]);
+                            }
                         }
                         __syncwarp();
                     }
