@@ -92,7 +92,8 @@ def check(p, w, out, got, base="base"):
 CASES = [(1, 1, 8, 8, 8), (1, 3, 1, 1, 1), (2, 1, 64, 128, 16), (5, 4, 100, 77, 5), (17, 3, 1111, 129, 12), (64, 48, 520, 300, 16),
          (128, 1, 512, 256, 32), (129, 2, 513, 257, 64), (300, 5, 1000, 1000, 128), (200, 2, 4096, 96, 100), (77, 9, 64, 2049, 33),
          (1000, 3, 264, 520, 8), (260, 1, 8192, 24, 127), (400, 30, 136, 4096, 24), (32, 1, 300, 200, 16), (33, 1, 300, 200, 16), (2048, 90, 72, 136, 16),
-         (2049, 90, 72, 136, 16), (2300, 2, 1032, 264, 64), (20000, 3, 40, 72, 32)]
+         (2049, 90, 72, 136, 16), (2300, 2, 1032, 264, 64), (20000, 3, 40, 72, 32), (64, 2, 520, 301, 12), (65, 2, 300, 200, 16),
+         (32, 1, 300, 200, 17), (64, 2, 300, 200, 17), (400, 3, 2100, 1153, 40)]
 
 
 @pytest.mark.parametrize("out", ["bf16", "f32"])
@@ -200,6 +201,27 @@ def test_other_stream_and_two_graphs():
         torch.cuda.synchronize()
         for a, b in zip(out, eager):
             assert torch.equal(a, b)
+
+
+def test_two_streams_at_once():
+    """Calls that run side by side: each stream's answers are those of the same calls one after another."""
+    import torch
+    jobs = [problem(tokens, 6, 1032, 1544, rank, seed)[0] for tokens, rank, seed in ((40, 16, 1), (700, 64, 2), (2300, 32, 3), (90, 128, 4))]
+
+    def all_of(streams):
+        outs = []
+        for turn in range(4):
+            for i, p in enumerate(jobs):
+                st = streams[(i + turn) % len(streams)]
+                with torch.cuda.stream(st):
+                    outs.append(B.adapters(p["x"], p["a"], p["b"], p["plan"], scale=p["scale"], base=p["base"]))
+        torch.cuda.synchronize()
+        return outs
+
+    torch.cuda.synchronize()
+    alone = all_of([torch.cuda.current_stream()])
+    for a, b in zip(alone, all_of([torch.cuda.Stream(), torch.cuda.Stream(), torch.cuda.Stream()])):
+        assert torch.equal(a, b)
 
 
 def test_refusals():
