@@ -387,7 +387,66 @@ __global__ void __launch_bounds__(1024, 1) k_rmsnorm_ring(const Rms a, int stage
     }
 }
 
-// Rows that neither holds: one to a block, in two walks, one value to an access.
+// Longer rows on 16-byte boundaries: one to a block, in two walks, the second of which finds h in L2.
+constexpr int kWideThreads = 512;
+template <typename T>
+__global__ void __launch_bounds__(kWideThreads, 3) k_rmsnorm_wide(const Rms a) {
+    pdl_prologue();
+    constexpr int V = 16 / int(sizeof(T));
+    __shared__ float slots[2][32];
+    const RmsSides s = sides_of<T>(a);
+    const int64_t first = int64_t(threadIdx.x & ~31) * V, step = kWideThreads * V;  // columns of the warp, the lane's among them
+    const int own = (threadIdx.x & 31) * V;
+    int turn = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+        const T *x = static_cast<const T *>(a.x) + row * a.ld_x;
+        const T *r = static_cast<const T *>(a.residual) + row * a.ld_residual;
+        T *h = static_cast<T *>(a.h) + row * a.ld_h;
+        T *y = static_cast<T *>(a.y) + row * a.ld_y;
+        float sum[1] = {0.0f};
+#pragma unroll 2
+        for (int64_t c = first; c < a.cols; c += step) {
+            const int64_t lo = c + own;
+            Pack<T, V> p = load_chunk<T, V, false>(x, lo, a.cols, s.x);
+            if (a.residual) {
+                const Pack<T, V> o = load_chunk<T, V, false>(r, lo, a.cols, s.res);
+                float v[V];
+#pragma unroll
+                for (int q = 0; q < V; ++q) v[q] = p.get(q) + o.get(q);
+                p.round(v);
+                if (lo < a.cols) store_chunk<T, V, false>(h, lo, a.cols, p, s.h);
+            }
+#pragma unroll
+            for (int q = 0; q < V; ++q) sum[0] = fmaf(p.get(q), p.get(q), sum[0]);
+        }
+        group_sum<kWideThreads, 1>(sum, slots[turn]);
+        const float rstd = __frsqrt_rn(fmaf(sum[0], a.inv_cols, a.eps));
+        if (threadIdx.x == 0 && a.rstd && TR_STORE_OK(s.rstd, a.rstd + row, 4)) a.rstd[row] = rstd;
+        const T *from = a.residual ? h : x;  // this thread's own values
+#pragma unroll 2
+        for (int64_t c = first; c < a.cols; c += step) {
+            const int64_t lo = c + own;
+            float v[V], w[V], n[1][V];
+            const Pack<T, V> p = load_chunk<T, V, false>(from, lo, a.cols, a.residual ? s.h : s.x);
+#pragma unroll
+            for (int q = 0; q < V; ++q) {
+                v[q] = p.get(q);
+                w[q] = 0.0f;
+            }
+            if (lo < a.cols) load_weights<V>(a.gamma, a.w_bf16, lo, w, s.w);
+            normed<V>(n[0], v, rstd, w);
+            if (a.y && lo < a.cols) {
+                Pack<T, V> o;
+                o.round(n[0]);
+                store_chunk<T, V, false>(y, lo, a.cols, o, s.y);
+            }
+            const int at[1] = {int(lo)};
+            if (a.q) quantize_chunks<V, 1>(a, row, at, n, s);
+        }
+    }
+}
+
+// Rows that none of them takes: one to a block, in two walks, one value to an access.
 template <typename T>
 __global__ void __launch_bounds__(1024) k_rmsnorm_any(const Rms a) {
     pdl_prologue();
@@ -700,7 +759,10 @@ cudaError_t launch_rows(const Rms &a, cudaStream_t stream) {
     const cudaError_t e = launch_ring<T>(a, vec, stream);
     if (e != cudaErrorNotSupported) return e;
     const int64_t most = int64_t(1) << 30;
-    return launch_pdl(k_rmsnorm_any<T>, dim3(unsigned(a.rows < most ? a.rows : most)), dim3(1024), 0, stream, a);
+    const dim3 grid(unsigned(a.rows < most ? a.rows : most));
+    if (vec && a.cols <= int64_t(1) << 30 && (reinterpret_cast<uintptr_t>(a.gamma) & 15u) == 0)  // columns in 32 bits
+        return launch_pdl(k_rmsnorm_wide<T>, grid, dim3(kWideThreads), 0, stream, a);
+    return launch_pdl(k_rmsnorm_any<T>, grid, dim3(1024), 0, stream, a);
 }
 
 template <typename T>
