@@ -1,5 +1,17 @@
 // Low-rank adapters of many requests at once: out[i] = base[i] + B_g (scale_g A_g x_i) for
 // each token i with its own adapter g.
+//
+// Bound by memory, 2 R (k + n) operations to 2 k + 4 n bytes of a token: x, base and out once, each adapter in use once.
+// A plan, made once for a batch, puts the tokens in the order of their adapters and cuts them into tiles of up to 128; a
+// cluster of CTAs works on a tile, contracts a part of k and makes a part of the columns each, and the inner values, which
+// all of them need, go through distributed shared memory, never through memory.  They are kept as two bf16 terms (three
+// for fp32 outputs), so that the second product has no rounding that the output does not have.
+//   many tokens   k_adapters, tensor cores fed by TMA: 8192 tokens of 8 adapters, 8192 x 8192 rank 16, 64 and 128 70, 76
+//                 and 90 us, 5.8, 5.5 and 4.8 TB/s (60, 62 and 64 at the copy rate); fp32 outputs, rank 64, 143 (102)
+//   few tokens    k_adapters_few, matrix instructions of a warp straight from memory: bound by latency, three reads that
+//                 wait for one another (plan, x and a, b); one token rank 16 and 64 7.1 and 12.9 us, 64 of 48 adapters
+//                 15.5 and 36.4 (4.2 and 15.3 at the copy rate)
+// Two launches a call at the most; nothing depends on the order in which blocks run.
 #include <type_traits>
 
 #include "adapter_plan.cuh"
@@ -152,6 +164,7 @@ constexpr int kGroups = 3;              // of four warps that take sums out of t
 constexpr int kThreads = 128 + 128 * kGroups;
 constexpr int kTileX = 128 * 128;       // bytes of 128 rows x 64 values
 constexpr int kColumns = 128;           // of the output, worked on together
+constexpr int kBox = 32;                // neighbouring tokens' rows to a load
 // Word c (a multiple of 4) of a row of inner values in shared memory: chunks of 16 bytes in an order that 8
 // rows' accesses to the same chunk do not share a bank.
 template <int RP>
@@ -236,9 +249,9 @@ __device__ __forceinline__ void copy_rows(const Adapt &g, const int32_t *rows, i
 // EDGE: rows of base and out that are off 16-byte boundaries or end off them.
 template <int RP, typename T, bool EDGE>
 __global__ void __launch_bounds__(kThreads, 1)
-k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_rows,
+k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_x32, const __grid_constant__ CUtensorMap map_rows,
            const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-           const __grid_constant__ CUtensorMap map_base, const __grid_constant__ CUtensorMap map_base_rows,
+           const __grid_constant__ CUtensorMap map_base, const __grid_constant__ CUtensorMap map_base32, const __grid_constant__ CUtensorMap map_base_rows,
            const __grid_constant__ Adapt g) {
     constexpr int TERMS = sizeof(T) == 2 ? 2 : 3;
     using S = Shape<RP, TERMS>;
@@ -307,53 +320,76 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
     } else {
         const int first = int(int64_t(g.chunks) * rank / g.split), chunks = int(int64_t(g.chunks) * (rank + 1) / g.split) - first;
         const int tiles = int(last_tile - first_tile);
-        // Tokens that lie side by side are one box, others four rows to a load (the last one's row fills up).
+        // A tile's tokens that all lie side by side are one box, else 32 at a time are, else they go four rows to a load (the
+        // last one's row fills up).  30 prompts of 8 adapters in turn, 8192 tokens, 8192 x 8192 rank 64: 246 us without boxes
+        // of 32, 158 with them and nothing else (and one prompt to an adapter 77 us with a tile's box, 95 in boxes of 32).
         const bool together = rows[count - 1] - rows[0] == count - 1;
-        const int fours = (count + 3) / 4;
-        auto load_rows = [&](uint8_t *dst, const CUtensorMap *box, const CUtensorMap *four, uint64_t *bar, int32_t c) {
+        uint32_t boxes = 0, rows_bytes = kTileX;  // of the warps that load
+        if (!together && (warp == 0 || warp == 2)) {
+            rows_bytes = 0;
+            for (int r = 0; r < count; r += kBox) {
+                const int last = (r + kBox < count ? r + kBox : count) - 1;
+                const bool box = rows[last] - rows[r] == last - r;
+                if (box) boxes |= 1u << (r / kBox);
+                rows_bytes += box ? kBox * 128 : (last - r + 4) / 4 * 512;
+            }
+        }
+        auto load_rows = [&](uint8_t *dst, const CUtensorMap *all, const CUtensorMap *box, const CUtensorMap *four, uint64_t *bar, int32_t c) {
             if (together) {
-                ptx::tma_load_2d(dst, box, bar, c, rows[0]);
+                ptx::tma_load_2d(dst, all, bar, c, rows[0]);
                 return;
             }
-            for (int q = 0; q < fours; ++q) {
-                const int last = count - 1, r = 4 * q;
-                ptx::tma_gather4(dst + q * 512, four, bar, c, rows[r], rows[r + 1 < last ? r + 1 : last],
-                                 rows[r + 2 < last ? r + 2 : last], rows[r + 3 < last ? r + 3 : last]);
+            for (int r0 = 0; r0 < count; r0 += kBox) {
+                if (boxes >> (r0 / kBox) & 1) {
+                    ptx::tma_load_2d(dst + r0 * 128, box, bar, c, rows[r0]);
+                    continue;
+                }
+                const int last = (r0 + kBox < count ? r0 + kBox : count) - 1;
+                for (int r = r0; r <= last; r += 4)
+                    ptx::tma_gather4(dst + r * 128, four, bar, c, rows[r], rows[r + 1 < last ? r + 1 : last],
+                                     rows[r + 2 < last ? r + 2 : last], rows[r + 3 < last ? r + 3 : last]);
             }
         };
-        const uint32_t rows_bytes = together ? kTileX : fours * 512;
         constexpr int kPiece = 128 / int(sizeof(T)), kPieces = kColumns / kPiece;  // columns of a piece of base; pieces of a tile
         if (warp == 0) {
-            if (lane == 0) {
-                int c = 0, i = 0;
-                for (; c < chunks; ++c) {
-                    const int s = c % S::kStagesX;
-                    if (c >= S::kStagesX) ok = ptx::mbar_wait_bounded(empty_x + s, (c / S::kStagesX - 1) & 1);
-                    if (!ok) break;
-                    uint8_t *dst = stages + s * S::kStageBytes;
-                    const int32_t k0 = (first + c) * 64;
+            // The whole warp waits and one elected lane issues, here and below: the 30 prompts above take 118 us, 137 with
+            // these copies inside `lane == 0`, 131 with those of base there.
+            const bool leader = ptx::elect_one();
+            int c = 0, i = 0;
+            for (; c < chunks; ++c) {
+                const int s = c % S::kStagesX;
+                if (c >= S::kStagesX) ok = ptx::mbar_wait_bounded(empty_x + s, (c / S::kStagesX - 1) & 1);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                uint8_t *dst = stages + s * S::kStageBytes;
+                const int32_t k0 = (first + c) * 64;
+                if (leader) {
                     ptx::mbar_arrive_expect_tx(full_x + s, RP * 128 + rows_bytes);
                     ptx::tma_load_3d(dst + kTileX, &map_a, full_x + s, k0, 0, at.x);
-                    load_rows(dst, &map_x, &map_rows, full_x + s, k0);
+                    load_rows(dst, &map_x, &map_x32, &map_rows, full_x + s, k0);
                 }
-                // Nothing may arrive after the block has gone, nor into memory that is used for something else.
-                if (!leave_ring<S::kStagesX>(
-                        c, [&](int s, uint32_t parity) { return ptx::mbar_wait_bounded(empty_x + s, parity); },
-                        [&](int s, uint32_t parity) { ptx::mbar_wait_bounded(full_x + s, parity); }))
-                    ok = false;
-                for (; i < tiles && ok; ++i) {
-                    const int s = i % S::kStages;
-                    if (i >= S::kStages) ok = ptx::mbar_wait_bounded(empty + s, (i / S::kStages - 1) & 1);
-                    if (!ok) break;
+            }
+            // Nothing may arrive after the block has gone, nor into memory that is used for something else.
+            if (!leave_ring<S::kStagesX>(
+                    c, [&](int s, uint32_t parity) { return ptx::mbar_wait_bounded(empty_x + s, parity); },
+                    [&](int s, uint32_t parity) { ptx::mbar_wait_bounded(full_x + s, parity); }))
+                ok = false;
+            ok = __all_sync(0xffffffffu, ok);
+            for (; i < tiles && ok; ++i) {
+                const int s = i % S::kStages;
+                if (i >= S::kStages) ok = ptx::mbar_wait_bounded(empty + s, (i / S::kStages - 1) & 1);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (leader) {
                     ptx::mbar_arrive_expect_tx(full + s, (RP + 63) / 64 * kTileX);
                     for (int k = 0; k < RP; k += 64)
                         ptx::tma_load_3d(stages + s * S::kStageBytes + k / 64 * kTileX, &map_b, full + s, k, int32_t((first_tile + i) * kColumns), at.x);
                 }
-                if (!leave_ring<S::kStages>(
-                        i, [&](int s, uint32_t parity) { return ptx::mbar_wait_bounded(empty + s, parity); },
-                        [&](int s, uint32_t parity) { ptx::mbar_wait_bounded(full + s, parity); }))
-                    ok = false;
             }
+            if (!leave_ring<S::kStages>(
+                    i, [&](int s, uint32_t parity) { return ptx::mbar_wait_bounded(empty + s, parity); },
+                    [&](int s, uint32_t parity) { ptx::mbar_wait_bounded(full + s, parity); }))
+                ok = false;
         } else if (warp == 1) {
             const bool leader = ptx::elect_one();
             const uint32_t idesc_a = ptx::bf16_idesc(128, RP), idesc_b = ptx::bf16_idesc(128, kColumns);
@@ -399,19 +435,22 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
                 ptx::mbar_wait_bounded(&drained, 0);
             }
         } else if (warp < 4) {
-            const int pieces = EDGE || warp != 2 || lane != 0 ? 0 : tiles * kPieces;
+            const bool leader = ptx::elect_one();
+            const int pieces = EDGE || warp != 2 ? 0 : tiles * kPieces;
             if (pieces && chunks) ok = ptx::mbar_wait_bounded(&inner_full, 0);  // the slots were stages
-            for (int p = 0; p < pieces && ok; ++p) {
+            for (int p = 0; p < pieces; ++p) {
                 const int i = p / kPieces, mine = i / kGroups * kPieces + p % kPieces;  // of the group's pieces
                 const int slot = i % kGroups * S::kPer + mine % S::kPer;
-                if (mine >= S::kPer) ok = ptx::mbar_wait_bounded(base_empty + slot, (mine / S::kPer - 1) & 1);
+                if (ok && mine >= S::kPer) ok = ptx::mbar_wait_bounded(base_empty + slot, (mine / S::kPer - 1) & 1);
+                ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
+                if (!leader) continue;
                 if (!g.base) {
                     ptx::mbar_arrive(base_full + slot);
                     continue;
                 }
                 ptx::mbar_arrive_expect_tx(base_full + slot, rows_bytes);
-                load_rows(slots + slot * kTileX, &map_base, &map_base_rows, base_full + slot, int32_t(first_tile) * kColumns + p * kPiece);
+                load_rows(slots + slot * kTileX, &map_base, &map_base32, &map_base_rows, base_full + slot, int32_t(first_tile) * kColumns + p * kPiece);
             }
             if (!ok)  // no load may land after the block has gone
                 for (int i = 0; i < S::kSlots; ++i) {
@@ -549,9 +588,6 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(&inner_ready);
             }
-            int32_t token[8];  // of the rows that this lane stores
-#pragma unroll
-            for (int l = 0; l < 8; ++l) token[l] = l * 4 + lane / 8 < left ? rows[w * 32 + l * 4 + lane / 8] : 0;
             for (int i = group; i < tiles; i += kGroups) {
                 if (ok) ok = ptx::mbar_wait_bounded(sums_full + group, (i / kGroups) & 1);
                 __syncwarp();
@@ -567,21 +603,22 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
                         if (left > 0) {
                             // Every step's accesses are under way before the first is used.
                             const uint32_t piece = ptx::smem_addr(slots + slot * kTileX), own = piece + row * 128;
-                            uint4 was[8];
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) was[k] = g.base ? ptx::load_shared_16(own + ((k ^ (row & 7)) << 4)) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
                             for (int c = 0; c < kPiece; c += 32) {
+                                uint4 old[32 / V];
+#pragma unroll
+                                for (int k = 0; k < 32 / V; ++k)
+                                    old[k] = g.base ? ptx::load_shared_16(own + (((c / V + k) ^ (row & 7)) << 4)) : make_uint4(0u, 0u, 0u, 0u);
                                 float sums[32];
                                 ptx::tmem_load32(sums, from + p * kPiece + c);
                                 ptx::tmem_wait_load32(sums);
 #pragma unroll
                                 for (int k = 0; k < 32; k += V) {
                                     const int at = (c + k) / V;
-                                    const Pack<T, V> old = *reinterpret_cast<const Pack<T, V> *>(&was[at]);
+                                    const Pack<T, V> b = *reinterpret_cast<const Pack<T, V> *>(&old[k / V]);
                                     float f[V];
 #pragma unroll
-                                    for (int q = 0; q < V; ++q) f[q] = sums[k + q] + old.get(q);
+                                    for (int q = 0; q < V; ++q) f[q] = sums[k + q] + b.get(q);
                                     Pack<T, V> o;
                                     o.round(f);
                                     ptx::store_shared_16(own + ((at ^ (row & 7)) << 4), *reinterpret_cast<const uint4 *>(&o));
@@ -589,9 +626,12 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
                             }
                             __syncwarp();
                             const int j = j_first + i * kColumns + p * kPiece + lane % 8 * V;
+                            uint4 was[8];
+                            int32_t token[8];  // read here: registers are short while the sums are there
 #pragma unroll
                             for (int l = 0; l < 8; ++l) {
                                 const int r = l * 4 + lane / 8;
+                                token[l] = rows[w * 32 + r];
                                 was[l] = ptx::load_shared_16(piece + (w * 32 + r) * 128 + ((lane ^ r) % 8 << 4));
                             }
 #pragma unroll
@@ -975,7 +1015,7 @@ cudaError_t launch_few_rank(const Few &g, bool f32, bool edge, int64_t tiles, cu
 }
 
 template <int RP, typename T, bool EDGE>
-cudaError_t launch_one(const CUtensorMap (&maps)[6], Adapt g, int64_t tiles, cudaStream_t stream) {
+cudaError_t launch_one(const CUtensorMap (&maps)[8], Adapt g, int64_t tiles, cudaStream_t stream) {
     using S = Shape<RP, sizeof(T) == 2 ? 2 : 3>;
     auto kern = k_adapters<RP, T, EDGE>;
     const cudaError_t e = allow_shared<k_adapters<RP, T, EDGE>>(S::kSmem);
@@ -987,11 +1027,12 @@ cudaError_t launch_one(const CUtensorMap (&maps)[6], Adapt g, int64_t tiles, cud
     const int64_t likely = least + (tiles < g.adapters + 1 ? tiles : g.adapters + 1) / 2;
     g.split = 1;
     while (g.split < 8 && likely * g.split * 2 <= resident && g.chunks >= g.split * 4) g.split *= 2;
-    return launch_clusters(kern, tiles * g.split, kThreads, S::kSmem, g.split, stream, maps[0], maps[1], maps[2], maps[3], maps[4], maps[5], g);
+    return launch_clusters(kern, tiles * g.split, kThreads, S::kSmem, g.split, stream, maps[0], maps[1], maps[2], maps[3], maps[4], maps[5], maps[6],
+                           maps[7], g);
 }
 
 template <int RP>
-cudaError_t launch_rank(const CUtensorMap (&maps)[6], const Adapt &g, bool f32, bool edge, int64_t tiles, cudaStream_t stream) {
+cudaError_t launch_rank(const CUtensorMap (&maps)[8], const Adapt &g, bool f32, bool edge, int64_t tiles, cudaStream_t stream) {
     if (f32) return edge ? launch_one<RP, float, true>(maps, g, tiles, stream) : launch_one<RP, float, false>(maps, g, tiles, stream);
     return edge ? launch_one<RP, __nv_bfloat16, true>(maps, g, tiles, stream) : launch_one<RP, __nv_bfloat16, false>(maps, g, tiles, stream);
 }
@@ -1042,12 +1083,14 @@ cudaError_t launch_adapters(const tr_adapters_args &p, const char **why) {
         g.beside = 1;
     }
     const int64_t large = g.beside ? plan_large_tiles(p.tokens, p.adapters) : tiles;
-    CUtensorMap maps[6] = {};
-    if (!none && (!encode(maps, p.x, 2, 0, p.tokens, p.k, p.ld_x, 0, 128) || !encode(maps + 1, p.x, 2, 0, p.tokens, p.k, p.ld_x, 0, 1) ||
-                  !encode(maps + 2, p.a, 2, p.adapters, p.rank, p.k, p.ld_a, p.stride_a, rp) ||
-                  !encode(maps + 3, p.b, 2, p.adapters, p.n, p.rank, p.ld_b, p.stride_b, kColumns) ||
-                  (p.base && !edge && (!encode(maps + 4, p.base, es, 0, p.tokens, p.n, p.ld_base, 0, 128) ||
-                                       !encode(maps + 5, p.base, es, 0, p.tokens, p.n, p.ld_base, 0, 1))))) {
+    CUtensorMap maps[8] = {};
+    auto rows_maps = [&](CUtensorMap *m, const void *rows, int bytes, int64_t cols, int64_t ld) {
+        return encode(m, rows, bytes, 0, p.tokens, cols, ld, 0, 128) && encode(m + 1, rows, bytes, 0, p.tokens, cols, ld, 0, kBox) &&
+               encode(m + 2, rows, bytes, 0, p.tokens, cols, ld, 0, 1);
+    };
+    if (!none && (!rows_maps(maps, p.x, 2, p.k, p.ld_x) || !encode(maps + 3, p.a, 2, p.adapters, p.rank, p.k, p.ld_a, p.stride_a, rp) ||
+                  !encode(maps + 4, p.b, 2, p.adapters, p.n, p.rank, p.ld_b, p.stride_b, kColumns) ||
+                  (p.base && !edge && !rows_maps(maps + 5, p.base, es, p.n, p.ld_base)))) {
         *why = "adapters: cuTensorMapEncodeTiled rejected the operands (a pitch of 2^40 bytes or more)";
         return cudaErrorInvalidValue;
     }

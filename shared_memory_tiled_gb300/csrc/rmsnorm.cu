@@ -2,7 +2,14 @@
 // y = h * rstd * gamma with rstd = 1 / sqrt(sum(h^2) / n + eps), as rows of h's type and in
 // 8 bits with a scale for each block of 128, by rows and transposed.
 //
-// Bound by memory: x and residual are read once, h, y, q and qt written once.
+// Bound by memory: x and residual are read once, h, y, q and qt written once.  The statistics are held in 32 bits, y is
+// rounded once, and the 8-bit values come from y in 32 bits, not from its rounded form.  A row stays on the chip between
+// its two walks (registers, or shared memory that bulk copies fill rows ahead); the transposed 8-bit output, whose blocks
+// of 128 rows need every row's rstd, takes a second launch that reads h once more.  Device time, and the share of the
+// copy rate on the bytes above:
+//   1 x 8192 bf16 3 us; 16384 x 8192 bf16 157 us (101%), without a residual 87 (91%); 12289 x 7919 fp32 229-240 (96-100%)
+//   8 bits, 16384 x 8192 bf16: rows 146 us (95%), both ways 220 (73%: h's second read is 20% more bytes)
+//   4000 x 20000 bf16 121 us (78%), rows of 20001 values 486 (19%)
 #include <type_traits>
 
 #include "fp8.cuh"
@@ -387,7 +394,8 @@ __global__ void __launch_bounds__(1024, 1) k_rmsnorm_ring(const Rms a, int stage
     }
 }
 
-// Longer rows on 16-byte boundaries: one to a block, in two walks, the second of which finds h in L2.
+// Longer rows on 16-byte boundaries: one to a block, in two walks, the second of which finds h in L2.  4000 x 20000 bf16
+// 121 us, 468 with k_rmsnorm_any; 4096 x 16384 fp32 178 (89% of the copy rate).
 constexpr int kWideThreads = 512;
 template <typename T>
 __global__ void __launch_bounds__(kWideThreads, 3) k_rmsnorm_wide(const Rms a) {

@@ -112,6 +112,16 @@ def test_adapters(case, out):
     assert torch.equal(inside, got)
 
 
+@pytest.mark.parametrize("n", [264, 265])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_prompts_in_turn(out, n):
+    """Adapters whose requests do not lie side by side: tiles that begin, go on and end inside runs of tokens."""
+    runs = [50, 94, 222, 37, 31, 128, 300, 1, 33, 2, 64, 97, 160, 5]
+    for k, order in ((72, [0, 1] * 7), (1040, [2, 0, 1, 0, -1, 0, 1, 2, 0, 0, 2, 1, 0, 2])):
+        p, w = problem(sum(runs), 3, k, n, 24, len(runs) + k, out, index=np.repeat(order, runs))
+        check(p, w, out, B.adapters(p["x"], p["a"], p["b"], p["plan"], scale=p["scale"], base=p["base"]))
+
+
 @pytest.mark.parametrize("out", ["bf16", "f32"])
 def test_without_base_and_scale(out):
     import torch
