@@ -7,10 +7,10 @@
 // all of them need, go through distributed shared memory, never through memory.  They are kept as two bf16 terms (three
 // for fp32 outputs), so that the second product has no rounding that the output does not have.
 //   many tokens   k_adapters, tensor cores fed by TMA: 8192 tokens of 8 adapters, 8192 x 8192 rank 16, 64 and 128 70, 76
-//                 and 90 us, 5.8, 5.5 and 4.8 TB/s (60, 62 and 64 at the copy rate); fp32 outputs, rank 64, 143 (102)
+//                 and 85 us, 5.8, 5.5 and 5.1 TB/s (60, 62 and 64 at the copy rate); fp32 outputs, rank 64, 144 (102)
 //   few tokens    k_adapters_few, matrix instructions of a warp straight from memory: bound by latency, three reads that
-//                 wait for one another (plan, x and a, b); one token rank 16 and 64 7.1 and 12.9 us, 64 of 48 adapters
-//                 15.5 and 36.4 (4.2 and 15.3 at the copy rate)
+//                 wait for one another (plan, x and a, b); one token rank 16 and 64 7.0 and 12.9 us, 64 of 48 adapters
+//                 15.5 and 36.3 (4.2 and 15.3 at the copy rate)
 // Two launches a call at the most; nothing depends on the order in which blocks run.
 #include <type_traits>
 
@@ -322,7 +322,7 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
         const int tiles = int(last_tile - first_tile);
         // A tile's tokens that all lie side by side are one box, else 32 at a time are, else they go four rows to a load (the
         // last one's row fills up).  30 prompts of 8 adapters in turn, 8192 tokens, 8192 x 8192 rank 64: 246 us without boxes
-        // of 32, 158 with them and nothing else (and one prompt to an adapter 77 us with a tile's box, 95 in boxes of 32).
+        // of 32, 158 with them and nothing else (and one prompt to an adapter 76 us with a tile's box, 85 in boxes of 32).
         const bool together = rows[count - 1] - rows[0] == count - 1;
         uint32_t boxes = 0, rows_bytes = kTileX;  // of the warps that load
         if (!together && (warp == 0 || warp == 2)) {

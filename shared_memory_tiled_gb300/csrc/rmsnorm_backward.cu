@@ -3,7 +3,12 @@
 //
 //   dx = rstd * (g - u * sum(g u)/n) + dresidual,  dgamma = sum_rows dy u
 //
-// Bound by memory: one read of dy, h and dresidual, one write of dx.
+// Bound by memory: one read of dy, h and dresidual, one write of dx.  A block walks its rows once, through a ring that
+// bulk copies fill, keeps a row's g and u in registers between the row's sum and dx, and holds its columns' part of dgamma
+// in registers throughout; a second launch adds the blocks' parts in a fixed order.  Device time, and the share of the
+// copy rate: 256 x 1024 bf16 7.0 us; 16384 x 8192 bf16 161 us (98%), 12289 x 7919 fp32 225 (102%), 65536 x 1024 bf16 122
+// (65%), 4096 x 16384 bf16 186 (43%).  Rows that the ring does not hold take three launches, and dy and h are read twice:
+// 4096 x 16384 fp32 329 us (48%), 4000 x 20000 bf16 224 (42%).
 #include "launch.cuh"
 #include "ptx.cuh"
 #include "row_chunk.cuh"
@@ -26,7 +31,7 @@ struct RmsBwd {
     float *dgamma, *part;
     int64_t rows, cols, ld_dy, ld_h, ld_dres, ld_dx;
     int64_t parts, rows_per_part;
-    bool w_bf16;
+    bool w_bf16, w_held;  // w_held: the ring leaves room for the weights
 };
 
 // Sum over the block, in every thread; `slot` holds a word for each of 32 warps.
@@ -45,7 +50,8 @@ __device__ __forceinline__ float block_sum(float v, float *slot) {
 // columns in 16-byte chunks, every row on a 16-byte boundary; else one column at a time, neighbouring
 // threads on neighbouring columns.  KEEP (up to 8192 columns): 512 threads to an SM, with a row's u, g and
 // dresidual in registers between its two walks; else 1024, which read them from the ring again, and the
-// weights from shared memory.
+// weights from shared memory, or from L2 where the rows leave no room for them (4096 x 16384 bf16 186 us, 588 with
+// k_rms_dx and k_rms_columns value by value).
 template <typename T, bool KEEP, bool VEC>
 __global__ void __launch_bounds__(KEEP ? 512 : 1024, 1)
 k_rms_backward(const RmsBwd a, int stages, uint32_t row_bytes) {
@@ -118,13 +124,14 @@ k_rms_backward(const RmsBwd a, int stages, uint32_t row_bytes) {
         dg[k] = make_float2(0.0f, 0.0f);
         if (KEEP) w[KEEP ? k : 0] = make_float2(kept(column(2 * k)), kept(column(2 * k + 1)));
     }
-    if (!KEEP) {
+    if (!KEEP && a.w_held) {
         for (int j = t; j < cols; j += nt) gammas[j] = kept(j);
         __syncthreads();
     }
     auto weights = [&](int k) {
         if (KEEP) return w[KEEP ? k : 0];
         const int j0 = column(2 * k), j1 = column(2 * k + 1);
+        if (!a.w_held) return make_float2(kept(j0), kept(j1));
         return make_float2(j0 < cols ? gammas[j0] : 0.0f, j1 < cols ? gammas[j1] : 0.0f);
     };
     const float inv_cols = 1.0f / float(cols);
@@ -241,8 +248,9 @@ k_rms_backward(const RmsBwd a, int stages, uint32_t row_bytes) {
     }
 }
 
-// dx of one row per block, in two walks along it: rows that the ring does not hold.
-template <typename T>
+// dx of one row per block, in two walks along it: rows that the ring does not hold.  V: values to an access, rows and
+// weights on 16-byte boundaries with more than one (4096 x 16384 fp32 329 us, value by value 570).
+template <typename T, int V>
 __global__ void __launch_bounds__(512) k_rms_dx(const RmsBwd a) {
     pdl_prologue();
     __shared__ float slots[2][16];
@@ -260,29 +268,48 @@ __global__ void __launch_bounds__(512) k_rms_dx(const RmsBwd a) {
         const T *dr = static_cast<const T *>(a.dres) + row * a.ld_dres;
         T *dx = static_cast<T *>(a.dx) + row * a.ld_dx;
         const float rstd = TR_LOAD_OK(sr, a.rstd + row, 4) ? a.rstd[row] : 0.0f;
+        // g and u of the V columns from j on.
+        auto values = [&](int64_t j, float (&g)[V], float (&u)[V]) {
+            const Pack<T, V> pd = load_chunk<T, V, false>(dy, j, a.cols, sd), ph = load_chunk<T, V, false>(h, j, a.cols, sh);
+            if constexpr (V > 1) load_weights<V>(a.gamma, a.w_bf16, j, g, sw);
+            else g[0] = weight(a.gamma, a.w_bf16, j, sw);
+#pragma unroll
+            for (int q = 0; q < V; ++q) {
+                g[q] = pd.get(q) * g[q];
+                u[q] = ph.get(q) * rstd;
+            }
+        };
         float s[1] = {0.0f};
-        for (int64_t j = threadIdx.x; j < a.cols; j += blockDim.x) {
-            if (!TR_LOAD_OK(sd, dy + j, int(sizeof(T))) || !TR_LOAD_OK(sh, h + j, int(sizeof(T)))) continue;
-            s[0] = fmaf(to_f32(dy[j]) * weight(a.gamma, a.w_bf16, j, sw), to_f32(h[j]) * rstd, s[0]);
+#pragma unroll 2
+        for (int64_t j = int64_t(threadIdx.x) * V; j < a.cols; j += int64_t(blockDim.x) * V) {
+            float g[V], u[V];
+            values(j, g, u);
+#pragma unroll
+            for (int q = 0; q < V; ++q) s[0] = fmaf(g[q], u[q], s[0]);
         }
         group_sum<512, 1>(s, slots[turn]);
         const float c = s[0] * inv_cols;
-        for (int64_t j = threadIdx.x; j < a.cols; j += blockDim.x) {
-            if (!TR_LOAD_OK(sd, dy + j, int(sizeof(T))) || !TR_LOAD_OK(sh, h + j, int(sizeof(T)))) continue;
-            const float g = to_f32(dy[j]) * weight(a.gamma, a.w_bf16, j, sw), u = to_f32(h[j]) * rstd;
-            float v = 0.0f;
-            if (a.dres && TR_LOAD_OK(se, dr + j, int(sizeof(T)))) v = to_f32(dr[j]);
-            v = fmaf(rstd, fmaf(-u, c, g), v);
-            if (TR_STORE_OK(so, dx + j, int(sizeof(T)))) put_value(dx + j, v);
+#pragma unroll 2
+        for (int64_t j = int64_t(threadIdx.x) * V; j < a.cols; j += int64_t(blockDim.x) * V) {
+            float g[V], u[V];
+            values(j, g, u);
+            Pack<T, V> pe;
+            pe.clear();
+            if (a.dres) pe = load_chunk<T, V, false>(dr, j, a.cols, se);
+#pragma unroll
+            for (int q = 0; q < V; ++q) g[q] = fmaf(rstd, fmaf(-u[q], c, g[q]), pe.get(q));
+            Pack<T, V> o;
+            o.round(g);
+            store_chunk<T, V, false>(dx, j, a.cols, o, so);
         }
     }
 }
 
-// Column sums of dy*u over one part of the rows: 32 columns by 8 rows of threads.
-template <typename T>
+// Column sums of dy*u over one part of the rows: 32 times V columns by 8 rows of threads.
+template <typename T, int V>
 __global__ void __launch_bounds__(256) k_rms_columns(const RmsBwd a) {
     pdl_prologue();
-    __shared__ float red[8][33];
+    __shared__ float red[8][32 * V + 1];
     [[maybe_unused]] const dbg::Side sd = dbg::side(a.dy, 1, a.rows, a.cols, a.ld_dy, 0, sizeof(T));
     [[maybe_unused]] const dbg::Side sh = dbg::side(a.h, 1, a.rows, a.cols, a.ld_h, 0, sizeof(T));
     [[maybe_unused]] const dbg::Side sp = dbg::side(a.part, 1, a.parts, a.cols, a.cols, 0, 4);
@@ -290,24 +317,29 @@ __global__ void __launch_bounds__(256) k_rms_columns(const RmsBwd a) {
     const int64_t part = blockIdx.y;
     const int64_t r0 = part * a.rows_per_part;
     const int64_t r1 = r0 + a.rows_per_part < a.rows ? r0 + a.rows_per_part : a.rows;
-    for (int64_t c0 = int64_t(blockIdx.x) * 32; c0 < a.cols; c0 += int64_t(gridDim.x) * 32) {
-        const int64_t j = c0 + tx;
-        float s = 0.0f;
+    for (int64_t c0 = int64_t(blockIdx.x) * 32 * V; c0 < a.cols; c0 += int64_t(gridDim.x) * 32 * V) {
+        const int64_t j = c0 + tx * V;
+        float s[V] = {};
         if (j < a.cols)
+#pragma unroll 2
             for (int64_t r = r0 + ty; r < r1; r += 8) {
-                const T *pd = static_cast<const T *>(a.dy) + r * a.ld_dy + j;
-                const T *ph = static_cast<const T *>(a.h) + r * a.ld_h + j;
-                if (!TR_LOAD_OK(sd, pd, int(sizeof(T))) || !TR_LOAD_OK(sh, ph, int(sizeof(T)))) continue;
-                s = fmaf(to_f32(*pd), to_f32(*ph) * a.rstd[r], s);
-            }
-        red[ty][tx] = s;
-        __syncthreads();
-        if (ty == 0 && j < a.cols) {
+                const Pack<T, V> pd = load_chunk<T, V, false>(static_cast<const T *>(a.dy) + r * a.ld_dy, j, a.cols, sd);
+                const Pack<T, V> ph = load_chunk<T, V, false>(static_cast<const T *>(a.h) + r * a.ld_h, j, a.cols, sh);
+                const float rstd = a.rstd[r];
 #pragma unroll
-            for (int i = 1; i < 8; ++i) s += red[i][tx];
-            float *p = a.part + part * a.cols + j;
-            if (TR_STORE_OK(sp, p, 4)) *p = s;
-        }
+                for (int q = 0; q < V; ++q) s[q] = fmaf(pd.get(q), ph.get(q) * rstd, s[q]);
+            }
+#pragma unroll
+        for (int q = 0; q < V; ++q) red[ty][tx * V + q] = s[q];
+        __syncthreads();
+        for (int c = threadIdx.x; c < 32 * V; c += 256)
+            if (c0 + c < a.cols) {
+                float sum = red[0][c];
+#pragma unroll
+                for (int i = 1; i < 8; ++i) sum += red[i][c];
+                float *p = a.part + part * a.cols + c0 + c;
+                if (TR_STORE_OK(sp, p, 4)) *p = sum;
+            }
         __syncthreads();
     }
 }
@@ -364,12 +396,13 @@ cudaError_t launch_ring(RmsBwd a, bool vec, cudaStream_t stream) {
     int threads = 64;
     while (threads * 16 < a.cols) threads *= 2;
     const uint32_t row_bytes = uint32_t((a.cols * int64_t(sizeof(T)) + 30) / 16 * 16), stage_bytes = (a.dres ? 3 : 2) * row_bytes;
-    const uint32_t weights = keep ? 0 : uint32_t(a.cols * 4 + 15) / 16 * 16;
+    uint32_t weights = keep ? 0 : uint32_t(a.cols * 4 + 15) / 16 * 16;
+    if (ring_room(1) < weights + 2 * stage_bytes) weights = 0;  // one block to an SM
+    a.w_held = weights != 0;
     // 512 (1024) threads to an SM, in as many blocks; fewer where rows or the ring want it.
     int64_t per_sm = keep ? 512 / threads : 1;
     const int64_t cap = most_parts(a.rows, a.cols) / sm_count();
     if (per_sm > cap) per_sm = cap < 1 ? 1 : cap;
-    if (ring_room(per_sm) < weights) return cudaErrorNotSupported;
     uint32_t stages = (ring_room(per_sm) - weights) / stage_bytes;
     while (stages < 4 && per_sm > 1) {
         per_sm /= 2;
@@ -401,10 +434,13 @@ cudaError_t launch_typed(RmsBwd a, cudaStream_t stream) {
     a.parts = parts_of(a.rows);
     a.rows_per_part = (a.rows + a.parts - 1) / a.parts;
     const int64_t most = int64_t(1) << 30;
-    e = launch_pdl(k_rms_dx<T>, dim3(unsigned(a.rows < most ? a.rows : most)), dim3(512), 0, stream, a);
-    if (e != cudaSuccess) return e;
-    const int64_t strips = (a.cols + 31) / 32;
-    e = launch_pdl(k_rms_columns<T>, dim3(unsigned(strips < most ? strips : most), unsigned(a.parts)), dim3(256), 0, stream, a);
+    auto run = [&](auto dx, auto columns, int64_t strip) {
+        const cudaError_t err = launch_pdl(dx, dim3(unsigned(a.rows < most ? a.rows : most)), dim3(512), 0, stream, a);
+        const int64_t strips = (a.cols + strip - 1) / strip;
+        return err != cudaSuccess ? err : launch_pdl(columns, dim3(unsigned(strips < most ? strips : most), unsigned(a.parts)), dim3(256), 0, stream, a);
+    };
+    e = vec && (reinterpret_cast<uintptr_t>(a.gamma) & 15u) == 0 ? run(k_rms_dx<T, 16 / es>, k_rms_columns<T, 16 / es>, 32 * 16 / es)
+                                                                : run(k_rms_dx<T, 1>, k_rms_columns<T, 1>, 32);
     return e == cudaSuccess ? launch_join(a, stream) : e;
 }
 
@@ -419,7 +455,7 @@ cudaError_t launch_rmsnorm_backward(const tr_rmsnorm_backward_args &p) {
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(p.stream);
     if (p.rows == 0) return cudaMemsetAsync(p.dgamma, 0, size_t(p.cols) * 4, stream);  // the column sums are empty
     const RmsBwd a{p.dy, p.h, p.gamma, p.rstd, p.dresidual, p.dx, p.dgamma, static_cast<float *>(p.workspace),
-                   p.rows, p.cols, p.ld_dy, p.ld_h, p.ld_dresidual, p.ld_dx, 0, 0, p.w_dtype == TR_DTYPE_BF16};
+                   p.rows, p.cols, p.ld_dy, p.ld_h, p.ld_dresidual, p.ld_dx, 0, 0, p.w_dtype == TR_DTYPE_BF16, true};
     return p.x_dtype == TR_DTYPE_F32 ? launch_typed<float>(a, stream) : launch_typed<__nv_bfloat16>(a, stream);
 }
 
