@@ -1,7 +1,9 @@
 """libtranspose for GB300 (sm_103a): out-of-place matrix transpose staged
 through bank-conflict-free shared-memory tiles, and the operators of a linear
 layer in 8-bit floating point (``binding.quantize_fp8``, ``matmul_fp8``,
-``layernorm``, ``layernorm_backward``; ``train_linear`` runs them together).
+``layernorm``, ``layernorm_backward``, ``rmsnorm``, ``rmsnorm_fp8``,
+``rmsnorm_backward``, and ``adapter_plan`` and ``adapters`` for requests with
+low-rank adapters of their own; ``train_linear`` runs them together).
 
 The compute path is the C-ABI shared library ``libtranspose.so`` built from
 ``csrc/``; ``binding`` marshals arguments into it with ctypes.  Importing this

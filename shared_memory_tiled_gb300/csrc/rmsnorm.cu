@@ -8,7 +8,7 @@
 // of 128 rows need every row's rstd, takes a second launch that reads h once more.  Device time, and the share of the
 // copy rate on the bytes above:
 //   1 x 8192 bf16 3 us; 16384 x 8192 bf16 157 us (101%), without a residual 87 (91%); 12289 x 7919 fp32 229-240 (96-100%)
-//   8 bits, 16384 x 8192 bf16: rows 146 us (95%), both ways 220 (73%: h's second read is 20% more bytes)
+//   8 bits, 16384 x 8192 bf16: rows 146 us (95%), both ways 220 (73%: h's second read is 25% more bytes)
 //   4000 x 20000 bf16 121 us (78%), rows of 20001 values 486 (19%)
 #include <type_traits>
 
