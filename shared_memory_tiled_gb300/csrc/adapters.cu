@@ -352,8 +352,8 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
         };
         constexpr int kPiece = 128 / int(sizeof(T)), kPieces = kColumns / kPiece;  // columns of a piece of base; pieces of a tile
         if (warp == 0) {
-            // The whole warp waits and one elected lane issues, here and below: the 30 prompts above take 118 us, 137 with
-            // these copies inside `lane == 0`, 131 with those of base there.
+            // The whole warp waits and one elected lane issues, here and below: the 30 prompts above took 118 us (116 now),
+            // 137 with these copies inside `lane == 0`, 131 with those of base there.
             const bool leader = ptx::elect_one();
             int c = 0, i = 0;
             for (; c < chunks; ++c) {
