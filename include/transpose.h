@@ -526,7 +526,8 @@ typedef struct tr_adapters_args {
  *     out[i][j] = base[i][j] + sum over r of v[r] * b[g][j][r]
  *
  * and out[i] = base[i] for a token without one.  Sums are held in 32 bits, v in
- * 16 significant bits or more, out is rounded once.  Equal calls give equal bits.  x, a
+ * 16 significant bits or more (24 for fp32 out), out is rounded once.  Infinities and NaN go
+ * where these formulas take them, and stay with their token.  Equal calls give equal bits.  x, a
  * and b are 16-byte aligned, their row pitches and strides multiples of 8 values (else
  * TR_ERR_UNSUPPORTED); tokens is below 2^31, k and n are below 2^30. */
 tr_status tr_adapters(const tr_adapters_args *args);

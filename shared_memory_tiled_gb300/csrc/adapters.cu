@@ -4,8 +4,8 @@
 // Bound by memory, 2 R (k + n) operations to 2 k + 4 n bytes of a token: x, base and out once, each adapter in use once.
 // A plan, made once for a batch, puts the tokens in the order of their adapters and cuts them into tiles of up to 128; a
 // cluster of CTAs works on a tile, contracts a part of k and makes a part of the columns each, and the inner values, which
-// all of them need, go through distributed shared memory, never through memory.  They are kept as two bf16 terms (three
-// for fp32 outputs), so that the second product has no rounding that the output does not have.
+// all of them need, go through distributed shared memory, never through memory.  They are summed in 32 bits and go into the
+// second product as two bf16 terms, 16 significant bits against the output's 8 (three terms for fp32 outputs, 24 bits).
 //   many tokens   k_adapters, tensor cores fed by TMA: 8192 tokens of 8 adapters, 8192 x 8192 rank 16, 64 and 128 70, 76
 //                 and 85 us, 5.8, 5.5 and 5.1 TB/s (60, 62 and 64 at the copy rate); fp32 outputs, rank 64, 144 (102)
 //   few tokens    k_adapters_few, matrix instructions of a warp straight from memory: bound by latency, three reads that
@@ -159,6 +159,39 @@ struct Adapt {
     int32_t which;         // tiles (Which)
     int32_t beside;        // the small ones are another kernel's, just before this one
 };
+
+// The bf16 terms that inner values go into the second product as, two values' in a word each: the leading 8 significant
+// bits, cut off and not rounded, the next 8 (with three terms), and the rest rounded.  Two terms stand for 16 bits and three
+// for all 24, in products with b that are exact in 32 bits.  Cut off, because the terms then have the value's sign and none
+// is larger: with an infinite b each gives the infinity that the value gives (rounded, every second value is followed by a
+// term of the other sign, and the sum is NaN), and a value above bf16's largest does not become infinite.  For the same
+// reason a term is zero only where the value is (2^-133, bf16's least, in its place), and an infinity or NaN is every one.
+// (Rounded terms took 0.2 to 1 us less of a call: 8192 tokens rank 64 76.1 us, with these 76.5.)
+template <int TERMS>
+__device__ __forceinline__ void terms_of(float a, float b, uint32_t (&word)[TERMS]) {
+    float left[2] = {a, b};
+    const uint32_t sign[2] = {__float_as_uint(a) & 0x80000000u, __float_as_uint(b) & 0x80000000u};
+    const uint32_t least[2] = {a != 0.0f ? 0x00010000u : 0u, b != 0.0f ? 0x00010000u : 0u};
+    const bool finite[2] = {fabsf(a) < INFINITY, fabsf(b) < INFINITY};
+#pragma unroll
+    for (int term = 0; term < TERMS; ++term) {
+        uint32_t top[2];
+        if (term + 1 < TERMS) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                top[i] = __float_as_uint(left[i]) & 0xffff0000u;
+                left[i] = finite[i] ? left[i] - __uint_as_float(top[i]) : left[i];
+            }
+        } else {
+            const float2 rounded = __bfloat1622float2(__floats2bfloat162_rn(left[0], left[1]));
+            top[0] = __float_as_uint(rounded.x);
+            top[1] = __float_as_uint(rounded.y);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) top[i] = umax(top[i] & 0x7fffffffu, least[i]) | sign[i];
+        word[term] = __byte_perm(top[0], top[1], 0x7632);
+    }
+}
 
 constexpr int kGroups = 3;              // of four warps that take sums out of tensor memory, each with its own
 constexpr int kThreads = 128 + 128 * kGroups;
@@ -560,28 +593,18 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
                     }
                     if constexpr (!S::kApart) meet(2);  // every CTA has what it needs of the others: the region is free
                 }
-                // The terms of the inner values, 8 to a 16-byte chunk of a row in the 128-byte swizzle: hi + lo (+ a
-                // third) stand for 16 (24) significant bits, in products with b that are exact in 32 bits.  An
-                // infinity is all in the first.
+                // The terms of the inner values, 8 to a 16-byte chunk of a row in the 128-byte swizzle.
 #pragma unroll
                 for (int c = 0; c < W; c += 8) {
-                    float left[8];
+                    uint32_t word[4][TERMS];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) left[k] = c0 + c + k < g.rank ? v[c + k] * scale : 0.0f;
+                    for (int k = 0; k < 8; k += 2)
+                        terms_of<TERMS>(c0 + c + k < g.rank ? v[c + k] * scale : 0.0f, c0 + c + k + 1 < g.rank ? v[c + k + 1] * scale : 0.0f, word[k / 2]);
 #pragma unroll
                     for (int term = 0; term < TERMS; ++term) {
-                        uint32_t word[4];
-#pragma unroll
-                        for (int k = 0; k < 8; k += 2) {
-                            const __nv_bfloat162 two = __floats2bfloat162_rn(left[k], left[k + 1]);
-                            const float2 f = __bfloat1622float2(two);
-                            left[k] = fabsf(f.x) == INFINITY ? 0.0f : left[k] - f.x;
-                            left[k + 1] = fabsf(f.y) == INFINITY ? 0.0f : left[k + 1] - f.y;
-                            word[k / 2] = *reinterpret_cast<const uint32_t *>(&two);
-                        }
                         const int col = term * RP + c0 + c;
                         *reinterpret_cast<uint4 *>(region + S::kTermsAt + col / 64 * kTileX + row * 128 + ((col % 64 * 2) ^ ((row & 7) << 4))) =
-                            make_uint4(word[0], word[1], word[2], word[3]);
+                            make_uint4(word[0][term], word[1][term], word[2][term], word[3][term]);
                     }
                 }
                 ptx::fence_proxy_async_smem();
@@ -895,13 +918,10 @@ __global__ void __launch_bounds__(kFewThreads, 2) k_adapters_few(const Few g) {
 #pragma unroll
                 for (int peer = 0; peer < 8; ++peer)
                     if (peer < g.split) v += f[peer];
-                v = r < g.rank ? v * scale : 0.0f;
+                uint32_t word[TERMS];
+                terms_of<TERMS>(r < g.rank ? v * scale : 0.0f, 0.0f, word);
 #pragma unroll
-                for (int term = 0; term < TERMS; ++term) {  // as above
-                    const __nv_bfloat16 h = __float2bfloat16_rn(v);
-                    v = fabsf(__bfloat162float(h)) == INFINITY ? 0.0f : v - __bfloat162float(h);
-                    terms[term][m][r] = h;
-                }
+                for (int term = 0; term < TERMS; ++term) terms[term][m][r] = __ushort_as_bfloat16(uint16_t(word[term]));
             }
             __syncthreads();
             if (g.split > 1) ptx::cluster_arrive();
