@@ -529,7 +529,11 @@ typedef struct tr_adapters_args {
  * 16 significant bits or more (24 for fp32 out), out is rounded once.  Infinities and NaN go
  * where these formulas take them, and stay with their token.  Equal calls give equal bits.  x, a
  * and b are 16-byte aligned, their row pitches and strides multiples of 8 values (else
- * TR_ERR_UNSUPPORTED); tokens is below 2^31, k and n are below 2^30. */
+ * TR_ERR_UNSUPPORTED); tokens is below 2^31, k and n are below 2^30.
+ *
+ * The plan lies in device memory, so the call itself cannot check whose it is.  Given one
+ * that was made for another number of tokens or adapters (or memory in which none was made, as far as its first
+ * words tell), the kernels write nothing, and tr_device_status returns TR_ERR_UNSUPPORTED. */
 tr_status tr_adapters(const tr_adapters_args *args);
 
 /* Host-only planning: the variant tr_transpose_ex would run for these
@@ -560,7 +564,8 @@ tr_status tr_plan_ex(const tr_args *args, const tr_options *opts, tr_plan *plan)
 
 /* Reads and clears the device-side fault flag of the CURRENT device after
  * synchronizing it: TR_ERR_TIMEOUT if a bounded in-kernel wait ran out since
- * the last call, TR_OK otherwise (TR_ERR_CUDA if the read itself fails).
+ * the last call, else TR_ERR_UNSUPPORTED if tr_adapters met a plan of other sizes,
+ * TR_OK otherwise (TR_ERR_CUDA if the read itself fails).
  * tr_last_error() then names the kernels that raised it: transpose, matmul_fp8,
  * layernorm_backward, rmsnorm, rmsnorm_backward, adapters. */
 tr_status tr_device_status(void);

@@ -25,7 +25,7 @@
 
 namespace tr {
 
-// Set when a bounded in-kernel wait ran out; read and cleared by the host.
+// What went wrong (kFaultWait, kFaultPlan); read and cleared by the host.
 __device__ unsigned g_fault_flag_adapters = 0;
 
 namespace {
@@ -135,11 +135,15 @@ __global__ void __launch_bounds__(kPlanThreads) k_adapter_plan(const int32_t *in
 
 // --- the adapters ---------------------------------------------------------------------------
 
-// Tile k of a plan, of the large ones, the small ones or all; false where there is none.
+// Tile k of a plan, of the large ones, the small ones or all; false where there is none.  A plan of other sizes has none,
+// and is reported: its entries could be anything.
 enum Which { kAll, kLarge, kSmall };
 __device__ __forceinline__ bool plan_tile(const int32_t *plan, int64_t tokens, int64_t adapters, int which, int64_t k, int4 *tile) {
     const int4 head = *reinterpret_cast<const int4 *>(plan);
-    if (head.y != tokens || head.z != adapters) return false;  // not these tokens' plan
+    if (head.y != tokens || head.z != adapters) {
+        if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&g_fault_flag_adapters, kFaultPlan);
+        return false;
+    }
     const int64_t large = which == kSmall ? 0 : head.x, small = which == kLarge ? 0 : head.w;
     if (k >= large + small) return false;
     const int64_t place = k < large ? k : plan_tiles(tokens, adapters) - 1 - (k - large);
@@ -708,7 +712,7 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
             }
         }
     }
-    if (!ok) atomicExch(&g_fault_flag_adapters, 1u);
+    if (!ok) atomicOr(&g_fault_flag_adapters, kFaultWait);
     __syncwarp();
     ptx::tc_fence_before();
     __syncthreads();

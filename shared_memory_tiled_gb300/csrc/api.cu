@@ -482,6 +482,7 @@ tr_status tr_selftest_bounded_wait_in(const char *unit, int32_t arrive, int64_t 
 
 tr_status tr_device_status(void) {
     std::string units;
+    bool plan = false;
     for (const tr::WaitUnit &u : tr::kWaitUnits) {
         unsigned v = 0;
         const cudaError_t e = u.read(&v);
@@ -489,11 +490,16 @@ tr_status tr_device_status(void) {
             tr::set_error("reading the device fault flag failed", e);
             return TR_ERR_CUDA;
         }
-        if (v) units += std::string(" ") + u.name;
+        if (v & tr::kFaultWait) units += std::string(" ") + u.name;
+        plan = plan || (v & tr::kFaultPlan);
     }
-    if (units.empty()) return TR_OK;
-    tr::set_error(("a bounded wait ran out in:" + units).c_str(), cudaSuccess);
-    return TR_ERR_TIMEOUT;
+    if (!units.empty()) {
+        tr::set_error(("a bounded wait ran out in:" + units).c_str(), cudaSuccess);
+        return TR_ERR_TIMEOUT;
+    }
+    if (!plan) return TR_OK;
+    tr::set_error("adapters: a plan of other tokens or adapters than the call's, out is not written", cudaSuccess);
+    return TR_ERR_UNSUPPORTED;
 }
 
 tr_status tr_debug_bounds(tr_bounds_report *report) {

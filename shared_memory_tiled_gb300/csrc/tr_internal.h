@@ -74,6 +74,9 @@ cudaError_t launch_wait_selftest_rmsnorm(bool arrive, int64_t limit_ns, cudaStre
 cudaError_t launch_wait_selftest_rmsnorm_backward(bool arrive, int64_t limit_ns, cudaStream_t stream);
 cudaError_t launch_wait_selftest_adapters(bool arrive, int64_t limit_ns, cudaStream_t stream);
 
+// Bits of the device-side fault flags: a bounded wait ran out; a plan of other sizes (adapters).
+constexpr unsigned kFaultWait = 1, kFaultPlan = 2;
+
 // Device-side fault flag (bounded waits that ran out).  Reads and clears it;
 // the units of the linear layer keep one of their own each (read after it).
 cudaError_t read_and_clear_fault(unsigned *value);

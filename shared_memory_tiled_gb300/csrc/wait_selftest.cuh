@@ -5,6 +5,7 @@
 #pragma once
 
 #include "ptx.cuh"
+#include "tr_internal.h"
 
 namespace tr {
 
@@ -17,7 +18,7 @@ __device__ __forceinline__ void wait_selftest(unsigned *fault_flag, int arrive, 
     __syncwarp();
     if (arrive && threadIdx.x == 0) ptx::mbar_arrive(&bar);
     const bool ok = ptx::mbar_wait_bounded(&bar, 0, limit_ns);
-    if (__any_sync(0xffffffffu, !ok) && threadIdx.x == 0) atomicExch(fault_flag, 1u);
+    if (__any_sync(0xffffffffu, !ok) && threadIdx.x == 0) atomicOr(fault_flag, kFaultWait);
 }
 
 // A unit's self-test and the host's reader of its fault flag g_fault_flag_<unit>.
