@@ -135,11 +135,13 @@ __global__ void __launch_bounds__(kPlanThreads) k_adapter_plan(const int32_t *in
 
 // --- the adapters ---------------------------------------------------------------------------
 
+// Plan, scale and base are read past L1 (__ldcg): k_adapters beside k_adapters_few reads them without a wait of its own.
+
 // Tile k of a plan, of the large ones, the small ones or all; false where there is none.  A plan of other sizes has none,
 // and is reported: its entries could be anything.
 enum Which { kAll, kLarge, kSmall };
 __device__ __forceinline__ bool plan_tile(const int32_t *plan, int64_t tokens, int64_t adapters, int which, int64_t k, int4 *tile) {
-    const int4 head = *reinterpret_cast<const int4 *>(plan);
+    const int4 head = __ldcg(reinterpret_cast<const int4 *>(plan));
     if (head.y != tokens || head.z != adapters) {
         if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&g_fault_flag_adapters, kFaultPlan);
         return false;
@@ -147,7 +149,7 @@ __device__ __forceinline__ bool plan_tile(const int32_t *plan, int64_t tokens, i
     const int64_t large = which == kSmall ? 0 : head.x, small = which == kLarge ? 0 : head.w;
     if (k >= large + small) return false;
     const int64_t place = k < large ? k : plan_tiles(tokens, adapters) - 1 - (k - large);
-    *tile = *reinterpret_cast<const int4 *>(plan + plan_tiles_at() + 4 * place);
+    *tile = __ldcg(reinterpret_cast<const int4 *>(plan + plan_tiles_at() + 4 * place));
     return true;
 }
 
@@ -248,7 +250,7 @@ __device__ __forceinline__ void copy_rows(const Adapt &g, const int32_t *rows, i
                 for (int u = 0; u < U; ++u) {
                     const int64_t c = j + u * 32 * V;
                     v[u] = make_uint4(0u, 0u, 0u, 0u);
-                    if (g.base && c < j1 && TR_LOAD_OK(sb, p + c, 16)) v[u] = *reinterpret_cast<const uint4 *>(p + c);
+                    if (g.base && c < j1 && TR_LOAD_OK(sb, p + c, 16)) v[u] = __ldcg(reinterpret_cast<const uint4 *>(p + c));
                 }
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
@@ -262,7 +264,7 @@ __device__ __forceinline__ void copy_rows(const Adapt &g, const int32_t *rows, i
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     const int64_t c = j + u * 32;
-                    v[u] = g.base && c < j1 && TR_LOAD_OK(sb, p + c, int(sizeof(T))) ? p[c] : T(0.0f);
+                    v[u] = g.base && c < j1 && TR_LOAD_OK(sb, p + c, int(sizeof(T))) ? __ldcg(p + c) : T(0.0f);
                 }
 #pragma unroll
                 for (int u = 0; u < U; ++u)
@@ -333,8 +335,10 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
     if (g.split > 1) ptx::cluster_sync();  // the others' barriers are ready
     ptx::tc_fence_after();
     const uint32_t tmem = tmem_base;
-    // After the tensor memory is taken, as in the product.  The kernel beside this one lets it start when it has waited
-    // for what was before it, and writes other rows: that one is waited for at the end.
+    // After the tensor memory is taken, as in the product.  Beside k_adapters_few, the launch just before this one, this
+    // kernel starts when every block of that one has waited for what was before both (or has gone, having waited): that is
+    // complete, and its writes are in L2, where this kernel's reads go, by TMA or past L1.  The two write different rows
+    // and read none of one another's; that one is waited for at the end, so that whoever waits for this one has both.
     ptx::launch_dependents();
     if (!g.beside) ptx::wait_dependencies();
 
@@ -347,7 +351,7 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
     const int64_t first_tile = columns * rank / g.split, last_tile = columns * (rank + 1) / g.split;
     [[maybe_unused]] const dbg::Side sb = dbg::side(g.base, 1, g.tokens, g.n, g.ld_base, 0, sizeof(T));
     [[maybe_unused]] const dbg::Side so = dbg::side(g.out, 1, g.tokens, g.n, g.ld_out, 0, sizeof(T));
-    if (t < count) rows[t] = g.plan[plan_order_at(g.tokens, g.adapters) + at.y + t];
+    if (t < count) rows[t] = __ldcg(g.plan + plan_order_at(g.tokens, g.adapters) + at.y + t);
     __syncthreads();
     bool ok = true;
 
@@ -505,7 +509,7 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
             const int64_t own_base = own_token * g.ld_base, own_out = own_token * g.ld_out;
             auto old_value = [&](int r, int j) {
                 const T *p = static_cast<const T *>(g.base) + __shfl_sync(0xffffffffu, own_base, r) + (j < n ? j : n - 1);
-                return g.base && left > 0 && TR_LOAD_OK(sb, p, int(sizeof(T))) ? *p : T(0.0f);
+                return g.base && left > 0 && TR_LOAD_OK(sb, p, int(sizeof(T))) ? __ldcg(p) : T(0.0f);
             };
             [[maybe_unused]] T old[EDGE ? 32 : 1];
             if constexpr (EDGE) {
@@ -513,7 +517,7 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
                 for (int r = 0; r < 32; ++r) old[r] = old_value(r, j_first + group * kColumns + lane);
             }
             if (group < S::kHalves) {
-                const float scale = g.scale ? g.scale[at.x] : 1.0f;
+                const float scale = g.scale ? __ldcg(g.scale + at.x) : 1.0f;
                 constexpr int W = RP / S::kHalves;  // inner values to a thread
                 const int c0 = group * W;
                 float v[W];
@@ -786,7 +790,7 @@ constexpr int few_shares(int rp) { return rp <= 32 ? 1 : rp / 32; }
 template <int RP, typename T, bool EDGE>
 __global__ void __launch_bounds__(kFewThreads, 2) k_adapters_few(const Few g) {
     ptx::wait_dependencies();
-    ptx::launch_dependents();  // in this order: see k_adapters
+    ptx::launch_dependents();  // in this order, in every block: k_adapters beside this one counts on it
     constexpr int TERMS = sizeof(T) == 2 ? 2 : 3;
     constexpr int RC = RP == 16 ? 4 : 8, STEPS = RP / (4 * RC);  // values of a row of b to a lane and step
     constexpr int PITCH = RP + 8;                                // of the terms, in values
@@ -1104,7 +1108,7 @@ cudaError_t launch_adapters(const tr_adapters_args &p, const char **why) {
                                          : launch_few_rank<128>(few, f32, edge, small, stream);
         if (e != cudaSuccess || alone) return e;
         g.which = kLarge;
-        g.beside = 1;
+        g.beside = 1;  // nothing may be launched between the two
     }
     const int64_t large = g.beside ? plan_large_tiles(p.tokens, p.adapters) : tiles;
     CUtensorMap maps[8] = {};

@@ -10,7 +10,10 @@
 // until the previous grid has completed and its memory operations are
 // visible: nothing is read or written before that, so the result is the same
 // as with plain stream order whatever ran before (a kernel that never
-// signals simply lets the next one launch when it completes).  A dependent
+// signals simply lets the next one launch when it completes).  (One launch is
+// an exception: k_adapters beside k_adapters_few, which it directly follows.  That
+// one waits before it signals, so what was before both is complete when k_adapters
+// starts; it reads past L1 and waits at its end.)  A dependent
 // grid is launched only after all blocks of the previous one have started, so
 // waiting blocks never hold back a block they depend on.
 #pragma once
