@@ -171,32 +171,27 @@ struct Adapt {
 // for all 24, in products with b that are exact in 32 bits.  Cut off, because the terms then have the value's sign and none
 // is larger: with an infinite b each gives the infinity that the value gives (rounded, every second value is followed by a
 // term of the other sign, and the sum is NaN), and a value above bf16's largest does not become infinite.  For the same
-// reason a term is zero only where the value is (2^-133, bf16's least, in its place), and an infinity or NaN is every one.
-// (Rounded terms took 0.2 to 1 us less of a call: 8192 tokens rank 64 76.1 us, with these 76.5.)
+// reason no term of a value is zero: where nothing would be left for the next, it gets half (which is exact down to
+// 2^-125).  An infinity or NaN is every one of its terms.  The smallest comes first, as they are added: halves of a last bit
+// make that bit before they meet the rest.
+// Rounded terms take as long (8192 tokens, rank 64, 76.1 us, these 76.3; 64 tokens of 48 adapters 15.3 either way); three
+// for bf16 outputs, 24 bits where 8 are kept, would cost one token rank 16 7.0 -> 7.8 us and 8192 rank 128 85 -> 118.
 template <int TERMS>
 __device__ __forceinline__ void terms_of(float a, float b, uint32_t (&word)[TERMS]) {
     float left[2] = {a, b};
-    const uint32_t sign[2] = {__float_as_uint(a) & 0x80000000u, __float_as_uint(b) & 0x80000000u};
-    const uint32_t least[2] = {a != 0.0f ? 0x00010000u : 0u, b != 0.0f ? 0x00010000u : 0u};
-    const bool finite[2] = {fabsf(a) < INFINITY, fabsf(b) < INFINITY};
 #pragma unroll
-    for (int term = 0; term < TERMS; ++term) {
-        uint32_t top[2];
-        if (term + 1 < TERMS) {
+    for (int term = 0; term + 1 < TERMS; ++term) {
+        float cut[2];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                top[i] = __float_as_uint(left[i]) & 0xffff0000u;
-                left[i] = finite[i] ? left[i] - __uint_as_float(top[i]) : left[i];
-            }
-        } else {
-            const float2 rounded = __bfloat1622float2(__floats2bfloat162_rn(left[0], left[1]));
-            top[0] = __float_as_uint(rounded.x);
-            top[1] = __float_as_uint(rounded.y);
+        for (int i = 0; i < 2; ++i) {
+            cut[i] = __uint_as_float(__float_as_uint(left[i]) & 0xffff0000u);
+            if (cut[i] == left[i]) cut[i] = left[i] = 0.5f * left[i];
+            else left[i] -= cut[i];
         }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) top[i] = umax(top[i] & 0x7fffffffu, least[i]) | sign[i];
-        word[term] = __byte_perm(top[0], top[1], 0x7632);
+        word[TERMS - 1 - term] = __byte_perm(__float_as_uint(cut[0]), __float_as_uint(cut[1]), 0x7632);
     }
+    const __nv_bfloat162 two = __floats2bfloat162_rn(left[0], left[1]);
+    word[0] = *reinterpret_cast<const uint32_t *>(&two);
 }
 
 constexpr int kGroups = 3;              // of four warps that take sums out of tensor memory, each with its own
@@ -607,7 +602,8 @@ k_adapters(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
                     uint32_t word[4][TERMS];
 #pragma unroll
                     for (int k = 0; k < 8; k += 2)
-                        terms_of<TERMS>(c0 + c + k < g.rank ? v[c + k] * scale : 0.0f, c0 + c + k + 1 < g.rank ? v[c + k + 1] * scale : 0.0f, word[k / 2]);
+                        terms_of<TERMS>(c0 + c + k < g.rank ? __fmul_rn(v[c + k], scale) : 0.0f,  // rounded, whatever is taken from it
+                                        c0 + c + k + 1 < g.rank ? __fmul_rn(v[c + k + 1], scale) : 0.0f, word[k / 2]);
 #pragma unroll
                     for (int term = 0; term < TERMS; ++term) {
                         const int col = term * RP + c0 + c;
@@ -927,7 +923,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) k_adapters_few(const Few g) {
                 for (int peer = 0; peer < 8; ++peer)
                     if (peer < g.split) v += f[peer];
                 uint32_t word[TERMS];
-                terms_of<TERMS>(r < g.rank ? v * scale : 0.0f, 0.0f, word);
+                terms_of<TERMS>(r < g.rank ? __fmul_rn(v, scale) : 0.0f, 0.0f, word);
 #pragma unroll
                 for (int term = 0; term < TERMS; ++term) terms[term][m][r] = __ushort_as_bfloat16(uint16_t(word[term]));
             }
