@@ -525,7 +525,8 @@ typedef struct tr_adapters_args {
  *     v[r] = scale[g] * sum over l of x[i][l] * a[g][r][l]
  *     out[i][j] = base[i][j] + sum over r of v[r] * b[g][j][r]
  *
- * and out[i] = base[i] for a token without one.  Sums are held in 32 bits, v in
+ * and out[i] = base[i] for a token without one.  Sums are held in 32 bits (the tensor
+ * cores', which may cut off below the last bit where others round), v in
  * 16 significant bits or more (24 for fp32 out), out is rounded once.  Infinities and NaN go
  * where these formulas take them, and stay with their token.  Equal calls give equal bits.  x, a
  * and b are 16-byte aligned, their row pitches and strides multiples of 8 values (else

@@ -7,10 +7,12 @@
 // all of them need, go through distributed shared memory, never through memory.  They are summed in 32 bits and go into the
 // second product as two bf16 terms, 16 significant bits against the output's 8 (three terms for fp32 outputs, 24 bits).
 //   many tokens   k_adapters, tensor cores fed by TMA: 8192 tokens of 8 adapters, 8192 x 8192 rank 16, 64 and 128 70, 76
-//                 and 85 us, 5.8, 5.5 and 5.1 TB/s (60, 62 and 64 at the copy rate); fp32 outputs, rank 64, 144 (102)
+//                 and 85 us, 5.8, 5.5 and 5.1 TB/s (60, 62 and 64 at the copy rate); fp32 outputs, rank 64, 145 (102)
 //   few tokens    k_adapters_few, matrix instructions of a warp straight from memory: bound by latency, three reads that
-//                 wait for one another (plan, x and a, b); one token rank 16 and 64 7.0 and 12.9 us, 64 of 48 adapters
+//                 wait for one another (plan, x and a, b); one token rank 16 and 64 7.2 and 13.0 us, 64 of 48 adapters
 //                 15.5 and 36.3 (4.2 and 15.3 at the copy rate)
+// How wide the launches are goes by the adapters that are registered, which the host knows, not by those in use: 8192
+// tokens of 8 prompts, rank 16, take 73 us with 8 adapters registered, 101 with 64 and 100 with 2000.
 // Two launches a call at the most; nothing depends on the order in which blocks run.
 #include <type_traits>
 
@@ -171,8 +173,8 @@ struct Adapt {
 // for all 24, in products with b that are exact in 32 bits.  Cut off, because the terms then have the value's sign and none
 // is larger: with an infinite b each gives the infinity that the value gives (rounded, every second value is followed by a
 // term of the other sign, and the sum is NaN), and a value above bf16's largest does not become infinite.  For the same
-// reason no term of a value is zero: where nothing would be left for the next, it gets half (which is exact down to
-// 2^-125).  An infinity or NaN is every one of its terms.  The smallest comes first, as they are added: halves of a last bit
+// reason no term of a value is zero: where nothing would be left for the next, it gets half (exact while that is not
+// subnormal).  An infinity or NaN is every one of its terms.  The smallest comes first, as they are added: halves of a last bit
 // make that bit before they meet the rest.
 // Rounded terms take as long (8192 tokens, rank 64, 76.1 us, these 76.3; 64 tokens of 48 adapters 15.3 either way); three
 // for bf16 outputs, 24 bits where 8 are kept, would cost one token rank 16 7.0 -> 7.8 us and 8192 rank 128 85 -> 118.
@@ -743,8 +745,15 @@ struct Few {
 };
 
 // Up to kFewTokens tokens (kFewTokensNarrow with ranks up to 16) this kernel works alone, up to kBothTokens on the small
-// tiles.  64 tokens, 8192 x 8192, alone and both: rank 16 15.4 and 16.2 us with 48 adapters, 22.3 and 20.5 with one, and a
-// launch and six tensor maps less for the host; rank 32 23.1 and 23.9, 28.5 and 21.8.
+// tiles.  What decides, tokens to an adapter, only the device knows; each limit buys one kind of batch with another.
+// 8192 x 8192 bf16, one set of adapters again and again, us, alone and both:
+//   rank 16   64 tokens of 48 adapters 13.2 and 13.8, of one 22.2 and 19.2; 128 of 48 13.3 and 14.6, of one 42 and 21; alone
+//             is a launch and six tensor maps less for the host
+//   rank 32   48 tokens of 48 adapters 17.0 and 17.7, of one 22.1 and 20.3; 64 of one 28.5 and 20.5
+// Both, and k_adapters alone (a next token then takes a tile of 128):
+//   rank 16   8 prompts 23.6 and 22.0 (1024 tokens), 35 and 34 (2048), 75 and 74 (8192); with 48 next tokens 35 and 48,
+//             57 and 54, 121 and 102
+//   rank 64   8 prompts 29.6 and 27.3, 43 and 40, 82 and 80; with 48 next tokens 52 and 56, 72 and 65, 153 and 114
 constexpr int64_t kFewTokens = 32, kFewTokensNarrow = 64, kBothTokens = 2048;
 constexpr int kFewThreads = 256, kFewWarps = kFewThreads / 32;
 
