@@ -111,7 +111,10 @@ def train(steps: int = 60, tokens: int = 4096, inner: int = 1024, outer: int = 7
     g = torch.Generator(device="cuda").manual_seed(3)
     losses = []
     for _ in range(steps):
-        x = torch.randn(tokens, inner, device="cuda", generator=g).add_(0.5).bfloat16()
+        x = torch.randn(tokens, inner, device="cuda", generator=g)
+        if norm == "layer":  # which takes the mean out; behind the other one it is a direction along which steps of `rate` diverge
+            x.add_(0.5)
+        x = x.bfloat16()
         want = _normed(x, norm) @ teacher.w.t()
         out, kept = layer.forward(x)
         off = out.float() - want
